@@ -314,6 +314,124 @@ MOE_API int moe_expert_stages(const moe_config *cfg, const moe_weights *w, const
 MOE_API int moe_decode_timeline(const moe_config *cfg, int T, void *ws, size_t ws_bytes, void *stream,
                                 unsigned long long *host_stamps, int max_ctas, int *n_ctas);
 
+/* ------------------------------------------------------------------------
+ * Block-scaled operators: rows whose elements are narrow codes with one scale
+ * per block of consecutive elements, made by a norm or a quantiser and
+ * multiplied on the tensor cores in that form (both operands narrow).  They
+ * stand beside the layer above, which keeps its activations in 16 bits: the
+ * residual add and norm in front of it, its expert products at the tensor
+ * cores' 4-bit rate, and projections of any other kind.
+ *
+ * Formats (enum moe_scaled_format); v' is the value that is stored for v:
+ *   NVFP4  v' = e2m1(q) * e4m3(s) * g, s per 16 elements, g fp32 per row
+ *          (activations) or per matrix (weights).  g is given, or for a row
+ *          max(amax * (1/2688), 2^-110).  s = e4m3(amax_b * (1/g) * (1/6)),
+ *          q = e2m1(v * ((1/g) / s)); q = 0 where s = 0.
+ *   MXFP8  v' = e4m3(q) * 2^e, e per 32 elements: the smallest with
+ *          amax_b <= 448 * 2^e, -127 <= e <= 127, stored as e + 127 (E8M0).
+ *   MXFP4  v' = e2m1(q) * 2^e, e per 32 elements, amax_b <= 6 * 2^e.
+ *   Roundings are to nearest, ties to even, saturating.  A block with a
+ *   non-finite element gets the NaN scale (0x7F, E8M0 0xFF): every output
+ *   computed from that row is then NaN.  NVFP4 scales are unsigned here: the
+ *   sign bit of a scale byte must be clear.
+ * Codes: rows dense; 4-bit codes two a byte, the lower nibble first.
+ * Scales: in tiles of 128 rows x 4 blocks, 512 bytes, the order in which the
+ *   tensor core takes them: block b of row r is byte
+ *     ((r / 128) * ct + b / 4) * 512 + (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4
+ *   with ct = ceil(blocks per row / 4).  Bytes of blocks and rows that do not
+ *   exist may hold anything.
+ * Groups: rows of a product belong to groups (experts), in order; group g
+ *   multiplies matrix g of a stack.
+ *   Activations: codes, factors and outputs of R rows are dense; group g's
+ *     rows are offsets[g] .. offsets[g + 1] - 1 (the last group's end at
+ *     R - 1), and its scale rows start at row tile offsets[g] / 128 + g, so
+ *     that they take (R / 128 + G) row tiles in all.
+ *   Weights: matrix g's scale rows start at row tile g * ceil(N / 128).
+ * Pointers as above (16-byte aligned); MXFP4 weight codes 32-byte aligned.
+ * ws is any workspace of at least MOE_SCALED_WS_BYTES bytes whose first 512
+ * bytes were zero before its first use; it holds the status word
+ * (moe_get_device_status) and may be a workspace of moe_workspace_size too. */
+enum moe_scaled_format {
+    MOE_SCALED_NVFP4 = 1,
+    MOE_SCALED_MXFP8 = 2,   /* activations; their products take MXFP4 weights */
+    MOE_SCALED_MXFP4 = 3    /* weights */
+};
+#define MOE_SCALED_WS_BYTES 512
+
+/* R block-scaled rows (or where to write them). */
+typedef struct moe_scaled_rows {
+    uint8_t *codes;    /* [R, n] (MXFP8) or [R, n / 2] */
+    uint8_t *scales;   /* (R / 128 + G) * ct scale tiles */
+    float *row_scale;  /* NVFP4: fp32 [R], or NULL (all ones); other formats: NULL */
+} moe_scaled_rows;
+
+/* A stack of G block-scaled weight matrices [N, K]. */
+typedef struct moe_scaled_mat {
+    const uint8_t *codes;   /* [G, N, K / 2] */
+    const uint8_t *scales;  /* G * ceil(N / 128) * ct scale tiles */
+    const float *alpha;     /* fp32 [G] factor of each matrix's products, or NULL (ones) */
+} moe_scaled_mat;
+
+/* Residual add and root-mean-square norm of T rows of n elements:
+ *   s = bf16(x + residual)           (s = x without a residual)
+ *   y = s * rsqrt(mean(s^2) + eps) * (weight_offset + weight)   in fp32
+ *   residual   bf16 [T, n] or NULL
+ *   weight     bf16 [n], or NULL for none
+ *   sum_out    bf16 [T, n] s, or NULL; may be x or residual itself
+ *   y_out      bf16 [T, n] y rounded once, or NULL
+ *   format, q  y as MOE_SCALED_NVFP4 (q->row_scale required) or
+ *              MOE_SCALED_MXFP8 rows, one group; format 0 and q NULL for none.
+ * The codes are rounded from the fp32 y, not from y_out.  n: a multiple of the
+ * format's block (8 without one), at most 16384. */
+MOE_API int moe_add_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float weight_offset,
+                            float eps, int T, int n, uint16_t *sum_out, uint16_t *y_out, int format,
+                            const moe_scaled_rows *q, void *stream);
+
+/* Quantises T rows of n elements of x (bf16, or fp32 with x_f32 = 1), T / groups
+ * rows to a group, each group's scale rows from a new row tile (so a stack of
+ * weight matrices is quantised by one call with groups = G).
+ *   gscale  NVFP4: fp32 [groups] given factor g of each group's rows
+ *           (q->row_scale is not written), or NULL: a factor per row, written to
+ *           q->row_scale.  Other formats: NULL.
+ * n: a multiple of the block; at most 16384 for NVFP4 without gscale. */
+MOE_API int moe_quantize(int format, const void *x, int x_f32, int T, int n, int groups, const float *gscale,
+                         const moe_scaled_rows *q, void *stream);
+
+/* Quantises T rows of bf16 x into the expert-sorted rows of their k picks (ids,
+ * inv_perm, offsets as from moe_route and moe_permute) and, with has_shared, into
+ * row T*k + t of the shared expert's group E: the rows of a grouped product over
+ * E + has_shared groups.  format: NVFP4 (row factors) or MXFP8.  Picks that the
+ * arguments place outside the rows are reported (MOE_ERR_DEVICE) and not written. */
+MOE_API int moe_quantize_routed(int format, const uint16_t *x, int T, int n, int k, int E, int has_shared,
+                                const int32_t *ids, const int32_t *inv_perm, const int32_t *offsets,
+                                const moe_scaled_rows *q, void *ws, size_t ws_bytes, void *stream);
+
+/* Scales as checkpoints store them (bytes [G, N, n / block], row-major) to scale
+ * tiles of a weight stack.  Run once after loading. */
+MOE_API int moe_tile_scales(int format, const uint8_t *src, int G, int N, int n, uint8_t *dst, void *stream);
+
+/* Grouped product: y[r, :] = row_scale[r] alpha[g] (a[r, :] . w_g^T), bf16 or
+ * (y_f32) fp32 [R, N], accumulated in fp32.
+ *   format   of a: MOE_SCALED_NVFP4 (w NVFP4) or MOE_SCALED_MXFP8 (w MXFP4)
+ *   offsets  int32 [G] first row of each group, increasing from 0, or NULL
+ *            when G == 1 (moe_permute's offsets serve, also with a shared
+ *            expert as group E).  Entries outside [0, R] or decreasing are
+ *            reported (MOE_ERR_DEVICE) and clamped.
+ * K: a multiple of 64 (NVFP4) or 128 (MXFP8), at most 65536; N: a multiple of 8;
+ * G <= 1024.  R == 0 enqueues nothing. */
+MOE_API int moe_scaled_gemm(int format, const moe_scaled_rows *a, const moe_scaled_mat *w, int R, int N, int K, int G,
+                            const int32_t *offsets, void *y, int y_f32, void *ws, size_t ws_bytes, void *stream);
+
+/* Two grouped products and SwiGLU: h = silu(a . gate_g^T) * (a . up_g^T) with both
+ * products' factors, quantised to the rows' own format for the next product.
+ *   h_scale  NVFP4: fp32 [G] calibrated factor g of h (fold it into the next
+ *            matrices' alpha); MXFP8: NULL
+ *   h        [R, inter] rows, same groups; h->row_scale must be NULL
+ * inter: a multiple of 64 (NVFP4) or 128 (MXFP8). */
+MOE_API int moe_scaled_swiglu(int format, const moe_scaled_rows *a, const moe_scaled_mat *gate, const moe_scaled_mat *up,
+                              int R, int inter, int K, int G, const int32_t *offsets, const float *h_scale,
+                              const moe_scaled_rows *h, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

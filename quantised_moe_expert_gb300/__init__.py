@@ -33,10 +33,17 @@ MOE_PATH_PREFILL = 2
 MOE_FORMAT_AFFINE = 0
 MOE_FORMAT_NVFP4 = 1
 
+MOE_SCALED_NVFP4 = 1
+MOE_SCALED_MXFP8 = 2
+MOE_SCALED_MXFP4 = 3
+MOE_SCALED_WS_BYTES = 512
+
 EXPORTED = ("moe_status_string", "moe_check_config", "moe_workspace_size", "moe_route", "moe_permute",
             "moe_expert_ffn", "moe_combine", "moe_forward", "moe_get_device_status", "moe_pack_down",
             "moe_expert_stages",
-            "moe_decode_timeline", "moe_forward_decode_static")
+            "moe_decode_timeline", "moe_forward_decode_static",
+            "moe_add_rmsnorm", "moe_quantize", "moe_quantize_routed", "moe_tile_scales", "moe_scaled_gemm",
+            "moe_scaled_swiglu")
 
 
 class MoeError(RuntimeError):
@@ -62,6 +69,14 @@ class moe_weights(ctypes.Structure):
                 ("s_down_packed", ctypes.c_void_p)]
 
 
+class moe_scaled_rows(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "row_scale")]
+
+
+class moe_scaled_mat(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "alpha")]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -77,6 +92,8 @@ def library_path() -> str:
 def load(build: bool = True):
     """Load libmoe.so (building it with nvcc first if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -104,6 +121,13 @@ def load(build: bool = True):
         lib.moe_decode_timeline.argtypes = [P(moe_config), _I, _VP, _SZ, _VP, _VP, _I, P(ctypes.c_int)]
         lib.moe_forward_decode_static.argtypes = [P(moe_config), P(moe_weights), _VP, _I, _VP, _VP, _VP, _VP, _VP,
                                                   _VP, _VP]
+        R, M, F = P(moe_scaled_rows), P(moe_scaled_mat), ctypes.c_float
+        lib.moe_add_rmsnorm.argtypes = [_VP, _VP, _VP, F, F, _I, _I, _VP, _VP, _I, R, _VP]
+        lib.moe_quantize.argtypes = [_I, _VP, _I, _I, _I, _I, _VP, R, _VP]
+        lib.moe_quantize_routed.argtypes = [_I, _VP, _I, _I, _I, _I, _I, _VP, _VP, _VP, R, _VP, _SZ, _VP]
+        lib.moe_tile_scales.argtypes = [_I, _VP, _I, _I, _I, _VP, _VP]
+        lib.moe_scaled_gemm.argtypes = [_I, R, M, _I, _I, _I, _I, _VP, _VP, _I, _VP, _SZ, _VP]
+        lib.moe_scaled_swiglu.argtypes = [_I, R, M, M, _I, _I, _I, _I, _VP, _VP, R, _VP, _SZ, _VP]
         for name in EXPORTED:
             if name != "moe_status_string":
                 getattr(lib, name).restype = ctypes.c_int
@@ -123,7 +147,8 @@ def _ptr(t: Optional[torch.Tensor]):
 
 def _stream(stream) -> ctypes.c_void_p:
     if stream is None:
-        stream = torch.cuda.current_stream()
+        # the current stream's handle, without the stream object that torch.cuda.current_stream() makes
+        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -298,7 +323,70 @@ def moe_decode_timeline(cfg, T, ws, stream=None, max_ctas: int = 256) -> np.ndar
     return buf[:min(n.value, max_ctas)]
 
 
+def moe_add_rmsnorm(x, residual, weight, weight_offset, eps, T, n, sum_out, y_out, fmt, q, stream=None):
+    rc = load().moe_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), weight_offset, eps, T, n, _ptr(sum_out),
+                                _ptr(y_out), fmt, q, _stream(stream))
+    _check("moe_add_rmsnorm", rc)
+
+
+def moe_quantize(fmt, x, T, n, groups, gscale, q, stream=None):
+    """x: a bf16 (or int16 bits) or float32 tensor."""
+    rc = load().moe_quantize(fmt, _ptr(x), int(x.dtype == torch.float32), T, n, groups, _ptr(gscale), q, _stream(stream))
+    _check("moe_quantize", rc)
+
+
+def moe_quantize_routed(fmt, x, T, n, k, E, has_shared, ids, inv_perm, offsets, q, ws, stream=None):
+    rc = load().moe_quantize_routed(fmt, _ptr(x), T, n, k, E, has_shared, _ptr(ids), _ptr(inv_perm), _ptr(offsets), q,
+                                    _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
+    _check("moe_quantize_routed", rc)
+
+
+def moe_tile_scales(fmt, src, G, N, n, dst, stream=None):
+    _check("moe_tile_scales", load().moe_tile_scales(fmt, _ptr(src), G, N, n, _ptr(dst), _stream(stream)))
+
+
+def moe_scaled_gemm(fmt, a, w, R, N, K, G, offsets, y, ws, stream=None):
+    """y: a bf16 (or int16 bits) or float32 tensor [R, N]."""
+    rc = load().moe_scaled_gemm(fmt, a, w, R, N, K, G, _ptr(offsets), _ptr(y), int(y.dtype == torch.float32), _ptr(ws),
+                                ws.numel() * ws.element_size(), _stream(stream))
+    _check("moe_scaled_gemm", rc)
+
+
+def moe_scaled_swiglu(fmt, a, gate, up, R, inter, K, G, offsets, h_scale, h, ws, stream=None):
+    rc = load().moe_scaled_swiglu(fmt, a, gate, up, R, inter, K, G, _ptr(offsets), _ptr(h_scale), h, _ptr(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream))
+    _check("moe_scaled_swiglu", rc)
+
+
 # ---------------------------------------------------------------- conveniences
+
+def scaled_rows(codes, scales, row_scale=None) -> moe_scaled_rows:
+    """The C description of block-scaled rows held in these tensors (which it keeps alive)."""
+    r = moe_scaled_rows(_ptr(codes), _ptr(scales), _ptr(row_scale))
+    r.tensors = (codes, scales, row_scale)
+    return r
+
+
+def scaled_mat(codes, scales, alpha=None) -> moe_scaled_mat:
+    """The C description of a stack of block-scaled matrices held in these tensors (which it keeps alive)."""
+    m = moe_scaled_mat(_ptr(codes), _ptr(scales), _ptr(alpha))
+    m.tensors = (codes, scales, alpha)
+    return m
+
+
+def scaled_col_tiles(fmt: int, n: int) -> int:
+    """Scale tiles across a row of n elements."""
+    return -(-(n // (16 if fmt == MOE_SCALED_NVFP4 else 32)) // 4)
+
+
+def scaled_rows_empty(fmt: int, R: int, n: int, groups: int = 1, row_scale: bool = True, device="cuda") -> moe_scaled_rows:
+    """Room for R block-scaled rows of n elements in `groups` groups (row_scale: NVFP4 rows with their own factors)."""
+    codes = torch.empty((R, n if fmt == MOE_SCALED_MXFP8 else n // 2), dtype=torch.uint8, device=device)
+    scales = torch.zeros(((R // 128 + groups) * scaled_col_tiles(fmt, n) * 512,), dtype=torch.uint8, device=device)
+    rs = torch.empty((R,), device=device) if row_scale and fmt == MOE_SCALED_NVFP4 else None
+    return scaled_rows(codes, scales, rs)
+
+
 
 def workspace(cfg: moe_config, T: int, device="cuda") -> torch.Tensor:
     """A zero-filled device workspace of moe_workspace_size bytes (uint8, 256-byte aligned by the allocator)."""

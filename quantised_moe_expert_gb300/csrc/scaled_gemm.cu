@@ -1,0 +1,532 @@
+// Grouped products of block-scaled rows on the block-scaled tensor-core kinds.
+//
+//   acc[r, n] = sum_b sa[r, b] sw[g, n, b] sum_{j in block b} a[r, j] w[g, n, j]      (fp32, in tensor memory)
+//   y[r, n]   = row_scale[r] alpha[g] acc[r, n]
+//   h[r, n]   = silu(gate) up of two such products, quantised in the epilogue
+//
+// Rows are sorted by group (expert): group g owns rows [offsets[g], offsets[g + 1]).  Operands:
+//   NVFP4 x NVFP4   kind::mxf4nvf4, 64 elements an instruction, an E4M3 scale per 16
+//   MXFP8 x MXFP4   kind::mxf8f6f4, 32 elements an instruction, an E8M0 scale per 32; TMA widens the
+//                   4-bit codes to the byte containers that kind takes
+// Either way a K step of a tile is rows of 128 bytes (256 or 128 elements) in the 128-byte swizzle.  Tokens
+// are the M = 128 operand whatever their number (a step's cost is its weight bytes, not its rows: only
+// the rows present are copied), weights the N = BN operand, so that a thread of the epilogue holds
+// consecutive outputs of one row: whole blocks of h for its scale, whole sectors of y.
+//
+// One CTA per SM walks over the tiles: warp 0 copies codes (TMA), warp 2 copies scale tiles (bulk), warp 1
+// moves a step's scales from shared into tensor memory (tcgen05.cp) and issues its MMAs, warps 4-7 read
+// the accumulators and write.  Every stage has its own scale columns, so a stage's barrier also guards
+// them.
+#include "scaled.cuh"
+#include "tc_ptx.cuh"
+#include "tma_host.cuh"
+
+namespace qmoe {
+namespace {
+
+using namespace tc;
+
+constexpr int kThreads = 256;
+constexpr int kMaxGroups = 1024;
+constexpr int kStepBytes = 128;                    // bytes of a K step in a row of codes (as in shared memory)
+
+template <int FMT, bool DUAL, int BN>
+struct Plan {
+    static constexpr bool kNv = FMT == MOE_SCALED_NVFP4;
+    static constexpr int kStepK = kNv ? 256 : 128;           // elements of a K step
+    static constexpr int kTilesK = kNv ? 4 : 1;              // scale column tiles of a K step
+    static constexpr int kOutN = DUAL ? BN / 2 : BN;         // output columns of a tile
+    static constexpr int kMmaN = DUAL && BN == 128 ? 64 : BN;   // N of one instruction
+    static constexpr int kChunks = DUAL || BN > 128 ? 2 : 1; // weight scale row tiles of a tile
+    static constexpr int kABytes = 128 * kStepBytes, kBBytes = BN * kStepBytes;
+    static constexpr int kBTxBytes = kNv ? kBBytes : kBBytes / 2;   // a widened copy counts the codes, not the padding
+    static constexpr int kSfaBytes = kTilesK * kScaleTile, kSfbBytes = kChunks * kTilesK * kScaleTile;
+    static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
+    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? (DUAL ? 5 : 6) : 7;
+    static constexpr int kAccs = BN == 256 ? 1 : 2;          // accumulator buffers
+    static constexpr int kSfCols = 4 * kTilesK * (1 + kChunks);   // tensor-memory columns of a stage's scales
+    static constexpr int kSmem = kStages * kStageBytes + 1024;
+    static_assert(kAccs * BN + kStages * kSfCols <= 512, "tensor memory");
+};
+
+struct Maps {
+    CUtensorMap a128, a32, w[2];
+};
+
+struct Shared {
+    uint64_t full[8], empty[8], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort;
+    int warp_sum[8];
+    int first[kMaxGroups + 1];                               // row tiles of the groups before g
+};
+
+struct Tile {
+    int g, row0, rows, srow_tile, nt;                        // rows [row0, row0 + rows), their scale row tile
+};
+
+__device__ __forceinline__ int group_start(const ScaledGemmArgs &a, int g)
+{
+    if (g >= a.G) return a.R;
+    const int o = a.offsets ? __ldg(a.offsets + g) : 0;
+    return min(max(o, 0), a.R);
+}
+
+__device__ __forceinline__ Tile tile_at(const ScaledGemmArgs &a, const Shared &sh, int tile, int n_tiles)
+{
+    const int mt = tile / n_tiles;
+    int lo = 0, hi = a.G;                                    // first[lo] <= mt < first[hi]
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.first[mid] <= mt) lo = mid;
+        else hi = mid;
+    }
+    const int start = group_start(a, lo), end = max(group_start(a, lo + 1), start), m = mt - sh.first[lo];
+    Tile t;
+    t.g = lo;
+    t.row0 = start + m * kScaleRows;
+    t.rows = min(end - t.row0, kScaleRows);
+    t.srow_tile = group_row_tile(start, lo) + m;
+    t.nt = tile - mt * n_tiles;
+    return t;
+}
+
+// Scale tiles in shared memory as tcgen05.cp takes them: 8 rows x 16 bytes cores, 128 bytes apart, no swizzle.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t addr)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+}
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds: scale ids [4,6) (B) and [29,31) (A), A format [7,10),
+// B format [10,13), N >> 3 [17,23), scale format [23] (0 E4M3, 1 E8M0), M >> 4 [24,29).
+template <int FMT>
+__host__ __device__ constexpr uint32_t idesc_scaled(uint32_t n, uint32_t sf_id)
+{
+    return (sf_id << 4) | ((FMT == MOE_SCALED_NVFP4 ? 1u : 0u) << 7) | ((FMT == MOE_SCALED_NVFP4 ? 1u : 5u) << 10) |
+           ((n >> 3) << 17) | ((FMT == MOE_SCALED_NVFP4 ? 0u : 1u) << 23) | ((128u >> 4) << 24) | (sf_id << 29);
+}
+template <int FMT>
+__device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                           uint32_t sfb, uint32_t accumulate)
+{
+    if (FMT == MOE_SCALED_NVFP4)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            : "memory");
+}
+
+__device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+// 32 fp32 of one row to y (bf16 or fp32): columns [col, col + 32) below N, N a multiple of 8.
+__device__ __forceinline__ void store_y32(const ScaledGemmArgs &a, size_t row, int col, const float (&v)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (col + 8 * i >= a.N) return;
+        if (a.y_f32) {
+            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.y) + row * a.N + col + 8 * i);
+            p[0] = make_float4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
+            p[1] = make_float4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+                w[k] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + row * a.N + col + 8 * i) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+template <int FMT, bool DUAL, int BN>
+__global__ void __launch_bounds__(kThreads, 1)
+scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_constant__ Maps maps)
+{
+    using P = Plan<FMT, DUAL, BN>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared sh;
+    uint8_t *smem = align_smem_1024(smem_raw);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_tiles = (a.N + P::kOutN - 1) / P::kOutN, n_steps = (a.K + P::kStepK - 1) / P::kStepK;
+    const int ct = scaled_col_tiles(FMT, a.K);
+    const int w_row_tiles = (a.N + kScaleRows - 1) / kScaleRows;      // scale row tiles of a matrix
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < P::kStages; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 2);                      // codes and scales
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        for (int i = 0; i < P::kAccs; ++i) {
+            mbar_init(smem_u32(&sh.acc_full[i]), 1);
+            mbar_init(smem_u32(&sh.acc_empty[i]), 4);
+        }
+        mbar_init(smem_u32(&sh.drain), 1);
+        sh.abort = 0;
+        fence_mbar_init();
+    }
+    if (warp == 3) {
+        tmem_alloc(smem_u32(&sh.tmem), 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    // row tiles before each group: every thread takes a run of groups
+    {
+        const int per = (a.G + kThreads - 1) / kThreads, g0 = min((int)threadIdx.x * per, a.G), g1 = min(g0 + per, a.G);
+        int n = 0;
+        for (int g = g0; g < g1; ++g) {
+            const int s = group_start(a, g), e = group_start(a, g + 1);
+            if (e < s || (a.offsets && __ldg(a.offsets + g) != s)) record_status(a.status, MOE_ERR_DEVICE);
+            n += (max(e - s, 0) + kScaleRows - 1) / kScaleRows;
+        }
+        int incl = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) sh.warp_sum[warp] = incl;
+        __syncthreads();
+        int base = incl - n;
+        for (int w = 0; w < warp; ++w) base += sh.warp_sum[w];
+        for (int g = g0; g < g1; ++g) {
+            sh.first[g] = base;
+            const int s = group_start(a, g), e = group_start(a, g + 1);
+            base += (max(e - s, 0) + kScaleRows - 1) / kScaleRows;
+        }
+        if (g1 == a.G) sh.first[a.G] = base;                         // the threads past the last group agree
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int total = sh.first[a.G] * n_tiles;
+    volatile int *abort = &sh.abort;
+    const uint32_t smem0 = smem_u32(smem);
+    auto fail = [&]() {
+        record_status(a.status, MOE_ERR_TIMEOUT);
+        *abort = 1;
+    };
+
+    if ((warp == 0 || warp == 2) && lane == 0) {
+        // ---- copies: warp 0 the codes, warp 2 the scales
+        int st = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+            const Tile t = tile_at(a, sh, tile, n_tiles);
+            const int n0 = t.nt * P::kOutN;
+            const bool second = P::kChunks == 2 && (DUAL || n0 / kScaleRows + 1 < w_row_tiles);
+            for (int ks = 0; ks < n_steps; ++ks) {
+                if (!mbar_wait(smem_u32(&sh.empty[st]), ph ^ 1, a.wait_limit, abort)) {
+                    fail();
+                    ok = false;
+                    break;
+                }
+                const uint32_t base = smem0 + st * P::kStageBytes, bar = smem_u32(&sh.full[st]);
+                if (warp == 0) {
+                    const int boxes = t.rows > 96 ? 4 : (t.rows + 31) / 32;
+                    mbar_arrive_expect_tx(bar, boxes * 32 * kStepBytes + P::kBTxBytes);
+                    // x in the map's elements: bytes, or 4-bit codes for the widened weights
+                    const int xa = ks * kStepBytes, xw = P::kNv ? ks * kStepBytes : ks * P::kStepK;
+                    if (DUAL) {
+                        tma_load_2d(base + P::kABytes, &maps.w[0], xw, t.g * a.N + n0, bar);
+                        tma_load_2d(base + P::kABytes + P::kBBytes / 2, &maps.w[1], xw, t.g * a.N + n0, bar);
+                    } else {
+                        tma_load_2d(base + P::kABytes, &maps.w[0], xw, t.g * a.N + n0, bar);
+                    }
+                    if (boxes == 4)
+                        tma_load_2d(base, &maps.a128, xa, t.row0, bar);
+                    else
+                        for (int i = 0; i < boxes; ++i)
+                            tma_load_2d(base + i * 32 * kStepBytes, &maps.a32, xa, t.row0 + 32 * i, bar);
+                } else {
+                    const int nt = min(P::kTilesK, ct - ks * P::kTilesK), bytes = nt * kScaleTile;
+                    const uint32_t sfa = base + P::kABytes + P::kBBytes, sfb = sfa + P::kSfaBytes;
+                    mbar_arrive_expect_tx(bar, bytes * (second ? 3 : 2));
+                    const size_t k0 = (size_t)ks * P::kTilesK * kScaleTile, row = (size_t)ct * kScaleTile;
+                    const size_t wt = (size_t)t.g * w_row_tiles + n0 / kScaleRows;
+                    bulk_load(sfb, a.w_scales[0] + wt * row + k0, bytes, bar);
+                    if (second)
+                        bulk_load(sfb + P::kSfbBytes / 2, a.w_scales[DUAL ? 1 : 0] + (DUAL ? wt : wt + 1) * row + k0, bytes, bar);
+                    bulk_load(sfa, a.a_scales + t.srow_tile * row + k0, bytes, bar);
+                }
+                ++issued;
+                if (++st == P::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        // the newest copy of each stage lands before the CTA leaves, whoever gave up
+        for (int i = 0; i < min(issued, P::kStages); ++i) {
+            if (--st < 0) {
+                st = P::kStages - 1;
+                ph ^= 1;
+            }
+            mbar_wait(smem_u32(&sh.full[st]), ph, 1 << 20, nullptr);
+        }
+    } else if (warp == 1 && lane == 0) {
+        // ---- scales into tensor memory, MMAs
+        int st = 0, acc = 0;
+        uint32_t ph = 0, aph = 0;
+        bool ok = true;
+        const uint32_t sf0 = tmem + P::kAccs * BN;
+        for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+            const Tile t = tile_at(a, sh, tile, n_tiles);
+            // columns of the first weight row inside its scale row tile (32 rows a column)
+            const uint32_t sub = (uint32_t)(t.nt * P::kOutN % kScaleRows) / 32;
+            if (!mbar_wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1, a.wait_limit, abort)) {
+                fail();
+                break;
+            }
+            tc_fence_after();
+            const uint32_t d = tmem + acc * BN;
+            for (int ks = 0; ks < n_steps; ++ks) {
+                if (!mbar_wait(smem_u32(&sh.full[st]), ph, a.wait_limit, abort)) {
+                    fail();
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t base = smem0 + st * P::kStageBytes;
+                const uint32_t sfa_s = base + P::kABytes + P::kBBytes, sfb_s = sfa_s + P::kSfaBytes;
+                const uint32_t sfa = sf0 + st * P::kSfCols, sfb = sfa + 4 * P::kTilesK;
+                const uint64_t ad = desc_sw128(base), bd = desc_sw128(base + P::kABytes);
+#pragma unroll
+                for (int j = 0; j < P::kTilesK; ++j) {
+                    tmem_cp_scales(sfa + 4 * j, desc_scales(sfa_s + j * kScaleTile));
+#pragma unroll
+                    for (int c = 0; c < P::kChunks; ++c)
+                        tmem_cp_scales(sfb + 4 * (P::kChunks * j + c), desc_scales(sfb_s + (c * P::kTilesK + j) * kScaleTile));
+                }
+                const int kk = min(4, (a.K - ks * P::kStepK) / (P::kStepK / 4));
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (j >= kk) break;
+                    const uint32_t id = idesc_scaled<FMT>(P::kMmaN, P::kNv ? 0 : j), go = ks > 0 || j > 0;
+                    const uint32_t sa = sfa + (P::kNv ? 4 * j : 0), sb = sfb + (P::kNv ? 4 * P::kChunks * j : 0) + sub;
+                    // 32 bytes along K inside the swizzle atom
+                    mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, id, sa, sb, go);
+                    if (P::kMmaN != BN)
+                        mma_scaled<FMT>(d + P::kMmaN, ad + 2 * j, bd + 2 * j + (P::kMmaN * kStepBytes >> 4), id, sa, sb + 4, go);
+                }
+                mma_commit(smem_u32(&sh.empty[st]));
+                if (++st == P::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            mma_commit(smem_u32(&sh.acc_full[acc]));
+            if (++acc == P::kAccs) {
+                acc = 0;
+                aph ^= 1;
+            }
+        }
+        if (*abort) {
+            mma_commit(smem_u32(&sh.drain));
+            mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
+        }
+    } else if (warp >= 4) {
+        // ---- accumulators to outputs
+        const int quad = warp - 4;
+        int acc = 0;
+        uint32_t aph = 0;
+        for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+            const Tile t = tile_at(a, sh, tile, n_tiles);
+            bool ok = true;
+            if (lane == 0) ok = mbar_wait(smem_u32(&sh.acc_full[acc]), aph, a.wait_limit, abort);
+            if (!__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) {
+                if (lane == 0) fail();
+                break;
+            }
+            tc_fence_after();
+            const int r = quad * 32 + lane;
+            const uint32_t d = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
+            if (quad * 32 < t.rows) {
+                const bool live = r < t.rows;
+                const size_t row = (size_t)t.row0 + r;
+                const float rs = live && a.a_row_scale ? __ldg(a.a_row_scale + row) : 1.0f;
+                const float s0 = rs * (a.alpha[0] ? __ldg(a.alpha[0] + t.g) : 1.0f);
+                if (!DUAL) {
+#pragma unroll 1
+                    for (int c = 0; c < BN; c += 32) {
+                        uint32_t u0[16], u1[16];
+                        tmem_ld16(d + c, u0);
+                        tmem_ld16(d + c + 16, u1);
+                        tmem_ld_wait();
+                        float v[32];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            v[i] = __uint_as_float(u0[i]) * s0;
+                            v[16 + i] = __uint_as_float(u1[i]) * s0;
+                        }
+                        if (live) store_y32(a, row, t.nt * BN + c, v);
+                    }
+                } else {
+                    const float s1 = rs * (a.alpha[1] ? __ldg(a.alpha[1] + t.g) : 1.0f);
+                    float ginv = 1.0f;
+                    if (P::kNv) ginv = __fdiv_rn(1.0f, __ldg(a.h_gscale + t.g));
+                    const int hct = scaled_col_tiles(FMT, a.N);
+                    const long long srow = (long long)t.srow_tile * kScaleRows + r;
+                    uint32_t word = 0;
+#pragma unroll 1
+                    for (int c = 0; c < P::kOutN; c += 32) {
+                        const int col = t.nt * P::kOutN + c;
+                        if (col >= a.N) break;
+                        float h[32];
+                        uint32_t amax[2] = {0, 0};
+#pragma unroll
+                        for (int i0 = 0; i0 < 32; i0 += 16) {
+                            uint32_t ug[16], uu[16];
+                            tmem_ld16(d + c + i0, ug);
+                            tmem_ld16(d + BN / 2 + c + i0, uu);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float v = silu(__uint_as_float(ug[i]) * s0) * (__uint_as_float(uu[i]) * s1);
+                                h[i0 + i] = v;
+                                amax[i0 / 16] = max(amax[i0 / 16], __float_as_uint(v) & 0x7FFFFFFFu);
+                            }
+                        }
+                        if (P::kNv) {
+                            uint32_t q[4];
+#pragma unroll
+                            for (int b = 0; b < 2; ++b) {
+                                float inv;
+                                word |= nvfp4_scale(amax[b], ginv, inv) << (8 * ((c / 16 + b) & 3));
+#pragma unroll
+                                for (int i0 = 0; i0 < 16; i0 += 8) {
+                                    float e[8];
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) e[i] = h[16 * b + i0 + i] * inv;
+                                    q[2 * b + i0 / 8] = to_e2m1x8(e);
+                                }
+                            }
+                            if (live)
+                                *reinterpret_cast<uint4 *>(a.h_codes + row * (a.N / 2) + col / 2) = make_uint4(q[0], q[1], q[2], q[3]);
+                            if ((c & 32) != 0) {
+                                if (live) *reinterpret_cast<uint32_t *>(a.h_scales + scale_at(srow, (col - 32) / 16, hct)) = word;
+                                word = 0;
+                            }
+                        } else {
+                            const uint32_t s = pow2_scale<MOE_SCALED_MXFP8>(max(amax[0], amax[1]));
+                            const float inv = pow2_inverse(s);
+                            word |= s << (8 * ((col / 32) & 3));
+                            uint32_t q[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                q[i] = to_e4m3x2(h[4 * i + 1] * inv, h[4 * i] * inv) |
+                                       ((uint32_t)to_e4m3x2(h[4 * i + 3] * inv, h[4 * i + 2] * inv) << 16);
+                            if (live) {
+                                uint4 *p = reinterpret_cast<uint4 *>(a.h_codes + row * a.N + col);
+                                p[0] = make_uint4(q[0], q[1], q[2], q[3]);
+                                p[1] = make_uint4(q[4], q[5], q[6], q[7]);
+                            }
+                            if (P::kOutN == 64) {                      // half a column tile: two bytes
+                                if ((c & 32) != 0) {
+                                    if (live)
+                                        *reinterpret_cast<uint16_t *>(a.h_scales + scale_at(srow, (col - 32) / 32, hct)) =
+                                            (uint16_t)(word >> (8 * (((col - 32) / 32) & 3)));
+                                    word = 0;
+                                }
+                            } else if (((col / 32) & 3) == 3) {
+                                if (live) *reinterpret_cast<uint32_t *>(a.h_scales + scale_at(srow, col / 32 - 3, hct)) = word;
+                                word = 0;
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[acc]));
+            if (++acc == P::kAccs) {
+                acc = 0;
+                aph ^= 1;
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 3) tmem_dealloc(tmem, 512);
+}
+
+template <int FMT, bool DUAL, int BN>
+cudaError_t launch_plan(const ScaledGemmArgs &a, const Maps &maps, int ctas, cudaStream_t st)
+{
+    using P = Plan<FMT, DUAL, BN>;
+    auto k = scaled_gemm_kernel<FMT, DUAL, BN>;
+    static std::atomic<uint64_t> ready{0};               // devices on which the kernel's shared memory is set
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
+        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    }
+    k<<<ctas, kThreads, P::kSmem, st>>>(a, maps);
+    return cudaGetLastError();
+}
+
+template <int FMT, bool DUAL>
+cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
+{
+    constexpr bool kNv = FMT == MOE_SCALED_NVFP4;
+    const int sms = device_sm_count();
+    // row tiles at most: every group's last one may be partial
+    const long long mt = a.R / kScaleRows + (a.G < a.R ? a.G : a.R);
+    auto tiles = [&](int out_n) { return mt * ((a.N + out_n - 1) / out_n); };
+    int bn = 256;
+    if (DUAL) {
+        if (tiles(128) < sms) bn = 128;
+    } else {
+        if (tiles(256) < sms) bn = 128;
+        if (tiles(128) < sms) bn = 64;
+    }
+    const long long n = tiles(DUAL ? bn / 2 : bn);
+    const int ctas = (int)(n < sms ? n : sms);
+    Maps maps;
+    const uint64_t abytes = kNv ? a.K / 2 : a.K;
+    bool ok = make_map_2d(&maps.a128, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, abytes, a.R, kStepBytes, 128,
+                          CU_TENSOR_MAP_SWIZZLE_128B) &&
+              make_map_2d(&maps.a32, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, abytes, a.R, kStepBytes, 32,
+                          CU_TENSOR_MAP_SWIZZLE_128B);
+    for (int i = 0; i < 2; ++i) {
+        const uint8_t *w = a.w_codes[DUAL ? i : 0];
+        const uint32_t box = DUAL ? bn / 2 : bn;
+        if (kNv)
+            ok = ok && make_map_2d(&maps.w[i], w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.K / 2, (uint64_t)a.G * a.N, kStepBytes,
+                                   box, CU_TENSOR_MAP_SWIZZLE_128B);
+        else
+            ok = ok && make_map_4bit(&maps.w[i], w, a.K, (uint64_t)a.G * a.N, box);
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    if (bn == 256) return launch_plan<FMT, DUAL, 256>(a, maps, ctas, st);
+    if (bn == 128) return launch_plan<FMT, DUAL, 128>(a, maps, ctas, st);
+    if constexpr (!DUAL) return launch_plan<FMT, DUAL, 64>(a, maps, ctas, st);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_scaled_gemm(const ScaledGemmArgs &a, int fmt, bool swiglu, cudaStream_t st)
+{
+    if (fmt == MOE_SCALED_NVFP4)
+        return swiglu ? launch_fmt<MOE_SCALED_NVFP4, true>(a, st) : launch_fmt<MOE_SCALED_NVFP4, false>(a, st);
+    return swiglu ? launch_fmt<MOE_SCALED_MXFP8, true>(a, st) : launch_fmt<MOE_SCALED_MXFP8, false>(a, st);
+}
+
+}  // namespace qmoe

@@ -38,6 +38,22 @@ inline bool make_map_2d(CUtensorMap *m, const void *base, CUtensorMapDataType dt
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// 2D row-major map of 4-bit codes, two a byte, which the copy widens to one byte each in shared memory
+// (16 codes as 8 bytes of codes and 8 of padding): rows of 128-code boxes, 128-byte swizzle.  `cols` a
+// multiple of 128, base 32-byte aligned.
+inline bool make_map_4bit(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint32_t br)
+{
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {cols / 2};
+    cuuint32_t box[2] = {128, br};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // 3D map with explicit byte strides for dimensions 1 and 2 (inner dimension contiguous).
 inline bool make_map_3d(CUtensorMap *m, const void *base, CUtensorMapDataType dt, const uint64_t dims[3],
                         const uint64_t strides[2], const uint32_t box[3], CUtensorMapSwizzle swz)
