@@ -13,10 +13,10 @@
 // the rows present are copied), weights the N = BN operand, so that a thread of the epilogue holds
 // consecutive outputs of one row: whole blocks of h for its scale, whole sectors of y.
 //
-// One CTA per SM walks over the tiles: warp 0 copies codes (TMA), warp 2 copies scale tiles (bulk), warp 1
-// moves a step's scales from shared into tensor memory (tcgen05.cp) and issues its MMAs, warps 4-7 read
-// the accumulators and write.  Every stage has its own scale columns, so a stage's barrier also guards
-// them.
+// One CTA per SM walks over the tiles: warp 0 copies codes (TMA), warp 2 copies scale tiles (bulk), warp 3
+// moves a step's scales from shared into tensor memory (tcgen05.cp), warp 1 issues its MMAs, warps 4-11
+// read the accumulators and write.  Every stage has its own scale columns, so a stage's barriers also
+// guard them.
 #include "scaled.cuh"
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"
@@ -26,7 +26,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
 constexpr int kMaxGroups = 1024;
 constexpr int kStepBytes = 128;                    // bytes of a K step in a row of codes (as in shared memory)
 
@@ -54,10 +54,10 @@ struct Maps {
 };
 
 struct Shared {
-    uint64_t full[8], empty[8], acc_full[2], acc_empty[2], drain;
+    uint64_t full[8], sf_full[8], empty[8], acc_full[2], acc_empty[2], drain[2];
     uint32_t tmem;
     int abort;
-    int warp_sum[8];
+    int warp_sum[kThreads / 32];
     int first[kMaxGroups + 1];                               // row tiles of the groups before g
 };
 
@@ -129,27 +129,35 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t adesc, uint64_t 
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-// 32 fp32 of one row to y (bf16 or fp32): columns [col, col + 32) below N, N a multiple of 8.
-__device__ __forceinline__ void store_y32(const ScaledGemmArgs &a, size_t row, int col, const float (&v)[32])
+// 32 accumulator columns of the warp's rows, times s.
+__device__ __forceinline__ void load_cols(uint32_t taddr, float s, float (&v)[32])
+{
+    uint32_t u0[16], u1[16];
+    tmem_ld16(taddr, u0);
+    tmem_ld16(taddr + 16, u1);
+    tmem_ld_wait();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[i] = __uint_as_float(u0[i]) * s;
+        v[16 + i] = __uint_as_float(u1[i]) * s;
+    }
+}
+
+// The first n (a multiple of 8) of 32 fp32.
+__device__ __forceinline__ void store_f32(float *p, const float (&v)[32], int n)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (col + 8 * i >= a.N) return;
-        if (a.y_f32) {
-            float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(a.y) + row * a.N + col + 8 * i);
-            p[0] = make_float4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
-            p[1] = make_float4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
-        } else {
-            uint32_t w[4];
+    for (int i = 0; i < 32; i += 4)
+        if (i < n) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+}
+
+// The first n (a multiple of 8) of 2 W bf16.
+template <int W>
+__device__ __forceinline__ void store_bf16(uint16_t *p, const uint32_t (&w)[W], int n)
+{
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const __nv_bfloat162 b = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
-                w[k] = *reinterpret_cast<const uint32_t *>(&b);
-            }
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(a.y) + row * a.N + col + 8 * i) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-        }
-    }
+    for (int i = 0; i < W; i += 4)
+        if (2 * i < n) *reinterpret_cast<uint4 *>(p + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
 }
 
 template <int FMT, bool DUAL, int BN>
@@ -168,13 +176,15 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     if (threadIdx.x == 0) {
         for (int i = 0; i < P::kStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 2);                      // codes and scales
+            mbar_init(smem_u32(&sh.sf_full[i]), 1);
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
         for (int i = 0; i < P::kAccs; ++i) {
             mbar_init(smem_u32(&sh.acc_full[i]), 1);
-            mbar_init(smem_u32(&sh.acc_empty[i]), 4);
+            mbar_init(smem_u32(&sh.acc_empty[i]), 8);
         }
-        mbar_init(smem_u32(&sh.drain), 1);
+        mbar_init(smem_u32(&sh.drain[0]), 1);
+        mbar_init(smem_u32(&sh.drain[1]), 1);
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -280,7 +290,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             mbar_wait(smem_u32(&sh.full[st]), ph, 1 << 20, nullptr);
         }
     } else if (warp == 1 && lane == 0) {
-        // ---- scales into tensor memory, MMAs
+        // ---- MMAs
         int st = 0, acc = 0;
         uint32_t ph = 0, aph = 0;
         bool ok = true;
@@ -296,23 +306,16 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             tc_fence_after();
             const uint32_t d = tmem + acc * BN;
             for (int ks = 0; ks < n_steps; ++ks) {
-                if (!mbar_wait(smem_u32(&sh.full[st]), ph, a.wait_limit, abort)) {
+                if (!mbar_wait(smem_u32(&sh.full[st]), ph, a.wait_limit, abort) ||
+                    !mbar_wait(smem_u32(&sh.sf_full[st]), ph, a.wait_limit, abort)) {
                     fail();
                     ok = false;
                     break;
                 }
                 tc_fence_after();
                 const uint32_t base = smem0 + st * P::kStageBytes;
-                const uint32_t sfa_s = base + P::kABytes + P::kBBytes, sfb_s = sfa_s + P::kSfaBytes;
                 const uint32_t sfa = sf0 + st * P::kSfCols, sfb = sfa + 4 * P::kTilesK;
                 const uint64_t ad = desc_sw128(base), bd = desc_sw128(base + P::kABytes);
-#pragma unroll
-                for (int j = 0; j < P::kTilesK; ++j) {
-                    tmem_cp_scales(sfa + 4 * j, desc_scales(sfa_s + j * kScaleTile));
-#pragma unroll
-                    for (int c = 0; c < P::kChunks; ++c)
-                        tmem_cp_scales(sfb + 4 * (P::kChunks * j + c), desc_scales(sfb_s + (c * P::kTilesK + j) * kScaleTile));
-                }
                 const int kk = min(4, (a.K - ks * P::kStepK) / (P::kStepK / 4));
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -337,12 +340,47 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             }
         }
         if (*abort) {
-            mma_commit(smem_u32(&sh.drain));
-            mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
+            mma_commit(smem_u32(&sh.drain[0]));
+            mbar_wait(smem_u32(&sh.drain[0]), 0, 1 << 20, nullptr);
+        }
+    } else if (warp == 3 && lane == 0) {
+        // ---- scales into tensor memory
+        int st = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+            for (int ks = 0; ks < n_steps; ++ks) {
+                if (!mbar_wait(smem_u32(&sh.full[st]), ph, a.wait_limit, abort)) {
+                    fail();
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t sfa_s = smem0 + st * P::kStageBytes + P::kABytes + P::kBBytes, sfb_s = sfa_s + P::kSfaBytes;
+                const uint32_t sfa = tmem + P::kAccs * BN + st * P::kSfCols, sfb = sfa + 4 * P::kTilesK;
+#pragma unroll
+                for (int j = 0; j < P::kTilesK; ++j) {
+                    tmem_cp_scales(sfa + 4 * j, desc_scales(sfa_s + j * kScaleTile));
+#pragma unroll
+                    for (int c = 0; c < P::kChunks; ++c)
+                        tmem_cp_scales(sfb + 4 * (P::kChunks * j + c), desc_scales(sfb_s + (c * P::kTilesK + j) * kScaleTile));
+                }
+                mma_commit(smem_u32(&sh.sf_full[st]));
+                if (++st == P::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        if (*abort) {
+            mma_commit(smem_u32(&sh.drain[1]));
+            mbar_wait(smem_u32(&sh.drain[1]), 0, 1 << 20, nullptr);
         }
     } else if (warp >= 4) {
         // ---- accumulators to outputs
-        const int quad = warp - 4;
+        // two warps share a quarter of the rows, each with half of the tile's output columns
+        constexpr int kCols = P::kOutN / 2;
+        const int quad = warp & 3, half = (warp - 4) >> 2;
         int acc = 0;
         uint32_t aph = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
@@ -354,106 +392,100 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 break;
             }
             tc_fence_after();
-            const int r = quad * 32 + lane;
-            const uint32_t d = tmem + acc * BN + ((uint32_t)(quad * 32) << 16);
-            if (quad * 32 < t.rows) {
-                const bool live = r < t.rows;
-                const size_t row = (size_t)t.row0 + r;
-                const float rs = live && a.a_row_scale ? __ldg(a.a_row_scale + row) : 1.0f;
-                const float s0 = rs * (a.alpha[0] ? __ldg(a.alpha[0] + t.g) : 1.0f);
-                if (!DUAL) {
+            const int r = quad * 32 + lane, col0 = t.nt * P::kOutN + half * kCols;
+            const uint32_t d = tmem + acc * BN + half * kCols + ((uint32_t)(quad * 32) << 16);
+            const bool any = quad * 32 < t.rows && col0 < a.N, live = any && r < t.rows;
+            const size_t row = (size_t)t.row0 + r;
+            const float rs = live && a.a_row_scale ? __ldg(a.a_row_scale + row) : 1.0f;
+            const float s0 = rs * (a.alpha[0] ? __ldg(a.alpha[0] + t.g) : 1.0f);
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[acc]));
+            };
+            if (!any) {
+                release();
+            } else if (!DUAL && a.y_f32) {
 #pragma unroll 1
-                    for (int c = 0; c < BN; c += 32) {
-                        uint32_t u0[16], u1[16];
-                        tmem_ld16(d + c, u0);
-                        tmem_ld16(d + c + 16, u1);
-                        tmem_ld_wait();
-                        float v[32];
+                for (int c = 0; c < kCols; c += 32) {
+                    float v[32];
+                    load_cols(d + c, s0, v);
+                    if (live) store_f32(static_cast<float *>(a.y) + row * a.N + col0 + c, v, a.N - col0 - c);
+                }
+                release();
+            } else if (!DUAL) {
+                // the accumulators go to registers, rounded, before anything is stored: the next tile's
+                // products start while this one's outputs are on their way
+                uint32_t w[kCols / 2];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            v[i] = __uint_as_float(u0[i]) * s0;
-                            v[16 + i] = __uint_as_float(u1[i]) * s0;
-                        }
-                        if (live) store_y32(a, row, t.nt * BN + c, v);
+                for (int c = 0; c < kCols; c += 32) {
+                    float v[32];
+                    load_cols(d + c, s0, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                        w[c / 2 + i] = *reinterpret_cast<const uint32_t *>(&b);
                     }
-                } else {
-                    const float s1 = rs * (a.alpha[1] ? __ldg(a.alpha[1] + t.g) : 1.0f);
-                    float ginv = 1.0f;
-                    if (P::kNv) ginv = __fdiv_rn(1.0f, __ldg(a.h_gscale + t.g));
-                    const int hct = scaled_col_tiles(FMT, a.N);
-                    const long long srow = (long long)t.srow_tile * kScaleRows + r;
-                    uint32_t word = 0;
-#pragma unroll 1
-                    for (int c = 0; c < P::kOutN; c += 32) {
-                        const int col = t.nt * P::kOutN + c;
-                        if (col >= a.N) break;
-                        float h[32];
-                        uint32_t amax[2] = {0, 0};
+                }
+                release();
+                if (live) store_bf16<kCols / 2>(static_cast<uint16_t *>(a.y) + row * a.N + col0, w, a.N - col0);
+            } else {
+                const float s1 = rs * (a.alpha[1] ? __ldg(a.alpha[1] + t.g) : 1.0f);
+                float ginv = 1.0f;
+                if (P::kNv) ginv = __fdiv_rn(1.0f, __ldg(a.h_gscale + t.g));
+                const int hct = scaled_col_tiles(FMT, a.N);
+                const long long srow = (long long)t.srow_tile * kScaleRows + r;
+                constexpr int kBlk = scaled_block(FMT), kWords = kCols / (P::kNv ? 8 : 4);
+                uint32_t q[kWords], word = 0;                   // codes and scale bytes of the warp's columns
 #pragma unroll
-                        for (int i0 = 0; i0 < 32; i0 += 16) {
-                            uint32_t ug[16], uu[16];
-                            tmem_ld16(d + c + i0, ug);
-                            tmem_ld16(d + BN / 2 + c + i0, uu);
-                            tmem_ld_wait();
+                for (int c = 0; c < kCols; c += 32) {
+                    float h[32];
+                    {
+                        float u[32];
+                        load_cols(d + c, s0, h);
+                        load_cols(d + BN / 2 + c, s1, u);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float v = silu(__uint_as_float(ug[i]) * s0) * (__uint_as_float(uu[i]) * s1);
-                                h[i0 + i] = v;
-                                amax[i0 / 16] = max(amax[i0 / 16], __float_as_uint(v) & 0x7FFFFFFFu);
-                            }
-                        }
+                        for (int i = 0; i < 32; ++i) h[i] = silu(h[i]) * u[i];
+                    }
+#pragma unroll
+                    for (int i0 = 0; i0 < 32; i0 += kBlk) {
+                        uint32_t m = 0;
+#pragma unroll
+                        for (int i = 0; i < kBlk; ++i) m = max(m, __float_as_uint(h[i0 + i]) & 0x7FFFFFFFu);
+                        uint32_t sc;
+                        float inv;
                         if (P::kNv) {
-                            uint32_t q[4];
-#pragma unroll
-                            for (int b = 0; b < 2; ++b) {
-                                float inv;
-                                word |= nvfp4_scale(amax[b], ginv, inv) << (8 * ((c / 16 + b) & 3));
-#pragma unroll
-                                for (int i0 = 0; i0 < 16; i0 += 8) {
-                                    float e[8];
-#pragma unroll
-                                    for (int i = 0; i < 8; ++i) e[i] = h[16 * b + i0 + i] * inv;
-                                    q[2 * b + i0 / 8] = to_e2m1x8(e);
-                                }
-                            }
-                            if (live)
-                                *reinterpret_cast<uint4 *>(a.h_codes + row * (a.N / 2) + col / 2) = make_uint4(q[0], q[1], q[2], q[3]);
-                            if ((c & 32) != 0) {
-                                if (live) *reinterpret_cast<uint32_t *>(a.h_scales + scale_at(srow, (col - 32) / 16, hct)) = word;
-                                word = 0;
-                            }
+                            sc = nvfp4_scale(m, ginv, inv);
                         } else {
-                            const uint32_t s = pow2_scale<MOE_SCALED_MXFP8>(max(amax[0], amax[1]));
-                            const float inv = pow2_inverse(s);
-                            word |= s << (8 * ((col / 32) & 3));
-                            uint32_t q[8];
+                            sc = pow2_scale<MOE_SCALED_MXFP8>(m);
+                            inv = pow2_inverse(sc);
+                        }
+                        word |= sc << (8 * ((c + i0) / kBlk));
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                q[i] = to_e4m3x2(h[4 * i + 1] * inv, h[4 * i] * inv) |
-                                       ((uint32_t)to_e4m3x2(h[4 * i + 3] * inv, h[4 * i + 2] * inv) << 16);
-                            if (live) {
-                                uint4 *p = reinterpret_cast<uint4 *>(a.h_codes + row * a.N + col);
-                                p[0] = make_uint4(q[0], q[1], q[2], q[3]);
-                                p[1] = make_uint4(q[4], q[5], q[6], q[7]);
-                            }
-                            if (P::kOutN == 64) {                      // half a column tile: two bytes
-                                if ((c & 32) != 0) {
-                                    if (live)
-                                        *reinterpret_cast<uint16_t *>(a.h_scales + scale_at(srow, (col - 32) / 32, hct)) =
-                                            (uint16_t)(word >> (8 * (((col - 32) / 32) & 3)));
-                                    word = 0;
-                                }
-                            } else if (((col / 32) & 3) == 3) {
-                                if (live) *reinterpret_cast<uint32_t *>(a.h_scales + scale_at(srow, col / 32 - 3, hct)) = word;
-                                word = 0;
+                        for (int i = 0; i < kBlk; i += 8) {
+                            float e[8];
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) e[k] = h[i0 + i + k] * inv;
+                            if (P::kNv) {
+                                q[(c + i0 + i) / 8] = to_e2m1x8(e);
+                            } else {
+                                q[(c + i0 + i) / 4] = to_e4m3x2(e[1], e[0]) | ((uint32_t)to_e4m3x2(e[3], e[2]) << 16);
+                                q[(c + i0 + i) / 4 + 1] = to_e4m3x2(e[5], e[4]) | ((uint32_t)to_e4m3x2(e[7], e[6]) << 16);
                             }
                         }
                     }
                 }
-                tc_fence_before();
+                release();
+                if (live) {
+                    uint4 *p = reinterpret_cast<uint4 *>(a.h_codes + (P::kNv ? (row * a.N + col0) / 2 : row * a.N + col0));
+#pragma unroll
+                    for (int i = 0; i < kWords / 4; ++i) p[i] = make_uint4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+                    uint8_t *ps = a.h_scales + scale_at(srow, col0 / kBlk, hct);
+                    if (kCols / kBlk == 4) *reinterpret_cast<uint32_t *>(ps) = word;
+                    else if (kCols / kBlk == 2) *reinterpret_cast<uint16_t *>(ps) = (uint16_t)word;
+                    else *ps = (uint8_t)word;
+                }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[acc]));
             if (++acc == P::kAccs) {
                 acc = 0;
                 aph ^= 1;
