@@ -94,6 +94,27 @@ __device__ __forceinline__ float nvfp4_row_factor(uint32_t amax_bits)
                                  : fmaxf(__uint_as_float(amax_bits) * (1.0f / 2688.0f), 7.70371977754894e-34f);
 }
 
+// ---------------------------------------------------------------- launches
+
+// Every kernel of this family lets its successor in the stream start at once (griddepcontrol.launch_dependents
+// first thing) and reads or writes memory only after griddepcontrol.wait, in every block: a successor's
+// set-up (barriers, tensor memory, tensor maps) runs under its predecessor's tail.
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+
 // ---------------------------------------------------------------- kernel arguments
 
 // Rows to block-scaled rows (scaled_rows.cu).

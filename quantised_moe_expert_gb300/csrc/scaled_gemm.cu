@@ -17,6 +17,7 @@
 // moves a step's scales from shared into tensor memory (tcgen05.cp), warp 1 issues its MMAs, warps 4-11
 // read the accumulators and write.  Every stage has its own scale columns, so a stage's barriers also
 // guard them.
+#include <stdlib.h>
 #include "scaled.cuh"
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"
@@ -151,10 +152,18 @@ __device__ __forceinline__ void store_f32(float *p, const float (&v)[32], int n)
         if (i < n) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
 
-// The first n (a multiple of 8) of 2 W bf16.
+// The first n (a multiple of 8) of 2 W bf16.  Whole 32-byte sectors a lane where the row allows it.
 template <int W>
 __device__ __forceinline__ void store_bf16(uint16_t *p, const uint32_t (&w)[W], int n)
 {
+    if (2 * W <= n && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
+#pragma unroll
+        for (int i = 0; i < W; i += 8)
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 2 * i), "r"(w[i]), "r"(w[i + 1]),
+                         "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                         : "memory");
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < W; i += 4)
         if (2 * i < n) *reinterpret_cast<uint4 *>(p + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
@@ -173,7 +182,12 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     const int ct = scaled_col_tiles(FMT, a.K);
     const int w_row_tiles = (a.N + kScaleRows - 1) / kScaleRows;      // scale row tiles of a matrix
 
+    pdl_trigger();
     if (threadIdx.x == 0) {
+        prefetch_map(&maps.w[0]);
+        if (DUAL) prefetch_map(&maps.w[1]);
+        prefetch_map(&maps.a32);
+        prefetch_map(&maps.a128);
         for (int i = 0; i < P::kStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 2);                      // codes and scales
             mbar_init(smem_u32(&sh.sf_full[i]), 1);
@@ -509,8 +523,7 @@ cudaError_t launch_plan(const ScaledGemmArgs &a, const Maps &maps, int ctas, cud
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
     }
-    k<<<ctas, kThreads, P::kSmem, st>>>(a, maps);
-    return cudaGetLastError();
+    return launch_dependent(k, ctas, kThreads, P::kSmem, st, a, maps);
 }
 
 template <int FMT, bool DUAL>
@@ -528,6 +541,8 @@ cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
         if (tiles(256) < sms) bn = 128;
         if (tiles(128) < sms) bn = 64;
     }
+    if (getenv("SG_BN")) bn = atoi(getenv("SG_BN"));
+    if (DUAL && bn == 64) bn = 128;
     const long long n = tiles(DUAL ? bn / 2 : bn);
     const int ctas = (int)(n < sms ? n : sms);
     Maps maps;

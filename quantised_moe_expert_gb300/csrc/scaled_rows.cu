@@ -147,6 +147,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     constexpr int kLanes = kBlk / 8;                          // lanes of a block
     __shared__ float sbuf[kThreads / 32];
     __shared__ uint32_t mbuf[kThreads / 32];
+    tc::pdl_trigger();
     tc::pdl_wait();
     const int tr = threadIdx.x % TPR;
     const int t = blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
@@ -303,8 +304,7 @@ template <int FMT, bool NORM, bool F32, int TPR, int CH>
 cudaError_t launch_one(const RowArgs &a, cudaStream_t st)
 {
     const int rows = kThreads / TPR;
-    rows_kernel<FMT, NORM, F32, TPR, CH><<<(unsigned)((a.T + rows - 1) / rows), kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(rows_kernel<FMT, NORM, F32, TPR, CH>, (unsigned)((a.T + rows - 1) / rows), kThreads, 0, st, a);
 }
 
 // Threads a row and segments a thread.  Few rows: a segment a thread, for the shortest way through (T = 1,
@@ -328,6 +328,7 @@ cudaError_t launch_fmt(const RowArgs &a, cudaStream_t st)
 __global__ void tile_scales_kernel(const uint8_t *__restrict__ src, uint8_t *__restrict__ dst, int nb, int ct, int N,
                                    int row_tiles, size_t words)
 {
+    tc::pdl_trigger();
     tc::pdl_wait();
     for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < words; i += (size_t)gridDim.x * blockDim.x) {
         // word i of the tiles: tile i / 128, row (i % 128) % 4 * 32 + (i % 128) / 4 of it
@@ -368,8 +369,8 @@ cudaError_t launch_tile_scales(const uint8_t *src, uint8_t *dst, int fmt, int G,
     const int nb = n / scaled_block(fmt), ct = scaled_col_tiles(fmt, n), row_tiles = (N + kScaleRows - 1) / kScaleRows;
     const size_t words = (size_t)G * row_tiles * ct * 128;
     const size_t blocks = (words + 255) / 256;
-    tile_scales_kernel<<<(unsigned)(blocks < 152 * 16 ? blocks : 152 * 16), 256, 0, st>>>(src, dst, nb, ct, N, row_tiles, words);
-    return cudaGetLastError();
+    return launch_dependent(tile_scales_kernel, (unsigned)(blocks < 152 * 16 ? blocks : 152 * 16), 256, 0, st, src, dst, nb, ct,
+                            N, row_tiles, words);
 }
 
 }  // namespace qmoe
