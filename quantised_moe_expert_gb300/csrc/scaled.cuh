@@ -10,8 +10,8 @@ namespace qmoe {
 __host__ __device__ constexpr int scaled_block(int fmt) { return fmt == MOE_SCALED_NVFP4 ? 16 : 32; }
 __host__ __device__ constexpr bool scaled_is4(int fmt) { return fmt != MOE_SCALED_MXFP8; }
 
-// Scale tiles: 128 rows x 4 consecutive block scales of each row, 512 bytes, in the order in which
-// tcgen05.cp (32 x 128 bits) puts them into tensor memory: byte (r % 32) * 16 + (r / 32) * 4 + b.
+// Scale tiles: 128 rows x 4 consecutive block scales of each row, 512 bytes, in the order in which tensor
+// memory holds them (32 lanes x four 32-bit columns): byte (r % 32) * 16 + (r / 32) * 4 + b.
 constexpr int kScaleTile = 512;
 constexpr int kScaleRows = 128;
 __host__ __device__ constexpr int scaled_col_tiles(int fmt, int n) { return (n / scaled_block(fmt) + 3) / 4; }

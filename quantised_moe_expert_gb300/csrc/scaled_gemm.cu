@@ -13,10 +13,11 @@
 // the rows present are copied), weights the N = BN operand, so that a thread of the epilogue holds
 // consecutive outputs of one row: whole blocks of h for its scale, whole sectors of y.
 //
-// One CTA per SM walks over the tiles: warp 0 copies codes (TMA), warp 2 copies scale tiles (bulk), warp 3
-// moves a step's scales from shared into tensor memory (tcgen05.cp), warp 1 issues its MMAs, warps 4-11
-// read the accumulators and write.  Every stage has its own scale columns, so a stage's barriers also
-// guard them.
+// One CTA per SM walks over the tiles: warp 0 copies codes (TMA), warp 2 copies scale tiles (bulk), warps
+// 4-7 move a step's scales from shared into tensor memory, warp 1 issues its MMAs, warps 8-15 read the
+// accumulators and write.  Every stage has its own scale columns, so a stage's barriers also guard them.
+// The scales go through registers (tcgen05.st): a tcgen05.cp of a 512-byte tile costs its thread and the
+// tensor pipe 60 to 90 cycles, twelve of them more than the step's MMAs.
 #include <stdlib.h>
 #include "scaled.cuh"
 #include "tc_ptx.cuh"
@@ -27,7 +28,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kMaxGroups = 1024;
 constexpr int kStepBytes = 128;                    // bytes of a K step in a row of codes (as in shared memory)
 
@@ -55,7 +56,7 @@ struct Maps {
 };
 
 struct Shared {
-    uint64_t full[8], sf_full[8], empty[8], acc_full[2], acc_empty[2], drain[2];
+    uint64_t full[8], sf_full[8], empty[8], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
     int warp_sum[kThreads / 32];
@@ -92,14 +93,27 @@ __device__ __forceinline__ Tile tile_at(const ScaledGemmArgs &a, const Shared &s
     return t;
 }
 
-// Scale tiles in shared memory as tcgen05.cp takes them: 8 rows x 16 bytes cores, 128 bytes apart, no swizzle.
-__device__ __forceinline__ uint64_t desc_scales(uint32_t addr)
+__device__ __forceinline__ void set4(uint32_t *r, uint4 v)
 {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+    r[0] = v.x;
+    r[1] = v.y;
+    r[2] = v.z;
+    r[3] = v.w;
 }
-__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc)
+// Consecutive 32-bit columns of the warp's 32 lanes from registers.
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16(taddr, r); }
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[8])
 {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 
 // Instruction descriptor of the block-scaled kinds: scale ids [4,6) (B) and [29,31) (A), A format [7,10),
@@ -190,15 +204,14 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         prefetch_map(&maps.a128);
         for (int i = 0; i < P::kStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 2);                      // codes and scales
-            mbar_init(smem_u32(&sh.sf_full[i]), 1);
+            mbar_init(smem_u32(&sh.sf_full[i]), 4);
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
         for (int i = 0; i < P::kAccs; ++i) {
             mbar_init(smem_u32(&sh.acc_full[i]), 1);
             mbar_init(smem_u32(&sh.acc_empty[i]), 8);
         }
-        mbar_init(smem_u32(&sh.drain[0]), 1);
-        mbar_init(smem_u32(&sh.drain[1]), 1);
+        mbar_init(smem_u32(&sh.drain), 1);
         sh.abort = 0;
         fence_mbar_init();
     }
@@ -354,54 +367,55 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             }
         }
         if (*abort) {
-            mma_commit(smem_u32(&sh.drain[0]));
-            mbar_wait(smem_u32(&sh.drain[0]), 0, 1 << 20, nullptr);
+            mma_commit(smem_u32(&sh.drain));
+            mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
         }
-    } else if (warp == 3 && lane == 0) {
-        // ---- scales into tensor memory
+    } else if (warp >= 4 && warp < 8) {
+        // ---- scales from shared into tensor memory, a quarter of the lanes each: lane i of every quarter
+        // holds the scales of rows i, 32 + i, 64 + i and 96 + i of a tile, its 16 bytes
         int st = 0;
         uint32_t ph = 0;
         bool ok = true;
+        const uint32_t sf0 = tmem + P::kAccs * BN + ((uint32_t)((warp & 3) * 32) << 16);
         for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
             for (int ks = 0; ks < n_steps; ++ks) {
-                if (!mbar_wait(smem_u32(&sh.full[st]), ph, a.wait_limit, abort)) {
-                    fail();
-                    ok = false;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.full[st]), ph, a.wait_limit, abort));
+                if (!ok) {
+                    if (lane == 0) fail();
                     break;
                 }
-                tc_fence_after();
-                const uint32_t sfa_s = smem0 + st * P::kStageBytes + P::kABytes + P::kBBytes, sfb_s = sfa_s + P::kSfaBytes;
-                const uint32_t sfa = tmem + P::kAccs * BN + st * P::kSfCols, sfb = sfa + 4 * P::kTilesK;
+                const uint4 *sfa_s = reinterpret_cast<const uint4 *>(smem + st * P::kStageBytes + P::kABytes + P::kBBytes) + lane;
+                const uint4 *sfb_s = sfa_s + P::kSfaBytes / 16;
+                uint32_t ua[4 * P::kTilesK], ub[4 * P::kTilesK * P::kChunks];
 #pragma unroll
                 for (int j = 0; j < P::kTilesK; ++j) {
-                    tmem_cp_scales(sfa + 4 * j, desc_scales(sfa_s + j * kScaleTile));
+                    set4(ua + 4 * j, sfa_s[j * (kScaleTile / 16)]);
 #pragma unroll
                     for (int c = 0; c < P::kChunks; ++c)
-                        tmem_cp_scales(sfb + 4 * (P::kChunks * j + c), desc_scales(sfb_s + (c * P::kTilesK + j) * kScaleTile));
+                        set4(ub + 4 * (P::kChunks * j + c), sfb_s[(c * P::kTilesK + j) * (kScaleTile / 16)]);
                 }
-                mma_commit(smem_u32(&sh.sf_full[st]));
+                tmem_store(sf0 + st * P::kSfCols, ua);
+                tmem_store(sf0 + st * P::kSfCols + 4 * P::kTilesK, ub);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&sh.sf_full[st]));
                 if (++st == P::kStages) {
                     st = 0;
                     ph ^= 1;
                 }
             }
         }
-        if (*abort) {
-            mma_commit(smem_u32(&sh.drain[1]));
-            mbar_wait(smem_u32(&sh.drain[1]), 0, 1 << 20, nullptr);
-        }
-    } else if (warp >= 4) {
+    } else if (warp >= 8) {
         // ---- accumulators to outputs
         // two warps share a quarter of the rows, each with half of the tile's output columns
         constexpr int kCols = P::kOutN / 2;
-        const int quad = warp & 3, half = (warp - 4) >> 2;
+        const int quad = warp & 3, half = (warp - 8) >> 2;
         int acc = 0;
         uint32_t aph = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
             const Tile t = tile_at(a, sh, tile, n_tiles);
-            bool ok = true;
-            if (lane == 0) ok = mbar_wait(smem_u32(&sh.acc_full[acc]), aph, a.wait_limit, abort);
-            if (!__shfl_sync(0xFFFFFFFFu, (int)ok, 0)) {
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.acc_full[acc]), aph, a.wait_limit, abort))) {
                 if (lane == 0) fail();
                 break;
             }
