@@ -126,19 +126,19 @@ __host__ __device__ constexpr uint32_t idesc_scaled(uint32_t n, uint32_t sf_id)
 }
 template <int FMT>
 __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
-                                           uint32_t sfb, uint32_t accumulate)
+                                           uint32_t sfb, uint32_t accumulate, uint32_t issue)
 {
     if (FMT == MOE_SCALED_NVFP4)
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(issue)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+            "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(issue)
             : "memory");
 }
 
@@ -191,7 +191,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     __shared__ Shared sh;
     uint8_t *smem = align_smem_1024(smem_raw);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int n_tiles = (a.N + P::kOutN - 1) / P::kOutN, n_steps = (a.K + P::kStepK - 1) / P::kStepK;
     const int ct = scaled_col_tiles(FMT, a.K);
     const int w_row_tiles = (a.N + kScaleRows - 1) / kScaleRows;      // scale row tiles of a matrix
@@ -249,8 +249,8 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = sh.tmem;
-    const int total = sh.first[a.G] * n_tiles;
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem, 0);
+    const int total = __shfl_sync(0xFFFFFFFFu, sh.first[a.G] * n_tiles, 0);
     volatile int *abort = &sh.abort;
     const uint32_t smem0 = smem_u32(smem);
     auto fail = [&]() {
@@ -258,48 +258,51 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         *abort = 1;
     };
 
-    if ((warp == 0 || warp == 2) && lane == 0) {
+    // A role's warp walks its loop as a whole and only the issuing instructions are one lane's, so that loop
+    // counters, addresses and descriptors stay in uniform registers: with the loop itself in one lane's
+    // branch a step's issue took 750 cycles, twice its products.
+    if (warp == 0 || warp == 2) {
         // ---- copies: warp 0 the codes, warp 2 the scales
+        const bool leader = elect_one();
         int st = 0, issued = 0;
         uint32_t ph = 0;
         bool ok = true;
         for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
             const Tile t = tile_at(a, sh, tile, n_tiles);
-            const int n0 = t.nt * P::kOutN;
+            const int n0 = t.nt * P::kOutN, wrow = t.g * a.N + n0;
             const bool second = P::kChunks == 2 && (DUAL || n0 / kScaleRows + 1 < w_row_tiles);
+            const int boxes = t.rows > 96 ? 4 : (t.rows + 31) / 32;
+            const size_t row = (size_t)ct * kScaleTile, wt = (size_t)t.g * w_row_tiles + n0 / kScaleRows;
+            const uint8_t *pa = a.a_scales + t.srow_tile * row, *pb = a.w_scales[0] + wt * row;
+            const uint8_t *pc = a.w_scales[DUAL ? 1 : 0] + (DUAL ? wt : wt + 1) * row;
             for (int ks = 0; ks < n_steps; ++ks) {
-                if (!mbar_wait(smem_u32(&sh.empty[st]), ph ^ 1, a.wait_limit, abort)) {
-                    fail();
-                    ok = false;
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.empty[st]), ph ^ 1, a.wait_limit, abort));
+                if (!ok) {
+                    if (leader) fail();
                     break;
                 }
                 const uint32_t base = smem0 + st * P::kStageBytes, bar = smem_u32(&sh.full[st]);
                 if (warp == 0) {
-                    const int boxes = t.rows > 96 ? 4 : (t.rows + 31) / 32;
-                    mbar_arrive_expect_tx(bar, boxes * 32 * kStepBytes + P::kBTxBytes);
-                    // x in the map's elements: bytes, or 4-bit codes for the widened weights
-                    const int xa = ks * kStepBytes, xw = P::kNv ? ks * kStepBytes : ks * P::kStepK;
-                    if (DUAL) {
-                        tma_load_2d(base + P::kABytes, &maps.w[0], xw, t.g * a.N + n0, bar);
-                        tma_load_2d(base + P::kABytes + P::kBBytes / 2, &maps.w[1], xw, t.g * a.N + n0, bar);
-                    } else {
-                        tma_load_2d(base + P::kABytes, &maps.w[0], xw, t.g * a.N + n0, bar);
+                    if (leader) {
+                        mbar_arrive_expect_tx(bar, boxes * 32 * kStepBytes + P::kBTxBytes);
+                        // x in the map's elements: bytes, or 4-bit codes for the widened weights
+                        const int xa = ks * kStepBytes, xw = P::kNv ? ks * kStepBytes : ks * P::kStepK;
+                        tma_load_2d(base + P::kABytes, &maps.w[0], xw, wrow, bar);
+                        if (DUAL) tma_load_2d(base + P::kABytes + P::kBBytes / 2, &maps.w[1], xw, wrow, bar);
+                        if (boxes == 4)
+                            tma_load_2d(base, &maps.a128, xa, t.row0, bar);
+                        else
+                            for (int i = 0; i < boxes; ++i)
+                                tma_load_2d(base + i * 32 * kStepBytes, &maps.a32, xa, t.row0 + 32 * i, bar);
                     }
-                    if (boxes == 4)
-                        tma_load_2d(base, &maps.a128, xa, t.row0, bar);
-                    else
-                        for (int i = 0; i < boxes; ++i)
-                            tma_load_2d(base + i * 32 * kStepBytes, &maps.a32, xa, t.row0 + 32 * i, bar);
-                } else {
-                    const int nt = min(P::kTilesK, ct - ks * P::kTilesK), bytes = nt * kScaleTile;
+                } else if (leader) {
+                    const int bytes = min(P::kTilesK, ct - ks * P::kTilesK) * kScaleTile;
                     const uint32_t sfa = base + P::kABytes + P::kBBytes, sfb = sfa + P::kSfaBytes;
+                    const size_t k0 = (size_t)ks * P::kTilesK * kScaleTile;
                     mbar_arrive_expect_tx(bar, bytes * (second ? 3 : 2));
-                    const size_t k0 = (size_t)ks * P::kTilesK * kScaleTile, row = (size_t)ct * kScaleTile;
-                    const size_t wt = (size_t)t.g * w_row_tiles + n0 / kScaleRows;
-                    bulk_load(sfb, a.w_scales[0] + wt * row + k0, bytes, bar);
-                    if (second)
-                        bulk_load(sfb + P::kSfbBytes / 2, a.w_scales[DUAL ? 1 : 0] + (DUAL ? wt : wt + 1) * row + k0, bytes, bar);
-                    bulk_load(sfa, a.a_scales + t.srow_tile * row + k0, bytes, bar);
+                    bulk_load(sfb, pb + k0, bytes, bar);
+                    if (second) bulk_load(sfb + P::kSfbBytes / 2, pc + k0, bytes, bar);
+                    bulk_load(sfa, pa + k0, bytes, bar);
                 }
                 ++issued;
                 if (++st == P::kStages) {
@@ -316,58 +319,56 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             }
             mbar_wait(smem_u32(&sh.full[st]), ph, 1 << 20, nullptr);
         }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
         // ---- MMAs
+        const uint32_t leader = elect_one();
         int st = 0, acc = 0;
         uint32_t ph = 0, aph = 0;
         bool ok = true;
         const uint32_t sf0 = tmem + P::kAccs * BN;
         for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-            const Tile t = tile_at(a, sh, tile, n_tiles);
             // columns of the first weight row inside its scale row tile (32 rows a column)
-            const uint32_t sub = (uint32_t)(t.nt * P::kOutN % kScaleRows) / 32;
-            if (!mbar_wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1, a.wait_limit, abort)) {
-                fail();
-                break;
-            }
+            const uint32_t sub = P::kOutN % kScaleRows ? (uint32_t)(tile % n_tiles * P::kOutN % kScaleRows) / 32 : 0;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1, a.wait_limit, abort));
             tc_fence_after();
             const uint32_t d = tmem + acc * BN;
-            for (int ks = 0; ks < n_steps; ++ks) {
-                if (!mbar_wait(smem_u32(&sh.full[st]), ph, a.wait_limit, abort) ||
-                    !mbar_wait(smem_u32(&sh.sf_full[st]), ph, a.wait_limit, abort)) {
-                    fail();
-                    ok = false;
-                    break;
-                }
+            for (int ks = 0; ok && ks < n_steps; ++ks) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.sf_full[st]), ph, a.wait_limit, abort));
+                if (!ok) break;
                 tc_fence_after();
                 const uint32_t base = smem0 + st * P::kStageBytes;
-                const uint32_t sfa = sf0 + st * P::kSfCols, sfb = sfa + 4 * P::kTilesK;
+                const uint32_t sfa = sf0 + st * P::kSfCols, sfb = sfa + 4 * P::kTilesK + sub;
                 const uint64_t ad = desc_sw128(base), bd = desc_sw128(base + P::kABytes);
-                const int kk = min(4, (a.K - ks * P::kStepK) / (P::kStepK / 4));
+                const int kk = (a.K - ks * P::kStepK) / (P::kStepK / 4);          // instructions left along K
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    if (j >= kk) break;
-                    const uint32_t id = idesc_scaled<FMT>(P::kMmaN, P::kNv ? 0 : j), go = ks > 0 || j > 0;
-                    const uint32_t sa = sfa + (P::kNv ? 4 * j : 0), sb = sfb + (P::kNv ? 4 * P::kChunks * j : 0) + sub;
                     // 32 bytes along K inside the swizzle atom
-                    mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, id, sa, sb, go);
+                    const uint32_t id = idesc_scaled<FMT>(P::kMmaN, P::kNv ? 0 : j), go = ks > 0 || j > 0;
+                    const uint32_t sa = sfa + (P::kNv ? 4 * j : 0), sb = sfb + (P::kNv ? 4 * P::kChunks * j : 0);
+                    const uint32_t on = leader & (uint32_t)(j < kk);
+                    mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, id, sa, sb, go, on);
                     if (P::kMmaN != BN)
-                        mma_scaled<FMT>(d + P::kMmaN, ad + 2 * j, bd + 2 * j + (P::kMmaN * kStepBytes >> 4), id, sa, sb + 4, go);
+                        mma_scaled<FMT>(d + P::kMmaN, ad + 2 * j, bd + 2 * j + (P::kMmaN * kStepBytes >> 4), id, sa, sb + 4, go, on);
                 }
-                mma_commit(smem_u32(&sh.empty[st]));
+                if (leader) mma_commit(smem_u32(&sh.empty[st]));
                 if (++st == P::kStages) {
                     st = 0;
                     ph ^= 1;
                 }
             }
-            mma_commit(smem_u32(&sh.acc_full[acc]));
+            if (!ok) break;
+            if (leader) mma_commit(smem_u32(&sh.acc_full[acc]));
             if (++acc == P::kAccs) {
                 acc = 0;
                 aph ^= 1;
             }
         }
-        if (*abort) {
-            mma_commit(smem_u32(&sh.drain));
+        if (!ok) {
+            if (leader) {
+                fail();
+                mma_commit(smem_u32(&sh.drain));
+            }
+            __syncwarp();
             mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
         }
     } else if (warp >= 4 && warp < 8) {

@@ -23,6 +23,14 @@ __device__ __forceinline__ uint8_t *align_smem_1024(uint8_t *raw)
     return raw + ((0u - smem_u32(raw)) & 1023u);
 }
 
+// Nonzero in one lane of a whole warp, the same one every time.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
+}
+
 // ------------------------------------------------------------------ mbarrier
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
