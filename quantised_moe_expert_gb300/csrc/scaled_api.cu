@@ -7,6 +7,7 @@ namespace {
 
 constexpr long long kWaitPolls = 1ll << 20;   // bound of every wait inside a kernel, about a second
 constexpr int kMaxRows = 1 << 24;
+constexpr int kMaxProductRows = 1 << 21;      // start rows share a word with their group in the kernels' table
 constexpr int kMaxGroups = 1024;              // with N <= 2^20 a stack's rows stay 32-bit copy coordinates
 constexpr int kMaxRowLength = 16384;          // rows that a kernel keeps in registers whole
 
@@ -38,7 +39,7 @@ int check_ws(void *ws, size_t bytes)
 // Sizes of a product over R rows, N outputs, K inputs and G groups.
 int check_product(int fmt, int R, int N, int K, int G, const int32_t *offsets, int n_unit)
 {
-    if (R < 0 || N <= 0 || K <= 0 || G <= 0 || R > kMaxRows) return MOE_ERR_INVALID_ARG;
+    if (R < 0 || N <= 0 || K <= 0 || G <= 0 || R > kMaxProductRows) return MOE_ERR_INVALID_ARG;
     if (!aligned_or_null(offsets, 4) || (!offsets && G != 1)) return MOE_ERR_INVALID_ARG;
     if (!activation_format(fmt) || G > kMaxGroups) return MOE_ERR_UNSUPPORTED;
     if (K % (fmt == MOE_SCALED_NVFP4 ? 64 : 128) || K > 65536 || N % n_unit || N > (1 << 20)) return MOE_ERR_UNSUPPORTED;

@@ -59,37 +59,42 @@ struct Shared {
     uint64_t full[8], sf_full[8], empty[8], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
-    int warp_sum[kThreads / 32];
-    int first[kMaxGroups + 1];                               // row tiles of the groups before g
+    int bad, groups, row_tiles;                              // malformed offsets; groups with rows; their row tiles
+    int2 warp_sum[kThreads / 32];
+    int2 group[kMaxGroups + 1];                              // those groups: row tiles before it, start << 10 | group
 };
 
 struct Tile {
     int g, row0, rows, srow_tile, nt;                        // rows [row0, row0 + rows), their scale row tile
 };
 
-__device__ __forceinline__ int group_start(const ScaledGemmArgs &a, int g)
-{
-    if (g >= a.G) return a.R;
-    const int o = a.offsets ? __ldg(a.offsets + g) : 0;
-    return min(max(o, 0), a.R);
-}
+constexpr int kGroupBits = 10;
+static_assert(kMaxGroups == 1 << kGroupBits, "the table's packing");
 
 __device__ __forceinline__ Tile tile_at(const ScaledGemmArgs &a, const Shared &sh, int tile, int n_tiles)
 {
     const int mt = tile / n_tiles;
-    int lo = 0, hi = a.G;                                    // first[lo] <= mt < first[hi]
+    Tile t;
+    t.nt = tile - mt * n_tiles;
+    if (!a.offsets) {                                        // one group
+        t.g = 0;
+        t.row0 = mt * kScaleRows;
+        t.rows = min(a.R - t.row0, kScaleRows);
+        t.srow_tile = mt;
+        return t;
+    }
+    int lo = 0, hi = sh.groups;                              // the last entry whose first tile is not past mt
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (sh.first[mid] <= mt) lo = mid;
+        if (sh.group[mid].x <= mt) lo = mid;
         else hi = mid;
     }
-    const int start = group_start(a, lo), end = max(group_start(a, lo + 1), start), m = mt - sh.first[lo];
-    Tile t;
-    t.g = lo;
+    const int2 e = sh.group[lo];
+    const int start = (int)((uint32_t)e.y >> kGroupBits), end = (int)((uint32_t)sh.group[lo + 1].y >> kGroupBits), m = mt - e.x;
+    t.g = e.y & (kMaxGroups - 1);
     t.row0 = start + m * kScaleRows;
     t.rows = min(end - t.row0, kScaleRows);
-    t.srow_tile = group_row_tile(start, lo) + m;
-    t.nt = tile - mt * n_tiles;
+    t.srow_tile = group_row_tile(start, t.g) + m;
     return t;
 }
 
@@ -144,26 +149,14 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t adesc, uint64_t 
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-// 32 accumulator columns of the warp's rows, times s.
-__device__ __forceinline__ void load_cols(uint32_t taddr, float s, float (&v)[32])
-{
-    uint32_t u0[16], u1[16];
-    tmem_ld16(taddr, u0);
-    tmem_ld16(taddr + 16, u1);
-    tmem_ld_wait();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        v[i] = __uint_as_float(u0[i]) * s;
-        v[16 + i] = __uint_as_float(u1[i]) * s;
-    }
-}
-
-// The first n (a multiple of 8) of 32 fp32.
-__device__ __forceinline__ void store_f32(float *p, const float (&v)[32], int n)
+// 16 accumulators times s, as fp32: the first n (a multiple of 8).
+__device__ __forceinline__ void store_f32(float *p, const uint32_t (&v)[16], float s, int n)
 {
 #pragma unroll
-    for (int i = 0; i < 32; i += 4)
-        if (i < n) *reinterpret_cast<float4 *>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    for (int i = 0; i < 16; i += 4)
+        if (i < n)
+            *reinterpret_cast<float4 *>(p + i) = make_float4(__uint_as_float(v[i]) * s, __uint_as_float(v[i + 1]) * s,
+                                                             __uint_as_float(v[i + 2]) * s, __uint_as_float(v[i + 3]) * s);
 }
 
 // The first n (a multiple of 8) of 2 W bf16.  Whole 32-byte sectors a lane where the row allows it.
@@ -213,44 +206,66 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         }
         mbar_init(smem_u32(&sh.drain), 1);
         sh.abort = 0;
+        sh.bad = 0;
+        sh.row_tiles = (a.R + kScaleRows - 1) / kScaleRows;
         fence_mbar_init();
     }
     if (warp == 3) {
         tmem_alloc(smem_u32(&sh.tmem), 512);
         tmem_relinquish();
     }
+    __syncthreads();
     pdl_wait();
-    // row tiles before each group: every thread takes a run of groups
-    {
-        const int per = (a.G + kThreads - 1) / kThreads, g0 = min((int)threadIdx.x * per, a.G), g1 = min(g0 + per, a.G);
-        int n = 0;
-        for (int g = g0; g < g1; ++g) {
-            const int s = group_start(a, g), e = group_start(a, g + 1);
-            if (e < s || (a.offsets && __ldg(a.offsets + g) != s)) record_status(a.status, MOE_ERR_DEVICE);
-            n += (max(e - s, 0) + kScaleRows - 1) / kScaleRows;
-        }
-        int incl = n;
+    if (a.offsets) {
+        // the table of groups with rows: each thread has up to two neighbouring groups, whose tiles and
+        // whose number it scans with the block
+        constexpr int kPer = kMaxGroups / kThreads;
+        const int g0 = threadIdx.x * kPer;
+        int o[kPer + 1];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-            if (lane >= o) incl += v;
+        for (int i = 0; i <= kPer; ++i) o[i] = g0 + i < a.G ? __ldg(a.offsets + g0 + i) : a.R;
+        int2 n = make_int2(0, 0);
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (o[i] < 0 || o[i] > a.R || o[i + 1] < o[i]) sh.bad = 1;
+            n.x += (max(o[i + 1] - o[i], 0) + kScaleRows - 1) / kScaleRows;
+            n.y += o[i + 1] > o[i];
+        }
+        int2 incl = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int x = __shfl_up_sync(0xFFFFFFFFu, incl.x, d), y = __shfl_up_sync(0xFFFFFFFFu, incl.y, d);
+            if (lane >= d) {
+                incl.x += x;
+                incl.y += y;
+            }
         }
         if (lane == 31) sh.warp_sum[warp] = incl;
         __syncthreads();
-        int base = incl - n;
-        for (int w = 0; w < warp; ++w) base += sh.warp_sum[w];
-        for (int g = g0; g < g1; ++g) {
-            sh.first[g] = base;
-            const int s = group_start(a, g), e = group_start(a, g + 1);
-            base += (max(e - s, 0) + kScaleRows - 1) / kScaleRows;
+        int2 base = make_int2(incl.x - n.x, incl.y - n.y);
+        for (int w = 0; w < warp; ++w) {
+            base.x += sh.warp_sum[w].x;
+            base.y += sh.warp_sum[w].y;
         }
-        if (g1 == a.G) sh.first[a.G] = base;                         // the threads past the last group agree
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (o[i + 1] <= o[i]) continue;
+            sh.group[base.y] = make_int2(base.x, o[i] << kGroupBits | (g0 + i));
+            base.x += (o[i + 1] - o[i] + kScaleRows - 1) / kScaleRows;
+            base.y += 1;
+        }
+        if (threadIdx.x == kThreads - 1) {
+            sh.groups = base.y;
+            sh.row_tiles = sh.bad ? 0 : base.x;
+            sh.group[base.y] = make_int2(base.x, (int)((uint32_t)a.R << kGroupBits));
+            if (sh.bad) record_status(a.status, MOE_ERR_DEVICE);
+        }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem, 0);
-    const int total = __shfl_sync(0xFFFFFFFFu, sh.first[a.G] * n_tiles, 0);
+    const int total = __shfl_sync(0xFFFFFFFFu, sh.row_tiles * n_tiles, 0);
     volatile int *abort = &sh.abort;
     const uint32_t smem0 = smem_u32(smem);
     auto fail = [&]() {
@@ -261,6 +276,8 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     // A role's warp walks its loop as a whole and only the issuing instructions are one lane's, so that loop
     // counters, addresses and descriptors stay in uniform registers: with the loop itself in one lane's
     // branch a step's issue took 750 cycles, twice its products.
+    // registers: 512 x 128 at launch, redistributed by warpgroup to 2 x 80 and 2 x 176 (the same total)
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     if (warp == 0 || warp == 2) {
         // ---- copies: warp 0 the codes, warp 2 the scales
         const bool leader = elect_one();
@@ -374,6 +391,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     } else if (warp >= 4 && warp < 8) {
         // ---- scales from shared into tensor memory, a quarter of the lanes each: lane i of every quarter
         // holds the scales of rows i, 32 + i, 64 + i and 96 + i of a tile, its 16 bytes
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         int st = 0;
         uint32_t ph = 0;
         bool ok = true;
@@ -408,6 +426,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             }
         }
     } else if (warp >= 8) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         // ---- accumulators to outputs
         // two warps share a quarter of the rows, each with half of the tile's output columns
         constexpr int kCols = P::kOutN / 2;
@@ -427,6 +446,8 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             const size_t row = (size_t)t.row0 + r;
             const float rs = live && a.a_row_scale ? __ldg(a.a_row_scale + row) : 1.0f;
             const float s0 = rs * (a.alpha[0] ? __ldg(a.alpha[0] + t.g) : 1.0f);
+            // the accumulators go to registers and are free for the next tile's products before anything is
+            // computed from them or stored
             auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
@@ -435,30 +456,41 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             if (!any) {
                 release();
             } else if (!DUAL && a.y_f32) {
-#pragma unroll 1
-                for (int c = 0; c < kCols; c += 32) {
-                    float v[32];
-                    load_cols(d + c, s0, v);
-                    if (live) store_f32(static_cast<float *>(a.y) + row * a.N + col0 + c, v, a.N - col0 - c);
-                }
+                uint32_t u[kCols / 16][16];
+#pragma unroll
+                for (int i = 0; i < kCols / 16; ++i) tmem_ld16(d + 16 * i, u[i]);
+                tmem_ld_wait();
                 release();
+#pragma unroll
+                for (int i = 0; i < kCols / 16; ++i)
+                    if (live) store_f32(static_cast<float *>(a.y) + row * a.N + col0 + 16 * i, u[i], s0, a.N - col0 - 16 * i);
             } else if (!DUAL) {
-                // the accumulators go to registers, rounded, before anything is stored: the next tile's
-                // products start while this one's outputs are on their way
+                constexpr int kBatch = kCols < 64 ? kCols : 64;
                 uint32_t w[kCols / 2];
 #pragma unroll
-                for (int c = 0; c < kCols; c += 32) {
-                    float v[32];
-                    load_cols(d + c, s0, v);
+                for (int c = 0; c < kCols; c += kBatch) {
+                    uint32_t u[kBatch / 16][16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    for (int i = 0; i < kBatch / 16; ++i) tmem_ld16(d + c + 16 * i, u[i]);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < kBatch / 2; ++i) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(u[i / 8][2 * i % 16]) * s0,
+                                                                       __uint_as_float(u[i / 8][2 * i % 16 + 1]) * s0);
                         w[c / 2 + i] = *reinterpret_cast<const uint32_t *>(&b);
                     }
                 }
                 release();
                 if (live) store_bf16<kCols / 2>(static_cast<uint16_t *>(a.y) + row * a.N + col0, w, a.N - col0);
             } else {
+                uint32_t u[kCols / 16][16], u2[kCols / 16][16];          // gate and up products
+#pragma unroll
+                for (int i = 0; i < kCols / 16; ++i) {
+                    tmem_ld16(d + 16 * i, u[i]);
+                    tmem_ld16(d + BN / 2 + 16 * i, u2[i]);
+                }
+                tmem_ld_wait();
+                release();
                 const float s1 = rs * (a.alpha[1] ? __ldg(a.alpha[1] + t.g) : 1.0f);
                 float ginv = 1.0f;
                 if (P::kNv) ginv = __fdiv_rn(1.0f, __ldg(a.h_gscale + t.g));
@@ -469,13 +501,9 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
 #pragma unroll
                 for (int c = 0; c < kCols; c += 32) {
                     float h[32];
-                    {
-                        float u[32];
-                        load_cols(d + c, s0, h);
-                        load_cols(d + BN / 2 + c, s1, u);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) h[i] = silu(h[i]) * u[i];
-                    }
+                    for (int i = 0; i < 32; ++i)
+                        h[i] = silu(__uint_as_float(u[(c + i) / 16][i % 16]) * s0) * (__uint_as_float(u2[(c + i) / 16][i % 16]) * s1);
 #pragma unroll
                     for (int i0 = 0; i0 < 32; i0 += kBlk) {
                         uint32_t m = 0;
@@ -504,7 +532,6 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                         }
                     }
                 }
-                release();
                 if (live) {
                     uint4 *p = reinterpret_cast<uint4 *>(a.h_codes + (P::kNv ? (row * a.N + col0) / 2 : row * a.N + col0));
 #pragma unroll
