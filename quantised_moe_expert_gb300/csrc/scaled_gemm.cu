@@ -13,11 +13,11 @@
 // the rows present are copied), weights the N = BN operand, so that a thread of the epilogue holds
 // consecutive outputs of one row: whole blocks of h for its scale, whole sectors of y.
 //
-// One CTA per SM walks over the tiles: warp 0 copies codes (TMA), warp 2 copies scale tiles (bulk), warps
-// 4-7 move a step's scales from shared into tensor memory, warp 1 issues its MMAs, warps 8-15 read the
-// accumulators and write.  Every stage has its own scale columns, so a stage's barriers also guard them.
-// The scales go through registers (tcgen05.st): a tcgen05.cp of a 512-byte tile costs its thread and the
-// tensor pipe 60 to 90 cycles, twelve of them more than the step's MMAs.
+// One CTA per SM walks over the tiles: warp 0 copies codes (TMA), warp 2 copies scale tiles (bulk), warp 1
+// moves a step's scales from shared into tensor memory (tcgen05.cp, in order with the MMAs behind it) and
+// issues its MMAs, warps 4-11 read the accumulators and write.  Every stage has its own scale columns, so
+// a stage's barriers also guard them.  (Scales through registers, tcgen05.st by four more warps, which
+// read every tile four times from shared memory: 8192 x 8192 x 4096 117 us against 112 us.)
 #include <stdlib.h>
 #include "scaled.cuh"
 #include "tc_ptx.cuh"
@@ -28,7 +28,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 384;
 constexpr int kMaxGroups = 1024;
 constexpr int kStepBytes = 128;                    // bytes of a K step in a row of codes (as in shared memory)
 
@@ -56,7 +56,7 @@ struct Maps {
 };
 
 struct Shared {
-    uint64_t full[8], sf_full[8], empty[8], acc_full[2], acc_empty[2], drain;
+    uint64_t full[8], empty[8], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
     int abort;
     int bad, groups, row_tiles;                              // malformed offsets; groups with rows; their row tiles
@@ -98,26 +98,16 @@ __device__ __forceinline__ Tile tile_at(const ScaledGemmArgs &a, const Shared &s
     return t;
 }
 
-__device__ __forceinline__ void set4(uint32_t *r, uint4 v)
+// Scale tiles in shared memory as tcgen05.cp takes them: 8 rows x 16 bytes cores, 128 bytes apart, no swizzle.
+__device__ __forceinline__ uint64_t desc_scales(uint32_t addr)
 {
-    r[0] = v.x;
-    r[1] = v.y;
-    r[2] = v.z;
-    r[3] = v.w;
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
 }
-// Consecutive 32-bit columns of the warp's 32 lanes from registers.
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[32]) { tmem_st32(taddr, r); }
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[16]) { tmem_st16(taddr, r); }
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[8])
+// One scale tile from shared memory to four columns of all four quarters of the lanes.
+__device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc, uint32_t issue)
 {
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(r[0]),
-                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-                 : "memory");
-}
-__device__ __forceinline__ void tmem_store(uint32_t taddr, const uint32_t (&r)[4])
-{
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
-                 "r"(r[2]), "r"(r[3])
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+                 "l"(desc), "r"(issue)
                  : "memory");
 }
 
@@ -197,7 +187,6 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         prefetch_map(&maps.a128);
         for (int i = 0; i < P::kStages; ++i) {
             mbar_init(smem_u32(&sh.full[i]), 2);                      // codes and scales
-            mbar_init(smem_u32(&sh.sf_full[i]), 4);
             mbar_init(smem_u32(&sh.empty[i]), 1);
         }
         for (int i = 0; i < P::kAccs; ++i) {
@@ -217,9 +206,9 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     __syncthreads();
     pdl_wait();
     if (a.offsets) {
-        // the table of groups with rows: each thread has up to two neighbouring groups, whose tiles and
+        // the table of groups with rows: each thread has a few neighbouring groups, whose tiles and
         // whose number it scans with the block
-        constexpr int kPer = kMaxGroups / kThreads;
+        constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
         const int g0 = threadIdx.x * kPer;
         int o[kPer + 1];
 #pragma unroll
@@ -276,8 +265,8 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     // A role's warp walks its loop as a whole and only the issuing instructions are one lane's, so that loop
     // counters, addresses and descriptors stay in uniform registers: with the loop itself in one lane's
     // branch a step's issue took 750 cycles, twice its products.
-    // registers: 512 x 128 at launch, redistributed by warpgroup to 2 x 80 and 2 x 176 (the same total)
-    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // registers: 384 x 168 at launch, redistributed by warpgroup to 104 and 2 x 200 (the same total)
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 0 || warp == 2) {
         // ---- copies: warp 0 the codes, warp 2 the scales
         const bool leader = elect_one();
@@ -350,11 +339,20 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             tc_fence_after();
             const uint32_t d = tmem + acc * BN;
             for (int ks = 0; ok && ks < n_steps; ++ks) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.sf_full[st]), ph, a.wait_limit, abort));
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.full[st]), ph, a.wait_limit, abort));
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t base = smem0 + st * P::kStageBytes;
                 const uint32_t sfa = sf0 + st * P::kSfCols, sfb = sfa + 4 * P::kTilesK + sub;
+                const uint32_t sfa_s = base + P::kABytes + P::kBBytes, sfb_s = sfa_s + P::kSfaBytes;
+#pragma unroll
+                for (int j = 0; j < P::kTilesK; ++j) {
+                    tmem_cp_scales(sfa + 4 * j, desc_scales(sfa_s + j * kScaleTile), leader);
+#pragma unroll
+                    for (int c = 0; c < P::kChunks; ++c)
+                        tmem_cp_scales(sfa + 4 * (P::kTilesK + P::kChunks * j + c),
+                                       desc_scales(sfb_s + (c * P::kTilesK + j) * kScaleTile), leader);
+                }
                 const uint64_t ad = desc_sw128(base), bd = desc_sw128(base + P::kABytes);
                 const int kk = (a.K - ks * P::kStepK) / (P::kStepK / 4);          // instructions left along K
 #pragma unroll
@@ -388,49 +386,12 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             __syncwarp();
             mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
         }
-    } else if (warp >= 4 && warp < 8) {
-        // ---- scales from shared into tensor memory, a quarter of the lanes each: lane i of every quarter
-        // holds the scales of rows i, 32 + i, 64 + i and 96 + i of a tile, its 16 bytes
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
-        int st = 0;
-        uint32_t ph = 0;
-        bool ok = true;
-        const uint32_t sf0 = tmem + P::kAccs * BN + ((uint32_t)((warp & 3) * 32) << 16);
-        for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-            for (int ks = 0; ks < n_steps; ++ks) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.full[st]), ph, a.wait_limit, abort));
-                if (!ok) {
-                    if (lane == 0) fail();
-                    break;
-                }
-                const uint4 *sfa_s = reinterpret_cast<const uint4 *>(smem + st * P::kStageBytes + P::kABytes + P::kBBytes) + lane;
-                const uint4 *sfb_s = sfa_s + P::kSfaBytes / 16;
-                uint32_t ua[4 * P::kTilesK], ub[4 * P::kTilesK * P::kChunks];
-#pragma unroll
-                for (int j = 0; j < P::kTilesK; ++j) {
-                    set4(ua + 4 * j, sfa_s[j * (kScaleTile / 16)]);
-#pragma unroll
-                    for (int c = 0; c < P::kChunks; ++c)
-                        set4(ub + 4 * (P::kChunks * j + c), sfb_s[(c * P::kTilesK + j) * (kScaleTile / 16)]);
-                }
-                tmem_store(sf0 + st * P::kSfCols, ua);
-                tmem_store(sf0 + st * P::kSfCols + 4 * P::kTilesK, ub);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_u32(&sh.sf_full[st]));
-                if (++st == P::kStages) {
-                    st = 0;
-                    ph ^= 1;
-                }
-            }
-        }
-    } else if (warp >= 8) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    } else if (warp >= 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---- accumulators to outputs
         // two warps share a quarter of the rows, each with half of the tile's output columns
         constexpr int kCols = P::kOutN / 2;
-        const int quad = warp & 3, half = (warp - 8) >> 2;
+        const int quad = warp & 3, half = (warp - 4) >> 2;
         int acc = 0;
         uint32_t aph = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
