@@ -100,19 +100,28 @@ __device__ __forceinline__ float nvfp4_row_factor(uint32_t amax_bits)
 // first thing) and reads or writes memory only after griddepcontrol.wait, in every block: a successor's
 // set-up (barriers, tensor memory, tensor maps) runs under its predecessor's tail.
 template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args)
+cudaError_t launch_dependent_clusters(void (*kernel)(P...), unsigned grid, unsigned cluster, unsigned block, size_t smem,
+                                      cudaStream_t st, A... args)
 {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(block);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+template <class... P, class... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args)
+{
+    return launch_dependent_clusters(kernel, grid, 1, block, smem, st, args...);
 }
 
 // ---------------------------------------------------------------- kernel arguments

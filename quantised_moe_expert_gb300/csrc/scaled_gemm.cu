@@ -18,7 +18,6 @@
 // issues its MMAs, warps 4-11 read the accumulators and write.  Every stage has its own scale columns, so
 // a stage's barriers also guard them.  (Scales through registers, tcgen05.st by four more warps, which
 // read every tile four times from shared memory: 8192 x 8192 x 4096 117 us against 112 us.)
-#include <stdlib.h>
 #include "scaled.cuh"
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"
@@ -71,6 +70,8 @@ struct Tile {
 constexpr int kGroupBits = 10;
 static_assert(kMaxGroups == 1 << kGroupBits, "the table's packing");
 
+// Tile `tile` of tiles of ROWS rows.
+template <int ROWS>
 __device__ __forceinline__ Tile tile_at(const ScaledGemmArgs &a, const Shared &sh, int tile, int n_tiles)
 {
     const int mt = tile / n_tiles;
@@ -78,9 +79,9 @@ __device__ __forceinline__ Tile tile_at(const ScaledGemmArgs &a, const Shared &s
     t.nt = tile - mt * n_tiles;
     if (!a.offsets) {                                        // one group
         t.g = 0;
-        t.row0 = mt * kScaleRows;
-        t.rows = min(a.R - t.row0, kScaleRows);
-        t.srow_tile = mt;
+        t.row0 = mt * ROWS;
+        t.rows = min(a.R - t.row0, ROWS);
+        t.srow_tile = mt * (ROWS / kScaleRows);
         return t;
     }
     int lo = 0, hi = sh.groups;                              // the last entry whose first tile is not past mt
@@ -92,10 +93,58 @@ __device__ __forceinline__ Tile tile_at(const ScaledGemmArgs &a, const Shared &s
     const int2 e = sh.group[lo];
     const int start = (int)((uint32_t)e.y >> kGroupBits), end = (int)((uint32_t)sh.group[lo + 1].y >> kGroupBits), m = mt - e.x;
     t.g = e.y & (kMaxGroups - 1);
-    t.row0 = start + m * kScaleRows;
-    t.rows = min(end - t.row0, kScaleRows);
-    t.srow_tile = group_row_tile(start, t.g) + m;
+    t.row0 = start + m * ROWS;
+    t.rows = min(end - t.row0, ROWS);
+    t.srow_tile = group_row_tile(start, t.g) + m * (ROWS / kScaleRows);
     return t;
+}
+
+// The table of groups with rows: each thread has a few neighbouring groups, whose tiles of ROWS rows and
+// whose number it scans with the block.  Every thread takes part.
+template <int ROWS>
+__device__ __forceinline__ void build_table(const ScaledGemmArgs &a, Shared &sh, int warp, int lane)
+{
+    constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
+    const int g0 = threadIdx.x * kPer;
+    int o[kPer + 1];
+#pragma unroll
+    for (int i = 0; i <= kPer; ++i) o[i] = g0 + i < a.G ? __ldg(a.offsets + g0 + i) : a.R;
+    int2 n = make_int2(0, 0);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (o[i] < 0 || o[i] > a.R || o[i + 1] < o[i]) sh.bad = 1;
+        n.x += (max(o[i + 1] - o[i], 0) + ROWS - 1) / ROWS;
+        n.y += o[i + 1] > o[i];
+    }
+    int2 incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, incl.x, d), y = __shfl_up_sync(0xFFFFFFFFu, incl.y, d);
+        if (lane >= d) {
+            incl.x += x;
+            incl.y += y;
+        }
+    }
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    __syncthreads();
+    int2 base = make_int2(incl.x - n.x, incl.y - n.y);
+    for (int w = 0; w < warp; ++w) {
+        base.x += sh.warp_sum[w].x;
+        base.y += sh.warp_sum[w].y;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (o[i + 1] <= o[i]) continue;
+        sh.group[base.y] = make_int2(base.x, o[i] << kGroupBits | (g0 + i));
+        base.x += (o[i + 1] - o[i] + ROWS - 1) / ROWS;
+        base.y += 1;
+    }
+    if (threadIdx.x == kThreads - 1) {
+        sh.groups = base.y;
+        sh.row_tiles = sh.bad ? 0 : base.x;
+        sh.group[base.y] = make_int2(base.x, (int)((uint32_t)a.R << kGroupBits));
+        if (sh.bad) record_status(a.status, MOE_ERR_DEVICE);
+    }
 }
 
 // Scale tiles in shared memory as tcgen05.cp takes them: 8 rows x 16 bytes cores, 128 bytes apart, no swizzle.
@@ -103,37 +152,39 @@ __device__ __forceinline__ uint64_t desc_scales(uint32_t addr)
 {
     return (uint64_t)((addr >> 4) & 0x3FFFu) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
 }
-// One scale tile from shared memory to four columns of all four quarters of the lanes.
+// One scale tile from shared memory to four columns of all four quarters of the lanes (CG == 2: in both CTAs
+// of the pair, each from its own shared memory).
+template <int CG>
 __device__ __forceinline__ void tmem_cp_scales(uint32_t taddr, uint64_t desc, uint32_t issue)
 {
-    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
-                 "l"(desc), "r"(issue)
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t@q tcgen05.cp.cta_group::%3.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+                 "l"(desc), "r"(issue), "n"(CG)
                  : "memory");
 }
 
 // Instruction descriptor of the block-scaled kinds: scale ids [4,6) (B) and [29,31) (A), A format [7,10),
 // B format [10,13), N >> 3 [17,23), scale format [23] (0 E4M3, 1 E8M0), M >> 4 [24,29).
 template <int FMT>
-__host__ __device__ constexpr uint32_t idesc_scaled(uint32_t n, uint32_t sf_id)
+__host__ __device__ constexpr uint32_t idesc_scaled(uint32_t m, uint32_t n, uint32_t sf_id)
 {
     return (sf_id << 4) | ((FMT == MOE_SCALED_NVFP4 ? 1u : 0u) << 7) | ((FMT == MOE_SCALED_NVFP4 ? 1u : 5u) << 10) |
-           ((n >> 3) << 17) | ((FMT == MOE_SCALED_NVFP4 ? 0u : 1u) << 23) | ((128u >> 4) << 24) | (sf_id << 29);
+           ((n >> 3) << 17) | ((FMT == MOE_SCALED_NVFP4 ? 0u : 1u) << 23) | ((m >> 4) << 24) | (sf_id << 29);
 }
-template <int FMT>
+template <int FMT, int CG>
 __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
                                            uint32_t sfb, uint32_t accumulate, uint32_t issue)
 {
     if (FMT == MOE_SCALED_NVFP4)
         asm volatile(
             "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(issue)
+            "@q tcgen05.mma.cta_group::%8.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(issue), "n"(CG)
             : "memory");
     else
         asm volatile(
             "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(issue)
+            "@q tcgen05.mma.cta_group::%8.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(issue), "n"(CG)
             : "memory");
 }
 
@@ -164,6 +215,41 @@ __device__ __forceinline__ void store_bf16(uint16_t *p, const uint32_t (&w)[W], 
 #pragma unroll
     for (int i = 0; i < W; i += 4)
         if (2 * i < n) *reinterpret_cast<uint4 *>(p + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+}
+
+// COLS accumulator columns of the warp's rows to y; release() once they are in registers.
+template <int COLS, class Release>
+__device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, size_t row, int col0, float s, bool live,
+                                           Release release)
+{
+    if (a.y_f32) {
+        uint32_t u[COLS / 16][16];
+#pragma unroll
+        for (int i = 0; i < COLS / 16; ++i) tmem_ld16(d + 16 * i, u[i]);
+        tmem_ld_wait();
+        release();
+#pragma unroll
+        for (int i = 0; i < COLS / 16; ++i)
+            if (live) store_f32(static_cast<float *>(a.y) + row * a.N + col0 + 16 * i, u[i], s, a.N - col0 - 16 * i);
+        return;
+    }
+    constexpr int kBatch = COLS < 64 ? COLS : 64;
+    uint32_t w[COLS / 2];
+#pragma unroll
+    for (int c = 0; c < COLS; c += kBatch) {
+        uint32_t u[kBatch / 16][16];
+#pragma unroll
+        for (int i = 0; i < kBatch / 16; ++i) tmem_ld16(d + c + 16 * i, u[i]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < kBatch / 2; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(u[i / 8][2 * i % 16]) * s,
+                                                           __uint_as_float(u[i / 8][2 * i % 16 + 1]) * s);
+            w[c / 2 + i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+    }
+    release();
+    if (live) store_bf16<COLS / 2>(static_cast<uint16_t *>(a.y) + row * a.N + col0, w, a.N - col0);
 }
 
 template <int FMT, bool DUAL, int BN>
@@ -205,51 +291,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     }
     __syncthreads();
     pdl_wait();
-    if (a.offsets) {
-        // the table of groups with rows: each thread has a few neighbouring groups, whose tiles and
-        // whose number it scans with the block
-        constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
-        const int g0 = threadIdx.x * kPer;
-        int o[kPer + 1];
-#pragma unroll
-        for (int i = 0; i <= kPer; ++i) o[i] = g0 + i < a.G ? __ldg(a.offsets + g0 + i) : a.R;
-        int2 n = make_int2(0, 0);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (o[i] < 0 || o[i] > a.R || o[i + 1] < o[i]) sh.bad = 1;
-            n.x += (max(o[i + 1] - o[i], 0) + kScaleRows - 1) / kScaleRows;
-            n.y += o[i + 1] > o[i];
-        }
-        int2 incl = n;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int x = __shfl_up_sync(0xFFFFFFFFu, incl.x, d), y = __shfl_up_sync(0xFFFFFFFFu, incl.y, d);
-            if (lane >= d) {
-                incl.x += x;
-                incl.y += y;
-            }
-        }
-        if (lane == 31) sh.warp_sum[warp] = incl;
-        __syncthreads();
-        int2 base = make_int2(incl.x - n.x, incl.y - n.y);
-        for (int w = 0; w < warp; ++w) {
-            base.x += sh.warp_sum[w].x;
-            base.y += sh.warp_sum[w].y;
-        }
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            if (o[i + 1] <= o[i]) continue;
-            sh.group[base.y] = make_int2(base.x, o[i] << kGroupBits | (g0 + i));
-            base.x += (o[i + 1] - o[i] + kScaleRows - 1) / kScaleRows;
-            base.y += 1;
-        }
-        if (threadIdx.x == kThreads - 1) {
-            sh.groups = base.y;
-            sh.row_tiles = sh.bad ? 0 : base.x;
-            sh.group[base.y] = make_int2(base.x, (int)((uint32_t)a.R << kGroupBits));
-            if (sh.bad) record_status(a.status, MOE_ERR_DEVICE);
-        }
-    }
+    if (a.offsets) build_table<kScaleRows>(a, sh, warp, lane);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -274,7 +316,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         uint32_t ph = 0;
         bool ok = true;
         for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-            const Tile t = tile_at(a, sh, tile, n_tiles);
+            const Tile t = tile_at<kScaleRows>(a, sh, tile, n_tiles);
             const int n0 = t.nt * P::kOutN, wrow = t.g * a.N + n0;
             const bool second = P::kChunks == 2 && (DUAL || n0 / kScaleRows + 1 < w_row_tiles);
             const int boxes = t.rows > 96 ? 4 : (t.rows + 31) / 32;
@@ -347,10 +389,10 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 const uint32_t sfa_s = base + P::kABytes + P::kBBytes, sfb_s = sfa_s + P::kSfaBytes;
 #pragma unroll
                 for (int j = 0; j < P::kTilesK; ++j) {
-                    tmem_cp_scales(sfa + 4 * j, desc_scales(sfa_s + j * kScaleTile), leader);
+                    tmem_cp_scales<1>(sfa + 4 * j, desc_scales(sfa_s + j * kScaleTile), leader);
 #pragma unroll
                     for (int c = 0; c < P::kChunks; ++c)
-                        tmem_cp_scales(sfa + 4 * (P::kTilesK + P::kChunks * j + c),
+                        tmem_cp_scales<1>(sfa + 4 * (P::kTilesK + P::kChunks * j + c),
                                        desc_scales(sfb_s + (c * P::kTilesK + j) * kScaleTile), leader);
                 }
                 const uint64_t ad = desc_sw128(base), bd = desc_sw128(base + P::kABytes);
@@ -358,12 +400,12 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     // 32 bytes along K inside the swizzle atom
-                    const uint32_t id = idesc_scaled<FMT>(P::kMmaN, P::kNv ? 0 : j), go = ks > 0 || j > 0;
+                    const uint32_t id = idesc_scaled<FMT>(128, P::kMmaN, P::kNv ? 0 : j), go = ks > 0 || j > 0;
                     const uint32_t sa = sfa + (P::kNv ? 4 * j : 0), sb = sfb + (P::kNv ? 4 * P::kChunks * j : 0);
                     const uint32_t on = leader & (uint32_t)(j < kk);
-                    mma_scaled<FMT>(d, ad + 2 * j, bd + 2 * j, id, sa, sb, go, on);
+                    mma_scaled<FMT, 1>(d, ad + 2 * j, bd + 2 * j, id, sa, sb, go, on);
                     if (P::kMmaN != BN)
-                        mma_scaled<FMT>(d + P::kMmaN, ad + 2 * j, bd + 2 * j + (P::kMmaN * kStepBytes >> 4), id, sa, sb + 4, go, on);
+                        mma_scaled<FMT, 1>(d + P::kMmaN, ad + 2 * j, bd + 2 * j + (P::kMmaN * kStepBytes >> 4), id, sa, sb + 4, go, on);
                 }
                 if (leader) mma_commit(smem_u32(&sh.empty[st]));
                 if (++st == P::kStages) {
@@ -395,7 +437,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         int acc = 0;
         uint32_t aph = 0;
         for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
-            const Tile t = tile_at(a, sh, tile, n_tiles);
+            const Tile t = tile_at<kScaleRows>(a, sh, tile, n_tiles);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.acc_full[acc]), aph, a.wait_limit, abort))) {
                 if (lane == 0) fail();
                 break;
@@ -416,33 +458,8 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             };
             if (!any) {
                 release();
-            } else if (!DUAL && a.y_f32) {
-                uint32_t u[kCols / 16][16];
-#pragma unroll
-                for (int i = 0; i < kCols / 16; ++i) tmem_ld16(d + 16 * i, u[i]);
-                tmem_ld_wait();
-                release();
-#pragma unroll
-                for (int i = 0; i < kCols / 16; ++i)
-                    if (live) store_f32(static_cast<float *>(a.y) + row * a.N + col0 + 16 * i, u[i], s0, a.N - col0 - 16 * i);
-            } else if (!DUAL) {
-                constexpr int kBatch = kCols < 64 ? kCols : 64;
-                uint32_t w[kCols / 2];
-#pragma unroll
-                for (int c = 0; c < kCols; c += kBatch) {
-                    uint32_t u[kBatch / 16][16];
-#pragma unroll
-                    for (int i = 0; i < kBatch / 16; ++i) tmem_ld16(d + c + 16 * i, u[i]);
-                    tmem_ld_wait();
-#pragma unroll
-                    for (int i = 0; i < kBatch / 2; ++i) {
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(u[i / 8][2 * i % 16]) * s0,
-                                                                       __uint_as_float(u[i / 8][2 * i % 16 + 1]) * s0);
-                        w[c / 2 + i] = *reinterpret_cast<const uint32_t *>(&b);
-                    }
-                }
-                release();
-                if (live) store_bf16<kCols / 2>(static_cast<uint16_t *>(a.y) + row * a.N + col0, w, a.N - col0);
+            } else if constexpr (!DUAL) {
+                store_rows<kCols>(a, d, row, col0, s0, live, release);
             } else {
                 uint32_t u[kCols / 16][16], u2[kCols / 16][16];          // gate and up products
 #pragma unroll
@@ -513,19 +530,255 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     if (warp == 3) tmem_dealloc(tmem, 512);
 }
 
+// ------------------------------------------------------------------ a pair of CTAs on one tile
+//
+// Large groups: two SMs share a tile of 256 rows x 256 outputs (cta_group::2).  Each holds the codes of its own
+// 128 rows and of half of the weights, so that a step brings an SM 38 KB in place of 54 KB for the same
+// products, and five stages fit in place of four: the one-CTA kernel waits a third of its time for a refilled
+// stage.  The first CTA issues the products of both; all copies of a stage complete on its barrier, and its
+// commits arrive in both.
+
+template <int FMT>
+struct PairPlan {
+    static constexpr bool kNv = FMT == MOE_SCALED_NVFP4;
+    static constexpr int kStepK = kNv ? 256 : 128, kTilesK = kNv ? 4 : 1;
+    static constexpr int kABytes = 128 * kStepBytes, kBBytes = 128 * kStepBytes;
+    static constexpr int kBTxBytes = kNv ? kBBytes : kBBytes / 2;
+    static constexpr int kSfBytes = kTilesK * kScaleTile;                   // one row tile's scales of a step
+    static constexpr int kStageBytes = kABytes + kBBytes + 3 * kSfBytes;
+    static constexpr int kStages = kNv ? 5 : 6;
+    static constexpr int kSfCols = 4 * kTilesK * 3;
+    static constexpr int kSmem = kStages * kStageBytes + 1024;
+    static_assert(256 + kStages * kSfCols <= 512, "tensor memory");
+};
+constexpr int kPairRows = 256;
+
+struct PairMaps {
+    CUtensorMap a, w, sa, sw;              // codes; scale tiles as rows of 128 words
+};
+
+template <int FMT>
+__global__ void __launch_bounds__(kThreads, 1)
+scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_constant__ PairMaps maps)
+{
+    using P = PairPlan<FMT>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared sh;
+    uint8_t *smem = align_smem_1024(smem_raw);
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = (int)cluster_ctarank(), first_tile = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    const int n_tiles = (a.N + 255) / 256, n_steps = (a.K + P::kStepK - 1) / P::kStepK;
+    const int ct = scaled_col_tiles(FMT, a.K), w_row_tiles = (a.N + kScaleRows - 1) / kScaleRows;
+
+    pdl_trigger();
+    if (threadIdx.x == 0) {
+        prefetch_map(&maps.a);
+        prefetch_map(&maps.w);
+        prefetch_map(&maps.sa);
+        prefetch_map(&maps.sw);
+        for (int i = 0; i < P::kStages; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 2);                      // codes and scales (of both CTAs, in the first)
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+        }
+        mbar_init(smem_u32(&sh.acc_full[0]), 1);
+        mbar_init(smem_u32(&sh.acc_empty[0]), 16);                    // the epilogue warps of both CTAs
+        mbar_init(smem_u32(&sh.drain), 1);
+        sh.abort = 0;
+        sh.bad = 0;
+        sh.row_tiles = (a.R + kPairRows - 1) / kPairRows;
+        fence_mbar_init();
+    }
+    if (warp == 3) {
+        tmem_alloc_pair(smem_u32(&sh.tmem), 512);
+        tmem_relinquish_pair();
+    }
+    __syncthreads();
+    pdl_wait();
+    if (a.offsets) build_table<kPairRows>(a, sh, warp, lane);
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();                                                   // the barriers of both CTAs are there
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem, 0);
+    const int total = __shfl_sync(0xFFFFFFFFu, sh.row_tiles * n_tiles, 0);
+    volatile int *abort = &sh.abort;
+    const uint32_t smem0 = smem_u32(smem);
+    auto fail = [&]() {
+        record_status(a.status, MOE_ERR_TIMEOUT);
+        *abort = 1;
+    };
+
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 0 || warp == 2) {
+        // ---- copies: warp 0 the codes, warp 2 the scales, each CTA its own; they complete on the first CTA's barrier
+        const bool leader = elect_one();
+        int st = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int tile = first_tile; ok && tile < total; tile += stride) {
+            const Tile t = tile_at<kPairRows>(a, sh, tile, n_tiles);
+            const int n0 = t.nt * 256, wrow = t.g * a.N + n0 + rank * 128, arow = t.row0 + rank * 128;
+            const int sa = (t.srow_tile + rank) * ct, sw = (t.g * w_row_tiles + n0 / kScaleRows) * ct;
+            for (int ks = 0; ks < n_steps; ++ks) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.empty[st]), ph ^ 1, a.wait_limit, abort));
+                if (!ok) {
+                    if (leader) fail();
+                    break;
+                }
+                const uint32_t base = smem0 + st * P::kStageBytes, bar = mapa_u32(smem_u32(&sh.full[st]), 0);
+                if (warp == 0) {
+                    if (leader) {
+                        if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[st]), 2 * (P::kABytes + P::kBTxBytes));
+                        tma_load_2d_pair(base + P::kABytes, &maps.w, P::kNv ? ks * kStepBytes : ks * P::kStepK, wrow, bar);
+                        tma_load_2d_pair(base, &maps.a, ks * kStepBytes, arow, bar);
+                    }
+                } else if (leader) {
+                    const uint32_t sf = base + P::kABytes + P::kBBytes;
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[st]), 2 * 3 * P::kSfBytes);
+                    tma_load_2d_pair(sf, &maps.sa, 0, sa + ks * P::kTilesK, bar);
+                    tma_load_2d_pair(sf + P::kSfBytes, &maps.sw, 0, sw + ks * P::kTilesK, bar);
+                    tma_load_2d_pair(sf + 2 * P::kSfBytes, &maps.sw, 0, sw + ct + ks * P::kTilesK, bar);
+                }
+                ++issued;
+                if (++st == P::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        // the newest copy of each stage lands before the pair leaves, whoever gave up
+        for (int i = 0; rank == 0 && i < min(issued, P::kStages); ++i) {
+            if (--st < 0) {
+                st = P::kStages - 1;
+                ph ^= 1;
+            }
+            mbar_wait(smem_u32(&sh.full[st]), ph, 1 << 20, nullptr);
+        }
+    } else if (warp == 1 && rank == 0) {
+        // ---- MMAs of the pair
+        const uint32_t leader = elect_one();
+        int st = 0;
+        uint32_t ph = 0, aph = 0;
+        bool ok = true;
+        const uint32_t sf0 = tmem + 256;
+        for (int tile = first_tile; ok && tile < total; tile += stride) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(smem_u32(&sh.acc_empty[0]), aph ^ 1, a.wait_limit, abort));
+            tc_fence_after();
+            for (int ks = 0; ok && ks < n_steps; ++ks) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(smem_u32(&sh.full[st]), ph, a.wait_limit, abort));
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t base = smem0 + st * P::kStageBytes, sf = base + P::kABytes + P::kBBytes;
+                const uint32_t sfa = sf0 + st * P::kSfCols, sfb = sfa + 4 * P::kTilesK;
+#pragma unroll
+                for (int j = 0; j < P::kTilesK; ++j) {
+                    tmem_cp_scales<2>(sfa + 4 * j, desc_scales(sf + j * kScaleTile), leader);
+                    tmem_cp_scales<2>(sfb + 8 * j, desc_scales(sf + P::kSfBytes + j * kScaleTile), leader);
+                    tmem_cp_scales<2>(sfb + 8 * j + 4, desc_scales(sf + 2 * P::kSfBytes + j * kScaleTile), leader);
+                }
+                const uint64_t ad = desc_sw128(base), bd = desc_sw128(base + P::kABytes);
+                const int kk = (a.K - ks * P::kStepK) / (P::kStepK / 4);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mma_scaled<FMT, 2>(tmem, ad + 2 * j, bd + 2 * j, idesc_scaled<FMT>(256, 256, P::kNv ? 0 : j),
+                                       sfa + (P::kNv ? 4 * j : 0), sfb + (P::kNv ? 8 * j : 0), ks > 0 || j > 0,
+                                       leader & (uint32_t)(j < kk));
+                if (leader) mma_commit_pair(smem_u32(&sh.empty[st]));
+                if (++st == P::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            if (!ok) break;
+            if (leader) mma_commit_pair(smem_u32(&sh.acc_full[0]));
+            aph ^= 1;
+        }
+        if (!ok) {
+            if (leader) {
+                fail();
+                mma_commit_pair(smem_u32(&sh.drain));
+            }
+            __syncwarp();
+            mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
+        }
+    } else if (warp >= 4) {
+        // ---- accumulators to outputs: each CTA its own rows
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        uint32_t aph = 0;
+        const uint32_t empty = mapa_u32(smem_u32(&sh.acc_empty[0]), 0);
+        for (int tile = first_tile; tile < total; tile += stride) {
+            const Tile t = tile_at<kPairRows>(a, sh, tile, n_tiles);
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(smem_u32(&sh.acc_full[0]), aph, a.wait_limit, abort))) {
+                if (lane == 0) fail();
+                break;
+            }
+            tc_fence_after();
+            const int r0 = rank * 128 + quad * 32, r = r0 + lane, col0 = t.nt * 256 + half * 128;
+            const bool any = r0 < t.rows && col0 < a.N, live = any && r < t.rows;
+            const size_t row = (size_t)t.row0 + r;
+            const float s = (live && a.a_row_scale ? __ldg(a.a_row_scale + row) : 1.0f) * (a.alpha[0] ? __ldg(a.alpha[0] + t.g) : 1.0f);
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(empty);
+            };
+            if (any) store_rows<128>(a, tmem + half * 128 + ((uint32_t)(quad * 32) << 16), row, col0, s, live, release);
+            else release();
+            aph ^= 1;
+        }
+    }
+    __syncthreads();
+    cluster_sync();                                                   // nothing of the pair is in flight any more
+    if (warp == 3) tmem_dealloc_pair(tmem, 512);
+}
+
+// Once per kernel and device: its dynamic shared memory (`ready`: the devices on which that is done).
+template <class K>
+cudaError_t set_shared(K kernel, int bytes, std::atomic<uint64_t> &ready)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (ready.load(std::memory_order_relaxed) >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
+}
+
+// Scale tiles as rows of 128 32-bit words, in boxes of `box` tiles.
+bool make_map_scales(CUtensorMap *m, const uint8_t *p, uint64_t tiles, uint32_t box)
+{
+    return make_map_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, kScaleTile / 4, tiles, kScaleTile / 4, box, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+template <int FMT>
+cudaError_t launch_pair(const ScaledGemmArgs &a, int clusters, cudaStream_t st)
+{
+    using P = PairPlan<FMT>;
+    PairMaps maps;
+    const uint64_t ct = scaled_col_tiles(FMT, a.K), wrt = (a.N + kScaleRows - 1) / kScaleRows;
+    bool ok = make_map_2d(&maps.a, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, P::kNv ? a.K / 2 : a.K, a.R, kStepBytes, 128,
+                          CU_TENSOR_MAP_SWIZZLE_128B) &&
+              make_map_scales(&maps.sa, a.a_scales, (uint64_t)(a.R / kScaleRows + a.G) * ct, P::kTilesK) &&
+              make_map_scales(&maps.sw, a.w_scales[0], (uint64_t)a.G * wrt * ct, P::kTilesK);
+    ok = ok && (P::kNv ? make_map_2d(&maps.w, a.w_codes[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.K / 2, (uint64_t)a.G * a.N, kStepBytes,
+                                     128, CU_TENSOR_MAP_SWIZZLE_128B)
+                       : make_map_4bit(&maps.w, a.w_codes[0], a.K, (uint64_t)a.G * a.N, 128));
+    if (!ok) return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = set_shared(scaled_pair_kernel<FMT>, P::kSmem, ready);
+    if (e != cudaSuccess) return e;
+    return launch_dependent_clusters(scaled_pair_kernel<FMT>, 2 * clusters, 2, kThreads, P::kSmem, st, a, maps);
+}
+
 template <int FMT, bool DUAL, int BN>
 cudaError_t launch_plan(const ScaledGemmArgs &a, const Maps &maps, int ctas, cudaStream_t st)
 {
     using P = Plan<FMT, DUAL, BN>;
     auto k = scaled_gemm_kernel<FMT, DUAL, BN>;
-    static std::atomic<uint64_t> ready{0};               // devices on which the kernel's shared memory is set
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-    if (dev >= 64 || !(ready.load(std::memory_order_relaxed) >> dev & 1)) {
-        const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, P::kSmem);
-        if (e != cudaSuccess) return e;
-        if (dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-    }
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = set_shared(k, P::kSmem, ready);
+    if (e != cudaSuccess) return e;
     return launch_dependent(k, ctas, kThreads, P::kSmem, st, a, maps);
 }
 
@@ -537,6 +790,11 @@ cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
     // row tiles at most: every group's last one may be partial
     const long long mt = a.R / kScaleRows + (a.G < a.R ? a.G : a.R);
     auto tiles = [&](int out_n) { return mt * ((a.N + out_n - 1) / out_n); };
+    if constexpr (!DUAL) {
+        // groups of 256 rows and more on average, and tiles for every pair of SMs
+        const long long pairs = (a.R / kPairRows) * ((long long)(a.N + 255) / 256);
+        if (a.R / a.G >= kPairRows && pairs >= sms / 2) return launch_pair<FMT>(a, sms / 2, st);
+    }
     int bn = 256;
     if (DUAL) {
         if (tiles(128) < sms) bn = 128;
@@ -544,8 +802,6 @@ cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
         if (tiles(256) < sms) bn = 128;
         if (tiles(128) < sms) bn = 64;
     }
-    if (getenv("SG_BN")) bn = atoi(getenv("SG_BN"));
-    if (DUAL && bn == 64) bn = 128;
     const long long n = tiles(DUAL ? bn / 2 : bn);
     const int ctas = (int)(n < sms ? n : sms);
     Maps maps;

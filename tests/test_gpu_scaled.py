@@ -388,6 +388,24 @@ def test_gemm_many_tiles(fmt):
     assert (np.abs(first - want) <= product_error(K) * mag).all()
 
 
+@pytest.mark.parametrize("fmt,K", [(NV, 2112), (M8, 1408)])
+@pytest.mark.parametrize("offsets", [None, [0, 0, 257, 1500]])
+def test_gemm_large_groups(fmt, K, offsets):
+    """Groups of many row tiles (the launch shape for them), rows and outputs that end inside a tile."""
+    rng = np.random.default_rng(K)
+    off = offsets or [0]
+    R, N, G = 3001, 2008, len(off)
+    a, av = operand(rng, fmt, R, K, off)
+    w, wv, alpha = weights(rng, fmt, G, N, K)
+    want, mag = grouped(av, wv, off, alpha)
+    for dt in (torch.bfloat16, torch.float32):
+        y, ws = Out((R, N), dt), workspace()
+        qm.moe_scaled_gemm(fmt, a, w, R, N, K, G, None if offsets is None else gpu(np.array(off, np.int32)), y.t, ws)
+        assert qm.moe_get_device_status(ws) == 0
+        tol = product_error(K) * mag + (2.0 ** -8 * np.abs(want) if dt == torch.bfloat16 else 0)
+        assert (np.abs(y.check() - want) <= tol).all()
+
+
 @pytest.mark.parametrize("fmt", [NV, M8])
 def test_gemm_nan_rows_stay_apart(fmt):
     """A NaN scale reaches its own row (or, in a weight, its own column) and no other."""
