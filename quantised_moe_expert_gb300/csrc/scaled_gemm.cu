@@ -43,10 +43,11 @@ struct Plan {
     static constexpr int kBTxBytes = kNv ? kBBytes : kBBytes / 2;   // a widened copy counts the codes, not the padding
     static constexpr int kSfaBytes = kTilesK * kScaleTile, kSfbBytes = kChunks * kTilesK * kScaleTile;
     static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-    static constexpr int kStages = BN == 256 ? 4 : BN == 128 ? (DUAL ? 5 : 6) : 7;
+    static constexpr int kStages = BN == 256 ? (DUAL ? 4 : 3) : BN == 128 ? 5 : 7;
+    static constexpr int kOutBytes = DUAL || BN == 64 ? 0 : 32768;   // output staging of the epilogue warps
     static constexpr int kAccs = BN == 256 ? 1 : 2;          // accumulator buffers
     static constexpr int kSfCols = 4 * kTilesK * (1 + kChunks);   // tensor-memory columns of a stage's scales
-    static constexpr int kSmem = kStages * kStageBytes + 1024;
+    static constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024;
     static_assert(kAccs * BN + kStages * kSfCols <= 512, "tensor memory");
 };
 
@@ -200,27 +201,14 @@ __device__ __forceinline__ void store_f32(float *p, const uint32_t (&v)[16], flo
                                                              __uint_as_float(v[i + 2]) * s, __uint_as_float(v[i + 3]) * s);
 }
 
-// The first n (a multiple of 8) of 2 W bf16.  Whole 32-byte sectors a lane where the row allows it.
-template <int W>
-__device__ __forceinline__ void store_bf16(uint16_t *p, const uint32_t (&w)[W], int n)
-{
-    if (2 * W <= n && (reinterpret_cast<uintptr_t>(p) & 31) == 0) {
-#pragma unroll
-        for (int i = 0; i < W; i += 8)
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + 2 * i), "r"(w[i]), "r"(w[i + 1]),
-                         "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
-                         : "memory");
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < W; i += 4)
-        if (2 * i < n) *reinterpret_cast<uint4 *>(p + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
-}
-
-// COLS accumulator columns of the warp's rows to y; release() once they are in registers.
+// COLS accumulator columns of the warp's 32 rows (from `row` on, the first `rows` of them exist) to y;
+// release() once they are in registers.  bf16 outputs go through `stage`, the warp's 4 KB of shared memory, 64
+// columns at a time, so that 8 lanes write the 128 bytes of a row together: a lane of its own row touches
+// 32 lines in every store, which costs the load/store unit a cycle a line or more (4300 cycles a 128 x 256
+// tile, more than its products at K = 512).
 template <int COLS, class Release>
-__device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, size_t row, int col0, float s, bool live,
-                                           Release release)
+__device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, size_t row, int rows, int col0, float s, int lane,
+                                           uint8_t *stage, Release release)
 {
     if (a.y_f32) {
         uint32_t u[COLS / 16][16];
@@ -230,10 +218,10 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
         release();
 #pragma unroll
         for (int i = 0; i < COLS / 16; ++i)
-            if (live) store_f32(static_cast<float *>(a.y) + row * a.N + col0 + 16 * i, u[i], s, a.N - col0 - 16 * i);
+            if (lane < rows) store_f32(static_cast<float *>(a.y) + (row + lane) * a.N + col0 + 16 * i, u[i], s, a.N - col0 - 16 * i);
         return;
     }
-    constexpr int kBatch = COLS < 64 ? COLS : 64;
+    constexpr int kBatch = COLS < 64 ? COLS : 64, kChunks = kBatch / 8;      // 16-byte chunks of a row
     uint32_t w[COLS / 2];
 #pragma unroll
     for (int c = 0; c < COLS; c += kBatch) {
@@ -249,7 +237,32 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
         }
     }
     release();
-    if (live) store_bf16<COLS / 2>(static_cast<uint16_t *>(a.y) + row * a.N + col0, w, a.N - col0);
+    uint16_t *y = static_cast<uint16_t *>(a.y) + row * a.N + col0;
+    if constexpr (COLS < 64) {                             // few tiles: the shortest way (0.15 us of 4.7 at one token)
+        if (lane < rows) {
+#pragma unroll
+            for (int i = 0; i < COLS / 2; i += 4)
+                if (col0 + 2 * i < a.N)
+                    *reinterpret_cast<uint4 *>(y + (size_t)lane * a.N + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        }
+    } else
+#pragma unroll
+    for (int c = 0; c < COLS; c += kBatch) {
+        // row r's chunk k at (k ^ r) % kChunks of its kBatch * 2 bytes: no bank is met twice in a phase
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k)
+            *reinterpret_cast<uint4 *>(stage + lane * (kBatch * 2) + ((k ^ lane) % kChunks) * 16) =
+                make_uint4(w[c / 2 + 4 * k], w[c / 2 + 4 * k + 1], w[c / 2 + 4 * k + 2], w[c / 2 + 4 * k + 3]);
+        __syncwarp();
+        const int k = lane % kChunks;
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int r = i * (32 / kChunks) + lane / kChunks;
+            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * (kBatch * 2) + ((k ^ r) % kChunks) * 16);
+            if (r < rows && col0 + c + 8 * k < a.N) *reinterpret_cast<uint4 *>(y + (size_t)r * a.N + c + 8 * k) = v;
+        }
+        __syncwarp();
+    }
 }
 
 template <int FMT, bool DUAL, int BN>
@@ -459,7 +472,8 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             if (!any) {
                 release();
             } else if constexpr (!DUAL) {
-                store_rows<kCols>(a, d, row, col0, s0, live, release);
+                store_rows<kCols>(a, d, (size_t)t.row0 + quad * 32, t.rows - quad * 32, col0, s0, lane,
+                                  smem + P::kStages * P::kStageBytes + (warp - 4) * (P::kOutBytes / 8), release);
             } else {
                 uint32_t u[kCols / 16][16], u2[kCols / 16][16];          // gate and up products
 #pragma unroll
@@ -546,9 +560,9 @@ struct PairPlan {
     static constexpr int kBTxBytes = kNv ? kBBytes : kBBytes / 2;
     static constexpr int kSfBytes = kTilesK * kScaleTile;                   // one row tile's scales of a step
     static constexpr int kStageBytes = kABytes + kBBytes + 3 * kSfBytes;
-    static constexpr int kStages = kNv ? 5 : 6;
+    static constexpr int kStages = kNv ? 4 : 5;
     static constexpr int kSfCols = 4 * kTilesK * 3;
-    static constexpr int kSmem = kStages * kStageBytes + 1024;
+    static constexpr int kSmem = kStages * kStageBytes + 32768 + 1024;
     static_assert(256 + kStages * kSfCols <= 512, "tensor memory");
 };
 constexpr int kPairRows = 256;
@@ -723,7 +737,9 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(empty);
             };
-            if (any) store_rows<128>(a, tmem + half * 128 + ((uint32_t)(quad * 32) << 16), row, col0, s, live, release);
+            if (any)
+                store_rows<128>(a, tmem + half * 128 + ((uint32_t)(quad * 32) << 16), (size_t)t.row0 + r0, t.rows - r0, col0, s, lane,
+                                smem + P::kStages * P::kStageBytes + (warp - 4) * 4096, release);
             else release();
             aph ^= 1;
         }
