@@ -432,6 +432,34 @@ MOE_API int moe_scaled_swiglu(int format, const moe_scaled_rows *a, const moe_sc
                               int R, int inter, int K, int G, const int32_t *offsets, const float *h_scale,
                               const moe_scaled_rows *h, void *ws, size_t ws_bytes, void *stream);
 
+/* All weights of one layer whose expert products run block-scaled.  gate, up
+ * and down are stacks of n_experts + has_shared matrices, the shared expert's
+ * last: [G, inter, hidden], [G, inter, hidden], [G, hidden, inter].  With NVFP4
+ * a matrix's fp32 scale is its alpha, and down's alpha also carries h_scale. */
+typedef struct moe_scaled_weights {
+    int format;                       /* MOE_SCALED_NVFP4, or MOE_SCALED_MXFP8 (MXFP4 matrices) */
+    moe_qmat router;                  /* as in moe_weights */
+    const uint16_t *shared_gate_vec;  /* bf16 [hidden]; may be NULL without a shared expert */
+    moe_scaled_mat gate, up, down;
+    const float *h_scale;             /* NVFP4: fp32 [G], see moe_scaled_swiglu; MXFP8: NULL */
+} moe_scaled_weights;
+
+/* Bytes of workspace moe_scaled_forward needs for T tokens (0 <= T <= 65536); its
+ * header as for moe_workspace_size. */
+MOE_API int moe_scaled_workspace_size(const moe_config *cfg, int format, int T, size_t *bytes);
+
+/* The whole layer with block-scaled expert products: moe_route, moe_permute,
+ * moe_quantize_routed, moe_scaled_swiglu, moe_scaled_gemm (fp32) and the
+ * weighted sum of each token's slots, rounded once.  Routing runs on the bf16 x
+ * and is that of moe_forward; x and h are quantised, so y differs from
+ * moe_forward's by the activations' 4- or 8-bit rounding.  cfg describes the
+ * shape and the router (its bits and format fields are not used for the
+ * experts); hidden and inter: multiples of 64 (NVFP4) or 128 (MXFP8).  Other
+ * arguments as in moe_forward. */
+MOE_API int moe_scaled_forward(const moe_config *cfg, const moe_scaled_weights *w, const uint16_t *x, int T,
+                               const float *router_bias, const float *logits_in, uint16_t *y, int32_t *ids_out,
+                               uint16_t *p_out, uint16_t *w_shared_out, void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -43,7 +43,7 @@ EXPORTED = ("moe_status_string", "moe_check_config", "moe_workspace_size", "moe_
             "moe_expert_stages",
             "moe_decode_timeline", "moe_forward_decode_static",
             "moe_add_rmsnorm", "moe_quantize", "moe_quantize_routed", "moe_tile_scales", "moe_scaled_gemm",
-            "moe_scaled_swiglu")
+            "moe_scaled_swiglu", "moe_scaled_workspace_size", "moe_scaled_forward")
 
 
 class MoeError(RuntimeError):
@@ -75,6 +75,11 @@ class moe_scaled_rows(ctypes.Structure):
 
 class moe_scaled_mat(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("codes", "scales", "alpha")]
+
+
+class moe_scaled_weights(ctypes.Structure):
+    _fields_ = [("format", ctypes.c_int), ("router", moe_qmat), ("shared_gate_vec", ctypes.c_void_p),
+                ("gate", moe_scaled_mat), ("up", moe_scaled_mat), ("down", moe_scaled_mat), ("h_scale", ctypes.c_void_p)]
 
 
 _lock = threading.Lock()
@@ -128,6 +133,9 @@ def load(build: bool = True):
         lib.moe_tile_scales.argtypes = [_I, _VP, _I, _I, _I, _VP, _VP]
         lib.moe_scaled_gemm.argtypes = [_I, R, M, _I, _I, _I, _I, _VP, _VP, _I, _VP, _SZ, _VP]
         lib.moe_scaled_swiglu.argtypes = [_I, R, M, M, _I, _I, _I, _I, _VP, _VP, R, _VP, _SZ, _VP]
+        lib.moe_scaled_workspace_size.argtypes = [P(moe_config), _I, _I, P(ctypes.c_size_t)]
+        lib.moe_scaled_forward.argtypes = [P(moe_config), P(moe_scaled_weights), _VP, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
+                                           _SZ, _VP]
         for name in EXPORTED:
             if name != "moe_status_string":
                 getattr(lib, name).restype = ctypes.c_int
@@ -145,10 +153,10 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream):
     if stream is None:
         # the current stream's handle, without the stream object that torch.cuda.current_stream() makes
-        return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
@@ -358,6 +366,19 @@ def moe_scaled_swiglu(fmt, a, gate, up, R, inter, K, G, offsets, h_scale, h, ws,
     _check("moe_scaled_swiglu", rc)
 
 
+def moe_scaled_workspace_size(cfg: moe_config, fmt: int, T: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check("moe_scaled_workspace_size", load().moe_scaled_workspace_size(ctypes.byref(cfg), fmt, T, ctypes.byref(n)))
+    return n.value
+
+
+def moe_scaled_forward(cfg, w, x, T, router_bias, logits_in, y, ids_out, p_out, w_shared_out, ws, stream=None):
+    rc = load().moe_scaled_forward(ctypes.byref(cfg), ctypes.byref(w), _ptr(x), T, _ptr(router_bias), _ptr(logits_in), _ptr(y),
+                                   _ptr(ids_out), _ptr(p_out), _ptr(w_shared_out), _ptr(ws), ws.numel() * ws.element_size(),
+                                   _stream(stream))
+    _check("moe_scaled_forward", rc)
+
+
 # ---------------------------------------------------------------- conveniences
 
 def scaled_rows(codes, scales, row_scale=None) -> moe_scaled_rows:
@@ -386,6 +407,84 @@ def scaled_rows_empty(fmt: int, R: int, n: int, groups: int = 1, row_scale: bool
     rs = torch.empty((R,), device=device) if row_scale and fmt == MOE_SCALED_NVFP4 else None
     return scaled_rows(codes, scales, rs)
 
+
+
+class ScaledLayer:
+    """One layer's weights for moe_scaled_forward: stacks of the routed experts' matrices and, last, the shared expert's.
+
+    From an NVFP4 layer on the host (from_nvfp4, the layer DeviceLayer takes) or from matrices in floating
+    point (quantized, either format)."""
+
+    def __init__(self, shape, fmt, router, v, gate, up, down, h_scale=None):
+        """router: DeviceLayer-style tensors (codes, scales, biases); v: bf16 bits [hidden] or None; gate, up, down:
+        moe_scaled_mat; h_scale: float32 [G] (NVFP4)."""
+        self.shape, self.fmt, self.cfg = shape, fmt, config_of(shape)
+        self.tensors = (router, v, gate, up, down, h_scale)
+        self.w = moe_scaled_weights(fmt, moe_qmat(*[_ptr(t) for t in router], None), _ptr(v), gate, up, down, _ptr(h_scale))
+
+    @staticmethod
+    def _router(host, device):
+        up = lambda a: torch.from_numpy(np.ascontiguousarray(a).view(np.int16 if a.dtype == np.uint16 else a.dtype)).to(device)
+        return [up(host.router.codes), up(host.router.scales), up(host.router.biases)], up(host.shared_gate_vec)
+
+    @classmethod
+    def from_nvfp4(cls, host, h_scale, device="cuda"):
+        """host: a synth.LayerWeights with NVFP4 experts; h_scale: the calibrated factor of h, a float32 tensor of one value
+        per expert, shared expert last (see calibrate_h_scale)."""
+        shape = host.shape
+
+        def stack(m, s, N, n, factor):
+            parts = [m, s] if shape.has_shared else [m]
+            up = lambda name: torch.from_numpy(np.ascontiguousarray(np.concatenate([getattr(q, name) for q in parts]))).to(device)
+            scales, codes, alpha = up("scales"), up("codes"), up("gscale")
+            G = codes.shape[0]
+            tiles = torch.empty(G * -(-N // 128) * scaled_col_tiles(MOE_SCALED_NVFP4, n) * 512, dtype=torch.uint8, device=device)
+            moe_tile_scales(MOE_SCALED_NVFP4, scales, G, N, n, tiles)
+            return scaled_mat(codes, tiles, alpha if factor is None else alpha * factor)
+
+        H, I = shape.hidden, shape.inter
+        h_scale = h_scale.to(device=device, dtype=torch.float32).contiguous()
+        router, v = cls._router(host, device)
+        return cls(shape, MOE_SCALED_NVFP4, router, v, stack(host.gate, host.s_gate, I, H, None),
+                   stack(host.up, host.s_up, I, H, None), stack(host.down, host.s_down, H, I, h_scale), h_scale)
+
+    @classmethod
+    def quantized(cls, host, fmt, gate, up, down, h_scale=None, device="cuda"):
+        """host: the layer's shape, router and gate vector; gate, up [G, inter, hidden], down [G, hidden, inter]: float32
+        device tensors, quantised here to NVFP4 (fmt MOE_SCALED_NVFP4) or MXFP4 (MOE_SCALED_MXFP8)."""
+        nv = fmt == MOE_SCALED_NVFP4
+
+        def mat(m, factor):
+            G, N, n = m.shape
+            g = (m.abs().amax((1, 2)) / 2688).clamp_min(2.0 ** -110) if nv else None
+            codes = torch.empty((G, N, n // 2), dtype=torch.uint8, device=device)
+            tiles = torch.zeros(G * -(-N // 128) * scaled_col_tiles(fmt, n) * 512, dtype=torch.uint8, device=device)
+            moe_quantize(fmt if nv else MOE_SCALED_MXFP4, m.contiguous(), G * N, n, G, g, scaled_rows(codes, tiles))
+            return scaled_mat(codes, tiles, g if factor is None else g * factor)
+
+        router, v = cls._router(host, device)
+        return cls(host.shape, fmt, router, v, mat(gate, None), mat(up, None), mat(down, h_scale), h_scale)
+
+
+def calibrate_h_scale(layer: DeviceLayer, x: torch.Tensor, margin: float = 1.0) -> torch.Tensor:
+    """The NVFP4 factor of h of every expert (shared expert last) from a batch of tokens: the largest |h| the layer
+    computes on x, over all experts, times margin, over 2688."""
+    T, s = x.shape[0], layer.shape
+    ws = workspace(layer.cfg, T, x.device)
+    i32 = lambda *n: torch.empty(n, dtype=torch.int32, device=x.device)
+    ids, p, w_s = i32(T, s.top_k), torch.empty((T, s.top_k), dtype=torch.int16, device=x.device), \
+        torch.empty((T,), dtype=torch.int16, device=x.device)
+    counts, offsets, perm, inv = i32(s.n_experts), i32(s.n_experts + 1), i32(T * s.top_k), i32(T * s.top_k)
+    moe_route(layer.cfg, layer.w, x, T, None, None, None, ids, p, w_s, ws)
+    moe_permute(layer.cfg, ids, T, counts, offsets, perm, inv, ws)
+    h = torch.zeros((T * (s.top_k + 1), s.inter), device=x.device)
+    moe_expert_stages(layer.cfg, layer.w, x, T, ids, counts, offsets, perm, h, None, MOE_PATH_AUTO, ws)
+    return (h.abs().amax() * (margin / 2688)).clamp_min(2.0 ** -110).repeat(s.n_experts + s.has_shared)
+
+
+def scaled_workspace(cfg: moe_config, fmt: int, T: int, device="cuda") -> torch.Tensor:
+    """A zero-filled device workspace of moe_scaled_workspace_size bytes."""
+    return torch.zeros(moe_scaled_workspace_size(cfg, fmt, T), dtype=torch.uint8, device=device)
 
 
 def workspace(cfg: moe_config, T: int, device="cuda") -> torch.Tensor:

@@ -1,6 +1,7 @@
 // C ABI of the MoE layer library: argument checks, workspace carving, launches.
 // The operations and their contract are stated in include/moe.h.
 #include "kernels.cuh"
+#include "scaled.cuh"
 
 using namespace qmoe;
 
@@ -324,6 +325,44 @@ bool weights_ok(const moe_config &c, const moe_weights *w, bool need_router, boo
     return true;
 }
 
+// Scratch of the block-scaled layer behind the layer's own workspace: the expert-sorted rows of x and h in
+// block-scaled form (offsets from the start of the workspace).
+struct ScaledWs {
+    size_t x_codes, x_scales, x_factor, h_codes, h_scales, total;
+};
+
+ScaledWs scaled_ws(const moe_config &c, int format, int T, const WsLayout &L)
+{
+    const size_t R = (size_t)(T > 0 ? T : 1) * (c.top_k + c.has_shared), G = (size_t)c.n_experts + c.has_shared;
+    const size_t row_tiles = R / kScaleRows + G, div = scaled_is4(format) ? 2 : 1;
+    size_t o = align_up(L.total, 256);
+    auto take = [&](size_t bytes) { size_t r = o; o = align_up(o + bytes, 256); return r; };
+    ScaledWs s{};
+    s.x_codes = take(R * c.hidden / div);
+    s.x_scales = take(row_tiles * scaled_col_tiles(format, c.hidden) * kScaleTile);
+    s.x_factor = take(4 * R);
+    s.h_codes = take(R * c.inter / div);
+    s.h_scales = take(row_tiles * scaled_col_tiles(format, c.inter) * kScaleTile);
+    s.total = o;
+    return s;
+}
+
+int check_scaled(const moe_config *cfg, int format, int T)
+{
+    const int rc = check_common(cfg, T);
+    if (rc) return rc;
+    if (format != MOE_SCALED_NVFP4 && format != MOE_SCALED_MXFP8) return MOE_ERR_UNSUPPORTED;
+    const int unit = format == MOE_SCALED_NVFP4 ? 64 : 128;
+    return cfg->hidden % unit || cfg->inter % unit ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+bool scaled_mat_ok(const moe_scaled_mat &m, int format)
+{
+    const uintptr_t a = format == MOE_SCALED_MXFP8 ? 31u : 15u;
+    return m.codes && (reinterpret_cast<uintptr_t>(m.codes) & a) == 0 && aligned16(m.scales) &&
+           (reinterpret_cast<uintptr_t>(m.alpha) & 3u) == 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -613,6 +652,121 @@ int moe_decode_timeline(const moe_config *cfg, int T, void *ws, size_t ws_bytes,
         rc = cuda_rc(cudaMemcpy(host_stamps, ws_at<unsigned long long>(ws, L.trace),
                                 sizeof(unsigned long long) * kTraceStamps * (size_t)m, cudaMemcpyDeviceToHost));
     return rc;
+}
+
+int moe_scaled_workspace_size(const moe_config *cfg, int format, int T, size_t *bytes)
+{
+    const int rc = check_scaled(cfg, format, T);
+    if (rc) return rc;
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    *bytes = scaled_ws(*cfg, format, T, ws_layout(*cfg, T)).total;
+    return MOE_OK;
+}
+
+int moe_scaled_forward(const moe_config *cfg, const moe_scaled_weights *w, const uint16_t *x, int T,
+                       const float *router_bias, const float *logits_in, uint16_t *y, int32_t *ids_out,
+                       uint16_t *p_out, uint16_t *w_shared_out, void *ws, size_t ws_bytes, void *stream)
+{
+    if (!w) return MOE_ERR_INVALID_ARG;
+    int rc = check_scaled(cfg, w->format, T);
+    if (rc) return rc;
+    const bool nv = w->format == MOE_SCALED_NVFP4;
+    if (!aligned16(x) || !aligned16(y) || (!logits_in && !qmat_ok(w->router))) return MOE_ERR_INVALID_ARG;
+    if (!scaled_mat_ok(w->gate, w->format) || !scaled_mat_ok(w->up, w->format) || !scaled_mat_ok(w->down, w->format))
+        return MOE_ERR_INVALID_ARG;
+    if (nv ? !w->h_scale || (reinterpret_cast<uintptr_t>(w->h_scale) & 3u) : w->h_scale != nullptr) return MOE_ERR_INVALID_ARG;
+    if (cfg->has_shared && !aligned16(w->shared_gate_vec)) return MOE_ERR_INVALID_ARG;
+    if (!aligned16_or_null(router_bias) || !aligned16_or_null(logits_in) || !aligned16_or_null(ids_out) ||
+        !aligned16_or_null(p_out) || !aligned16_or_null(w_shared_out) || !aligned16(ws))
+        return MOE_ERR_INVALID_ARG;
+    const WsLayout L = ws_layout(*cfg, T);
+    const ScaledWs S = scaled_ws(*cfg, w->format, T, L);
+    if (ws_bytes < S.total) return MOE_ERR_WORKSPACE;
+    if (T == 0) return MOE_OK;
+    auto st = static_cast<cudaStream_t>(stream);
+    const moe_config &c = *cfg;
+    const int G = c.n_experts + c.has_shared, R = T * (c.top_k + c.has_shared);
+    moe_weights router{};
+    router.router = w->router;
+    router.shared_gate_vec = w->shared_gate_vec;
+    int32_t *ids = ids_out ? ids_out : ws_at<int32_t>(ws, L.ids);
+    uint16_t *p = p_out ? p_out : ws_at<uint16_t>(ws, L.p);
+    uint16_t *w_s = w_shared_out ? w_shared_out : ws_at<uint16_t>(ws, L.w_s);
+    if ((rc = enqueue_route(c, router, x, T, router_bias, logits_in, logits_in ? nullptr : ws_at<float>(ws, L.logits), ids, p,
+                            w_s, L, ws, st)))
+        return rc;
+    int32_t *offsets = ws_at<int32_t>(ws, L.offsets), *inv_perm = ws_at<int32_t>(ws, L.inv_perm);
+    PermuteArgs pa = permute_args(c, ids, T, ws_at<int32_t>(ws, L.counts), offsets, ws_at<int32_t>(ws, L.perm), inv_perm, L, ws);
+    pa.build_work = 0;
+    if ((rc = cuda_rc(launch_permute(pa, st)))) return rc;
+
+    RowArgs ra{};
+    ra.x = x;
+    ra.codes = ws_at<uint8_t>(ws, S.x_codes);
+    ra.scales = ws_at<uint8_t>(ws, S.x_scales);
+    ra.row_scale = nv ? ws_at<float>(ws, S.x_factor) : nullptr;
+    ra.ids = ids;
+    ra.inv_perm = inv_perm;
+    ra.offsets = offsets;
+    ra.status = ws_at<int>(ws, L.status);
+    ra.T = T;
+    ra.n = c.hidden;
+    ra.k = c.top_k;
+    ra.E = c.n_experts;
+    ra.has_shared = c.has_shared;
+    if ((rc = cuda_rc(launch_rows(ra, w->format, false, st)))) return rc;
+
+    ScaledGemmArgs g{};
+    g.a_codes = ra.codes;
+    g.a_scales = ra.scales;
+    g.a_row_scale = ra.row_scale;
+    const moe_scaled_mat *m[2] = {&w->gate, &w->up};
+    for (int i = 0; i < 2; ++i) {
+        g.w_codes[i] = m[i]->codes;
+        g.w_scales[i] = m[i]->scales;
+        g.alpha[i] = m[i]->alpha;
+    }
+    g.offsets = offsets;
+    g.h_codes = ws_at<uint8_t>(ws, S.h_codes);
+    g.h_scales = ws_at<uint8_t>(ws, S.h_scales);
+    g.h_gscale = w->h_scale;
+    g.status = ra.status;
+    g.R = R;
+    g.N = c.inter;
+    g.K = c.hidden;
+    g.G = G;
+    g.wait_limit = wait_limit_of(c);
+    if ((rc = cuda_rc(launch_scaled_gemm(g, w->format, true, st)))) return rc;
+
+    ScaledGemmArgs d{};
+    d.a_codes = g.h_codes;
+    d.a_scales = g.h_scales;
+    d.w_codes[0] = w->down.codes;
+    d.w_scales[0] = w->down.scales;
+    d.alpha[0] = w->down.alpha;
+    d.offsets = offsets;
+    d.y = ws_at<float>(ws, L.yslot);
+    d.y_f32 = 1;
+    d.status = ra.status;
+    d.R = R;
+    d.N = c.hidden;
+    d.K = c.inter;
+    d.G = G;
+    d.wait_limit = g.wait_limit;
+    if ((rc = cuda_rc(launch_scaled_gemm(d, w->format, false, st)))) return rc;
+
+    ReduceArgs r{};
+    r.yslot = ws_at<float>(ws, L.yslot);
+    r.pos = inv_perm;
+    r.status = ra.status;
+    r.p = p;
+    r.w_s = w_s;
+    r.y = y;
+    r.T = T;
+    r.H = c.hidden;
+    r.k = c.top_k;
+    r.has_shared = c.has_shared;
+    return cuda_rc(launch_slot_sum(r, st));
 }
 
 }  // extern "C"

@@ -143,3 +143,17 @@ def test_errors_reach_python():
     with pytest.raises(qm.MoeError) as e:
         qm._check("moe_scaled_gemm", gemm(qm.load(), K=96))
     assert e.value.status == UNSUPPORTED and "moe_scaled_gemm" in str(e.value)
+
+
+@pytest.mark.parametrize("fmt,kw,expect", [
+    (NV, {}, OK), (M8, {}, OK), (M4, {}, UNSUPPORTED), (0, {}, UNSUPPORTED),
+    (M8, dict(hidden=2112), UNSUPPORTED), (NV, dict(hidden=2112), OK), (NV, dict(top_k=17), UNSUPPORTED), (NV, dict(hidden=0), INVALID),
+])
+def test_layer_workspace_size(lib, fmt, kw, expect):
+    d = dict(hidden=2048, inter=512, n_experts=256, top_k=8, group=64, bits=4, router_bits=8, has_shared=1, wait_polls=0)
+    cfg, n, plain = qm.moe_config(**{**d, **kw}), ctypes.c_size_t(), ctypes.c_size_t()
+    assert lib.moe_scaled_workspace_size(ctypes.byref(cfg), fmt, 16, ctypes.byref(n)) == expect
+    if expect == OK:
+        assert lib.moe_workspace_size(ctypes.byref(cfg), 16, ctypes.byref(plain)) == OK and n.value > plain.value
+        assert lib.moe_scaled_workspace_size(ctypes.byref(cfg), fmt, -1, ctypes.byref(n)) == INVALID
+        assert lib.moe_scaled_workspace_size(ctypes.byref(cfg), fmt, 16, None) == INVALID
