@@ -116,7 +116,8 @@ cudaError_t launch_dependent_clusters(void (*kernel)(P...), unsigned grid, unsig
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+    return e == cudaSuccess ? e : cudaGetLastError();    // the error is returned, not left for a later launch to find
 }
 template <class... P, class... A>
 cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t st, A... args)

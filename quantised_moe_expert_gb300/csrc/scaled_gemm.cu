@@ -804,20 +804,26 @@ cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
     constexpr bool kNv = FMT == MOE_SCALED_NVFP4;
     const int sms = device_sm_count();
     // row tiles at most: every group's last one may be partial
-    const long long mt = a.R / kScaleRows + (a.G < a.R ? a.G : a.R);
+    const long long mt = a.offsets ? a.R / kScaleRows + (a.G < a.R ? a.G : a.R) : (a.R + kScaleRows - 1) / kScaleRows;
     auto tiles = [&](int out_n) { return mt * ((a.N + out_n - 1) / out_n); };
     if constexpr (!DUAL) {
-        // groups of 256 rows and more on average, and tiles for every pair of SMs
-        const long long pairs = (a.R / kPairRows) * ((long long)(a.N + 255) / 256);
-        if (a.R / a.G >= kPairRows && pairs >= sms / 2) return launch_pair<FMT>(a, sms / 2, st);
+        // A pair of CTAs a tile: groups of 256 rows and more on average, a tile for every pair of SMs, and K steps
+        // enough to pay for the longer way of a tile's first and last step.  us, one CTA / a pair: 8192 x 8192 x
+        // 4096 NVFP4 (16 steps) 119 / 105, MXFP8 (32) 192 / 156, 4096 x 4096 x 2048 NVFP4 (8) 23.7 / 23.8, 8192 x
+        // 2048 x 512 (2) 12.9 / 16.9; 1024 x 4096 x 4096 (64 pair tiles for 76 pairs) 10.6 / 11.0.
+        using P = PairPlan<FMT>;
+        const long long pairs = (a.R / kPairRows) * ((long long)(a.N + 255) / 256), ct = scaled_col_tiles(FMT, a.K);
+        const bool coords = ((long long)a.G * ((a.N + kScaleRows - 1) / kScaleRows) + 1) * ct < 0x7FFFFFFFll &&
+                            ((long long)a.R / kScaleRows + a.G + 1) * ct < 0x7FFFFFFFll;   // scale tiles as 32-bit coordinates
+        if (a.R / a.G >= kPairRows && pairs >= sms / 2 && a.K >= 12 * P::kStepK && coords) return launch_pair<FMT>(a, sms / 2, st);
     }
+    // The widest tile, or the narrowest of which there is at most one an SM.  us at 64 / 128 / 256 columns: 1 x 16384
+    // x 2048 NVFP4 (256, 128, 64 tiles) 6.9 / 5.2 / 5.9, 512 x 4096 x 4096 (256, 128, 64) 11.6 / 7.9 / 10.4, 64 x 8192
+    // x 4096 MXFP8 (128, 64, 32) 9.5 / 9.8 / 12.3, 256 x 4096 x 4096 (128, 64, 32) 7.3 / 7.5 / 9.0; experts of 512
+    // tokens: the SwiGLU pair 56 us with 128, 51 with 256, the down products 39 with 128, 32 with 256.
     int bn = 256;
-    if (DUAL) {
-        if (tiles(128) < sms) bn = 128;
-    } else {
-        if (tiles(256) < sms) bn = 128;
-        if (tiles(128) < sms) bn = 64;
-    }
+    if (tiles(DUAL ? 64 : 128) <= sms) bn = 128;
+    if (!DUAL && tiles(64) <= sms) bn = 64;
     const long long n = tiles(DUAL ? bn / 2 : bn);
     const int ctas = (int)(n < sms ? n : sms);
     Maps maps;
