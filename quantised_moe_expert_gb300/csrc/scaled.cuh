@@ -96,9 +96,10 @@ __device__ __forceinline__ float nvfp4_row_factor(uint32_t amax_bits)
 
 // ---------------------------------------------------------------- launches
 
-// Every kernel of this family lets its successor in the stream start at once (griddepcontrol.launch_dependents
-// first thing) and reads or writes memory only after griddepcontrol.wait, in every block: a successor's
-// set-up (barriers, tensor memory, tensor maps) runs under its predecessor's tail.
+// Every kernel of this family lets its successor in the stream start early (griddepcontrol.launch_dependents)
+// and reads or writes memory only after griddepcontrol.wait, in every block: a successor's set-up (barriers,
+// tensor memory, tensor maps) runs under its predecessor's tail.  A norm of one row behind another: 2.6 us from
+// launch to launch without, 1.9 us with.
 template <class... P, class... A>
 cudaError_t launch_dependent_clusters(void (*kernel)(P...), unsigned grid, unsigned cluster, unsigned block, size_t smem,
                                       cudaStream_t st, A... args)

@@ -17,6 +17,7 @@ namespace qmoe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kEarlyBlocks = 152;                  // one block an SM
 
 // Sum or maximum over the TPR threads of a row; `buf` holds one value per warp.  Every thread of the
 // block takes part.
@@ -147,7 +148,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     constexpr int kLanes = kBlk / 8;                          // lanes of a block
     __shared__ float sbuf[kThreads / 32];
     __shared__ uint32_t mbuf[kThreads / 32];
-    tc::pdl_trigger();
+    // The successor may come in at once; beside a full grid that writes many copies a row only when the rows
+    // are read, since its waiting blocks slow that one (512 rows into 9 copies each: 5.2 us against 4.0; the
+    // norm of 777 x 5120 is faster with it, 7.9 us against 8.4).
+    const bool early = !a.ids || gridDim.x <= kEarlyBlocks;
+    if (early) tc::pdl_trigger();
     tc::pdl_wait();
     const int tr = threadIdx.x % TPR;
     const int t = blockIdx.x * (kThreads / TPR) + threadIdx.x / TPR;
@@ -273,6 +278,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
 #pragma unroll
             for (int o = kLanes; o < 4 * kLanes; o <<= 1) word[c] |= __shfl_xor_sync(0xFFFFFFFFu, word[c], o);
         }
+        if (!early) tc::pdl_trigger();
         if (!live) return;
         for (int j = 0; j < copies; ++j) {
             Dest d;
