@@ -43,8 +43,9 @@ struct Plan {
     static constexpr int kBTxBytes = kNv ? kBBytes : kBBytes / 2;   // a widened copy counts the codes, not the padding
     static constexpr int kSfaBytes = kTilesK * kScaleTile, kSfbBytes = kChunks * kTilesK * kScaleTile;
     static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-    static constexpr int kStages = BN == 256 ? (DUAL ? 4 : 3) : BN == 128 ? 5 : 7;
-    static constexpr int kOutBytes = DUAL || BN == 64 ? 0 : 32768;   // output staging of the epilogue warps
+    static constexpr int kStages = BN == 256 ? (DUAL || !kNv ? 4 : 3) : BN == 128 ? 5 : 7;
+    static constexpr int kStaged = BN == 256 && !kNv ? 32 : 64;      // columns an epilogue warp stages at a time
+    static constexpr int kOutBytes = DUAL || BN == 64 ? 0 : 8 * 32 * kStaged * 2;
     static constexpr int kAccs = BN == 256 ? 1 : 2;          // accumulator buffers
     static constexpr int kSfCols = 4 * kTilesK * (1 + kChunks);   // tensor-memory columns of a stage's scales
     static constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024;
@@ -202,11 +203,11 @@ __device__ __forceinline__ void store_f32(float *p, const uint32_t (&v)[16], flo
 }
 
 // COLS accumulator columns of the warp's 32 rows (from `row` on, the first `rows` of them exist) to y;
-// release() once they are in registers.  bf16 outputs go through `stage`, the warp's 4 KB of shared memory, 64
-// columns at a time, so that 8 lanes write the 128 bytes of a row together: a lane of its own row touches
-// 32 lines in every store, which costs the load/store unit a cycle a line or more (4300 cycles a 128 x 256
-// tile, more than its products at K = 512).
-template <int COLS, class Release>
+// release() once they are in registers.  bf16 outputs go through `stage`, the warp's part of shared memory,
+// STAGED columns at a time (64, or 32 where another stage of operands fits then), so that 8 or 4 lanes write a
+// row's bytes together: a lane of its own row touches 32 lines in every store, which costs the load/store
+// unit a cycle a line or more (4300 cycles a 128 x 256 tile, more than its products at K = 512).
+template <int COLS, int STAGED, class Release>
 __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, size_t row, int rows, int col0, float s, int lane,
                                            uint8_t *stage, Release release)
 {
@@ -221,7 +222,7 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
             if (lane < rows) store_f32(static_cast<float *>(a.y) + (row + lane) * a.N + col0 + 16 * i, u[i], s, a.N - col0 - 16 * i);
         return;
     }
-    constexpr int kBatch = COLS < 64 ? COLS : 64, kChunks = kBatch / 8;      // 16-byte chunks of a row
+    constexpr int kBatch = COLS < 64 ? COLS : 64, kChunks = STAGED / 8;      // 16-byte chunks of a row
     uint32_t w[COLS / 2];
 #pragma unroll
     for (int c = 0; c < COLS; c += kBatch) {
@@ -247,18 +248,18 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
         }
     } else
 #pragma unroll
-    for (int c = 0; c < COLS; c += kBatch) {
-        // row r's chunk k at (k ^ r) % kChunks of its kBatch * 2 bytes: no bank is met twice in a phase
+    for (int c = 0; c < COLS; c += STAGED) {
+        // row r's chunk k at (k ^ r) % kChunks of its STAGED * 2 bytes: no bank is met twice in a phase
 #pragma unroll
         for (int k = 0; k < kChunks; ++k)
-            *reinterpret_cast<uint4 *>(stage + lane * (kBatch * 2) + ((k ^ lane) % kChunks) * 16) =
+            *reinterpret_cast<uint4 *>(stage + lane * (STAGED * 2) + ((k ^ lane) % kChunks) * 16) =
                 make_uint4(w[c / 2 + 4 * k], w[c / 2 + 4 * k + 1], w[c / 2 + 4 * k + 2], w[c / 2 + 4 * k + 3]);
         __syncwarp();
         const int k = lane % kChunks;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
             const int r = i * (32 / kChunks) + lane / kChunks;
-            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * (kBatch * 2) + ((k ^ r) % kChunks) * 16);
+            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * (STAGED * 2) + ((k ^ r) % kChunks) * 16);
             if (r < rows && col0 + c + 8 * k < a.N) *reinterpret_cast<uint4 *>(y + (size_t)r * a.N + c + 8 * k) = v;
         }
         __syncwarp();
@@ -472,7 +473,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             if (!any) {
                 release();
             } else if constexpr (!DUAL) {
-                store_rows<kCols>(a, d, (size_t)t.row0 + quad * 32, t.rows - quad * 32, col0, s0, lane,
+                store_rows<kCols, P::kStaged>(a, d, (size_t)t.row0 + quad * 32, t.rows - quad * 32, col0, s0, lane,
                                   smem + P::kStages * P::kStageBytes + (warp - 4) * (P::kOutBytes / 8), release);
             } else {
                 uint32_t u[kCols / 16][16], u2[kCols / 16][16];          // gate and up products
@@ -548,7 +549,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
 //
 // Large groups: two SMs share a tile of 256 rows x 256 outputs (cta_group::2).  Each holds the codes of its own
 // 128 rows and of half of the weights, so that a step brings an SM 38 KB in place of 54 KB for the same
-// products, and five stages fit in place of four: the one-CTA kernel waits a third of its time for a refilled
+// products, and five stages fit in place of three: the one-CTA kernel waits a third of its time for a refilled
 // stage.  The first CTA issues the products of both; all copies of a stage complete on its barrier, and its
 // commits arrive in both.
 
@@ -560,9 +561,9 @@ struct PairPlan {
     static constexpr int kBTxBytes = kNv ? kBBytes : kBBytes / 2;
     static constexpr int kSfBytes = kTilesK * kScaleTile;                   // one row tile's scales of a step
     static constexpr int kStageBytes = kABytes + kBBytes + 3 * kSfBytes;
-    static constexpr int kStages = kNv ? 4 : 5;
+    static constexpr int kStages = kNv ? 5 : 6;
     static constexpr int kSfCols = 4 * kTilesK * 3;
-    static constexpr int kSmem = kStages * kStageBytes + 32768 + 1024;
+    static constexpr int kSmem = kStages * kStageBytes + 16384 + 1024;
     static_assert(256 + kStages * kSfCols <= 512, "tensor memory");
 };
 constexpr int kPairRows = 256;
@@ -738,8 +739,8 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 if (lane == 0) mbar_arrive_cluster(empty);
             };
             if (any)
-                store_rows<128>(a, tmem + half * 128 + ((uint32_t)(quad * 32) << 16), (size_t)t.row0 + r0, t.rows - r0, col0, s, lane,
-                                smem + P::kStages * P::kStageBytes + (warp - 4) * 4096, release);
+                store_rows<128, 32>(a, tmem + half * 128 + ((uint32_t)(quad * 32) << 16), (size_t)t.row0 + r0, t.rows - r0, col0, s, lane,
+                                smem + P::kStages * P::kStageBytes + (warp - 4) * 2048, release);
             else release();
             aph ^= 1;
         }
