@@ -331,39 +331,60 @@ def moe_decode_timeline(cfg, T, ws, stream=None, max_ctas: int = 256) -> np.ndar
     return buf[:min(n.value, max_ctas)]
 
 
+# The block-scaled operators are microseconds on the device at small sizes, so their bindings do no more than
+# they have to: no ctypes objects for pointers, the stream's handle and not its object.
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _handle(stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
 def moe_add_rmsnorm(x, residual, weight, weight_offset, eps, T, n, sum_out, y_out, fmt, q, stream=None):
-    rc = load().moe_add_rmsnorm(_ptr(x), _ptr(residual), _ptr(weight), weight_offset, eps, T, n, _ptr(sum_out),
-                                _ptr(y_out), fmt, q, _stream(stream))
-    _check("moe_add_rmsnorm", rc)
+    rc = (_lib or load()).moe_add_rmsnorm(x.data_ptr(), _addr(residual), _addr(weight), weight_offset, eps, T, n,
+                                          _addr(sum_out), _addr(y_out), fmt, q, _handle(stream))
+    if rc:
+        raise MoeError("moe_add_rmsnorm", rc)
 
 
 def moe_quantize(fmt, x, T, n, groups, gscale, q, stream=None):
     """x: a bf16 (or int16 bits) or float32 tensor."""
-    rc = load().moe_quantize(fmt, _ptr(x), int(x.dtype == torch.float32), T, n, groups, _ptr(gscale), q, _stream(stream))
-    _check("moe_quantize", rc)
+    rc = (_lib or load()).moe_quantize(fmt, x.data_ptr(), x.dtype == torch.float32, T, n, groups, _addr(gscale), q,
+                                       _handle(stream))
+    if rc:
+        raise MoeError("moe_quantize", rc)
 
 
 def moe_quantize_routed(fmt, x, T, n, k, E, has_shared, ids, inv_perm, offsets, q, ws, stream=None):
-    rc = load().moe_quantize_routed(fmt, _ptr(x), T, n, k, E, has_shared, _ptr(ids), _ptr(inv_perm), _ptr(offsets), q,
-                                    _ptr(ws), ws.numel() * ws.element_size(), _stream(stream))
-    _check("moe_quantize_routed", rc)
+    rc = (_lib or load()).moe_quantize_routed(fmt, x.data_ptr(), T, n, k, E, has_shared, ids.data_ptr(), inv_perm.data_ptr(),
+                                              offsets.data_ptr(), q, ws.data_ptr(), ws.nbytes, _handle(stream))
+    if rc:
+        raise MoeError("moe_quantize_routed", rc)
 
 
 def moe_tile_scales(fmt, src, G, N, n, dst, stream=None):
-    _check("moe_tile_scales", load().moe_tile_scales(fmt, _ptr(src), G, N, n, _ptr(dst), _stream(stream)))
+    rc = (_lib or load()).moe_tile_scales(fmt, src.data_ptr(), G, N, n, dst.data_ptr(), _handle(stream))
+    if rc:
+        raise MoeError("moe_tile_scales", rc)
 
 
 def moe_scaled_gemm(fmt, a, w, R, N, K, G, offsets, y, ws, stream=None):
     """y: a bf16 (or int16 bits) or float32 tensor [R, N]."""
-    rc = load().moe_scaled_gemm(fmt, a, w, R, N, K, G, _ptr(offsets), _ptr(y), int(y.dtype == torch.float32), _ptr(ws),
-                                ws.numel() * ws.element_size(), _stream(stream))
-    _check("moe_scaled_gemm", rc)
+    rc = (_lib or load()).moe_scaled_gemm(fmt, a, w, R, N, K, G, _addr(offsets), y.data_ptr(), y.dtype == torch.float32,
+                                          ws.data_ptr(), ws.nbytes, _handle(stream))
+    if rc:
+        raise MoeError("moe_scaled_gemm", rc)
 
 
 def moe_scaled_swiglu(fmt, a, gate, up, R, inter, K, G, offsets, h_scale, h, ws, stream=None):
-    rc = load().moe_scaled_swiglu(fmt, a, gate, up, R, inter, K, G, _ptr(offsets), _ptr(h_scale), h, _ptr(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream))
-    _check("moe_scaled_swiglu", rc)
+    rc = (_lib or load()).moe_scaled_swiglu(fmt, a, gate, up, R, inter, K, G, _addr(offsets), _addr(h_scale), h,
+                                            ws.data_ptr(), ws.nbytes, _handle(stream))
+    if rc:
+        raise MoeError("moe_scaled_swiglu", rc)
 
 
 def moe_scaled_workspace_size(cfg: moe_config, fmt: int, T: int) -> int:

@@ -829,12 +829,15 @@ cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
     const int ctas = (int)(n < sms ? n : sms);
     Maps maps;
     const uint64_t abytes = kNv ? a.K / 2 : a.K;
-    bool ok = make_map_2d(&maps.a128, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, abytes, a.R, kStepBytes, 128,
-                          CU_TENSOR_MAP_SWIZZLE_128B) &&
-              make_map_2d(&maps.a32, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, abytes, a.R, kStepBytes, 32,
+    bool ok = make_map_2d(&maps.a32, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, abytes, a.R, kStepBytes, 32,
                           CU_TENSOR_MAP_SWIZZLE_128B);
-    for (int i = 0; i < 2; ++i) {
-        const uint8_t *w = a.w_codes[DUAL ? i : 0];
+    maps.a128 = maps.a32;                                // up to 96 rows the kernel takes 32 at a time
+    maps.w[1] = CUtensorMap{};
+    if (a.R > 96)
+        ok = ok && make_map_2d(&maps.a128, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, abytes, a.R, kStepBytes, 128,
+                               CU_TENSOR_MAP_SWIZZLE_128B);
+    for (int i = 0; i < (DUAL ? 2 : 1); ++i) {
+        const uint8_t *w = a.w_codes[i];
         const uint32_t box = DUAL ? bn / 2 : bn;
         if (kNv)
             ok = ok && make_map_2d(&maps.w[i], w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, a.K / 2, (uint64_t)a.G * a.N, kStepBytes,
