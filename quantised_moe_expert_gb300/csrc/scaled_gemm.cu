@@ -31,7 +31,7 @@ constexpr int kThreads = 384;
 constexpr int kMaxGroups = 1024;
 constexpr int kStepBytes = 128;                    // bytes of a K step in a row of codes (as in shared memory)
 
-template <int FMT, bool DUAL, int BN>
+template <int FMT, bool DUAL, int BN, bool SPLIT>
 struct Plan {
     static constexpr bool kNv = FMT == MOE_SCALED_NVFP4;
     static constexpr int kStepK = kNv ? 256 : 128;           // elements of a K step
@@ -48,7 +48,9 @@ struct Plan {
     static constexpr int kOutBytes = DUAL || BN == 64 ? 0 : 8 * 32 * kStaged * 2;
     static constexpr int kAccs = BN == 256 ? 1 : 2;          // accumulator buffers
     static constexpr int kSfCols = 4 * kTilesK * (1 + kChunks);   // tensor-memory columns of a stage's scales
-    static constexpr int kSmem = kStages * kStageBytes + kOutBytes + 1024;
+    static constexpr int kPartCols = (DUAL ? 2 : 1) * kOutN / 2;     // accumulator columns of an epilogue warp
+    static constexpr int kPartBytes = SPLIT ? 2 * 32 * kPartCols * 4 : 0;   // the other CTA's sums (32 rows)
+    static constexpr int kSmem = kStages * kStageBytes + kOutBytes + kPartBytes + 1024;
     static_assert(kAccs * BN + kStages * kSfCols <= 512, "tensor memory");
 };
 
@@ -57,7 +59,7 @@ struct Maps {
 };
 
 struct Shared {
-    uint64_t full[8], empty[8], acc_full[2], acc_empty[2], drain;
+    uint64_t full[8], empty[8], acc_full[2], acc_empty[2], part[2], drain;
     uint32_t tmem;
     int abort;
     int bad, groups, row_tiles;                              // malformed offsets; groups with rows; their row tiles
@@ -202,6 +204,20 @@ __device__ __forceinline__ void store_f32(float *p, const uint32_t (&v)[16], flo
                                                              __uint_as_float(v[i + 2]) * s, __uint_as_float(v[i + 3]) * s);
 }
 
+// Adds the other CTA's sums of 16 columns from `col` on to this row's: part[column / 4][row], or null.
+__device__ __forceinline__ void add_part(uint32_t (&u)[16], const float4 *part, int col, int lane)
+{
+    if (part == nullptr) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 p = part[(col / 4 + i) * 32 + lane];
+        u[4 * i] = __float_as_uint(__uint_as_float(u[4 * i]) + p.x);
+        u[4 * i + 1] = __float_as_uint(__uint_as_float(u[4 * i + 1]) + p.y);
+        u[4 * i + 2] = __float_as_uint(__uint_as_float(u[4 * i + 2]) + p.z);
+        u[4 * i + 3] = __float_as_uint(__uint_as_float(u[4 * i + 3]) + p.w);
+    }
+}
+
 // COLS accumulator columns of the warp's 32 rows (from `row` on, the first `rows` of them exist) to y;
 // release() once they are in registers.  bf16 outputs go through `stage`, the warp's part of shared memory,
 // STAGED columns at a time (64, or 32 where another stage of operands fits then), so that 8 or 4 lanes write a
@@ -209,7 +225,7 @@ __device__ __forceinline__ void store_f32(float *p, const uint32_t (&v)[16], flo
 // unit a cycle a line or more (4300 cycles a 128 x 256 tile, more than its products at K = 512).
 template <int COLS, int STAGED, class Release>
 __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, size_t row, int rows, int col0, float s, int lane,
-                                           uint8_t *stage, Release release)
+                                           uint8_t *stage, const float4 *part, Release release)
 {
     if (a.y_f32) {
         uint32_t u[COLS / 16][16];
@@ -217,6 +233,8 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
         for (int i = 0; i < COLS / 16; ++i) tmem_ld16(d + 16 * i, u[i]);
         tmem_ld_wait();
         release();
+#pragma unroll
+        for (int i = 0; i < COLS / 16; ++i) add_part(u[i], part, 16 * i, lane);
 #pragma unroll
         for (int i = 0; i < COLS / 16; ++i)
             if (lane < rows) store_f32(static_cast<float *>(a.y) + (row + lane) * a.N + col0 + 16 * i, u[i], s, a.N - col0 - 16 * i);
@@ -230,6 +248,8 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
 #pragma unroll
         for (int i = 0; i < kBatch / 16; ++i) tmem_ld16(d + c + 16 * i, u[i]);
         tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < kBatch / 16; ++i) add_part(u[i], part, c + 16 * i, lane);
 #pragma unroll
         for (int i = 0; i < kBatch / 2; ++i) {
             const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(u[i / 8][2 * i % 16]) * s,
@@ -266,17 +286,24 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
     }
 }
 
-template <int FMT, bool DUAL, int BN>
+// SPLIT: few rows (at most 32) on no more tiles than half the SMs, where the K steps one after the other are
+// the time: two CTAs (a cluster) take half of a tile's steps each, and the second hands its sums to the first
+// through that one's shared memory.
+template <int FMT, bool DUAL, int BN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_constant__ Maps maps)
 {
-    using P = Plan<FMT, DUAL, BN>;
+    using P = Plan<FMT, DUAL, BN, SPLIT>;
     extern __shared__ uint8_t smem_raw[];
     __shared__ Shared sh;
     uint8_t *smem = align_smem_1024(smem_raw);
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int n_tiles = (a.N + P::kOutN - 1) / P::kOutN, n_steps = (a.K + P::kStepK - 1) / P::kStepK;
     const int ct = scaled_col_tiles(FMT, a.K);
+    // this CTA's tiles and its K steps of each
+    const int rank = SPLIT ? (int)cluster_ctarank() : 0;
+    const int first_tile = SPLIT ? blockIdx.x >> 1 : blockIdx.x, stride = SPLIT ? gridDim.x >> 1 : gridDim.x;
+    const int ks0 = SPLIT && rank ? (n_steps + 1) / 2 : 0, ks1 = SPLIT && !rank ? (n_steps + 1) / 2 : n_steps;
     const int w_row_tiles = (a.N + kScaleRows - 1) / kScaleRows;      // scale row tiles of a matrix
 
     pdl_trigger();
@@ -294,6 +321,8 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             mbar_init(smem_u32(&sh.acc_empty[i]), 8);
         }
         mbar_init(smem_u32(&sh.drain), 1);
+        mbar_init(smem_u32(&sh.part[0]), 1);
+        mbar_init(smem_u32(&sh.part[1]), 1);
         sh.abort = 0;
         sh.bad = 0;
         sh.row_tiles = (a.R + kScaleRows - 1) / kScaleRows;
@@ -304,10 +333,12 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         tmem_relinquish();
     }
     __syncthreads();
+    if (SPLIT) cluster_arrive();
     pdl_wait();
     if (a.offsets) build_table<kScaleRows>(a, sh, warp, lane);
     tc_fence_before();
     __syncthreads();
+    if (SPLIT) cluster_wait();                                        // the first CTA's barriers are there
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem, 0);
     const int total = __shfl_sync(0xFFFFFFFFu, sh.row_tiles * n_tiles, 0);
@@ -329,7 +360,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         int st = 0, issued = 0;
         uint32_t ph = 0;
         bool ok = true;
-        for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        for (int tile = first_tile; ok && tile < total; tile += stride) {
             const Tile t = tile_at<kScaleRows>(a, sh, tile, n_tiles);
             const int n0 = t.nt * P::kOutN, wrow = t.g * a.N + n0;
             const bool second = P::kChunks == 2 && (DUAL || n0 / kScaleRows + 1 < w_row_tiles);
@@ -337,7 +368,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             const size_t row = (size_t)ct * kScaleTile, wt = (size_t)t.g * w_row_tiles + n0 / kScaleRows;
             const uint8_t *pa = a.a_scales + t.srow_tile * row, *pb = a.w_scales[0] + wt * row;
             const uint8_t *pc = a.w_scales[DUAL ? 1 : 0] + (DUAL ? wt : wt + 1) * row;
-            for (int ks = 0; ks < n_steps; ++ks) {
+            for (int ks = ks0; ks < ks1; ++ks) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.empty[st]), ph ^ 1, a.wait_limit, abort));
                 if (!ok) {
                     if (leader) fail();
@@ -388,13 +419,13 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         uint32_t ph = 0, aph = 0;
         bool ok = true;
         const uint32_t sf0 = tmem + P::kAccs * BN;
-        for (int tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+        for (int tile = first_tile; ok && tile < total; tile += stride) {
             // columns of the first weight row inside its scale row tile (32 rows a column)
             const uint32_t sub = P::kOutN % kScaleRows ? (uint32_t)(tile % n_tiles * P::kOutN % kScaleRows) / 32 : 0;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1, a.wait_limit, abort));
             tc_fence_after();
             const uint32_t d = tmem + acc * BN;
-            for (int ks = 0; ok && ks < n_steps; ++ks) {
+            for (int ks = ks0; ok && ks < ks1; ++ks) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.full[st]), ph, a.wait_limit, abort));
                 if (!ok) break;
                 tc_fence_after();
@@ -414,7 +445,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     // 32 bytes along K inside the swizzle atom
-                    const uint32_t id = idesc_scaled<FMT>(128, P::kMmaN, P::kNv ? 0 : j), go = ks > 0 || j > 0;
+                    const uint32_t id = idesc_scaled<FMT>(128, P::kMmaN, P::kNv ? 0 : j), go = ks > ks0 || j > 0;
                     const uint32_t sa = sfa + (P::kNv ? 4 * j : 0), sb = sfb + (P::kNv ? 4 * P::kChunks * j : 0);
                     const uint32_t on = leader & (uint32_t)(j < kk);
                     mma_scaled<FMT, 1>(d, ad + 2 * j, bd + 2 * j, id, sa, sb, go, on);
@@ -450,7 +481,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         const int quad = warp & 3, half = (warp - 4) >> 2;
         int acc = 0;
         uint32_t aph = 0;
-        for (int tile = blockIdx.x; tile < total; tile += gridDim.x) {
+        for (int tile = first_tile; tile < total; tile += stride) {
             const Tile t = tile_at<kScaleRows>(a, sh, tile, n_tiles);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.acc_full[acc]), aph, a.wait_limit, abort))) {
                 if (lane == 0) fail();
@@ -470,11 +501,41 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 __syncwarp();
                 if (lane == 0) mbar_arrive(smem_u32(&sh.acc_empty[acc]));
             };
+            const float4 *part = nullptr;
+            if constexpr (SPLIT) {
+                float4 *const mine = reinterpret_cast<float4 *>(smem + P::kStages * P::kStageBytes + P::kOutBytes) + half * 8 * P::kPartCols;
+                if (rank) {
+                    if (any) {
+                        const uint32_t to = mapa_u32(smem_u32(mine), 0) + lane * 16;
+#pragma unroll
+                        for (int i = 0; i < P::kPartCols; i += 16) {
+                            uint32_t u[16];
+                            // a SwiGLU tile's up products follow its gate products of all the tile's columns
+                            tmem_ld16(d + (DUAL && i >= kCols ? BN / 2 - kCols + i : i), u);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) st_cluster_v4(to + (i / 4 + c) * 512, u[4 * c], u[4 * c + 1], u[4 * c + 2], u[4 * c + 3]);
+                        }
+                        fence_cluster();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(mapa_u32(smem_u32(&sh.part[half]), 0));
+                    }
+                    release();
+                    break;                                                // the tile is the first CTA's from here on
+                }
+                if (any) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(smem_u32(&sh.part[half]), 0, a.wait_limit, abort))) {
+                        if (lane == 0) fail();
+                        break;
+                    }
+                    part = mine;
+                }
+            }
             if (!any) {
                 release();
             } else if constexpr (!DUAL) {
                 store_rows<kCols, P::kStaged>(a, d, (size_t)t.row0 + quad * 32, t.rows - quad * 32, col0, s0, lane,
-                                  smem + P::kStages * P::kStageBytes + (warp - 4) * (P::kOutBytes / 8), release);
+                                  smem + P::kStages * P::kStageBytes + (warp - 4) * (P::kOutBytes / 8), part, release);
             } else {
                 uint32_t u[kCols / 16][16], u2[kCols / 16][16];          // gate and up products
 #pragma unroll
@@ -484,6 +545,11 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 }
                 tmem_ld_wait();
                 release();
+#pragma unroll
+                for (int i = 0; i < kCols / 16; ++i) {
+                    add_part(u[i], part, 16 * i, lane);
+                    add_part(u2[i], part, kCols + 16 * i, lane);
+                }
                 const float s1 = rs * (a.alpha[1] ? __ldg(a.alpha[1] + t.g) : 1.0f);
                 float ginv = 1.0f;
                 if (P::kNv) ginv = __fdiv_rn(1.0f, __ldg(a.h_gscale + t.g));
@@ -542,6 +608,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         }
     }
     __syncthreads();
+    if (SPLIT) cluster_sync();                                        // no store of the second CTA is on its way any more
     if (warp == 3) tmem_dealloc(tmem, 512);
 }
 
@@ -740,7 +807,7 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             };
             if (any)
                 store_rows<128, 32>(a, tmem + half * 128 + ((uint32_t)(quad * 32) << 16), (size_t)t.row0 + r0, t.rows - r0, col0, s, lane,
-                                smem + P::kStages * P::kStageBytes + (warp - 4) * 2048, release);
+                                smem + P::kStages * P::kStageBytes + (warp - 4) * 2048, nullptr, release);
             else release();
             aph ^= 1;
         }
@@ -788,15 +855,15 @@ cudaError_t launch_pair(const ScaledGemmArgs &a, int clusters, cudaStream_t st)
     return launch_dependent_clusters(scaled_pair_kernel<FMT>, 2 * clusters, 2, kThreads, P::kSmem, st, a, maps);
 }
 
-template <int FMT, bool DUAL, int BN>
+template <int FMT, bool DUAL, int BN, bool SPLIT = false>
 cudaError_t launch_plan(const ScaledGemmArgs &a, const Maps &maps, int ctas, cudaStream_t st)
 {
-    using P = Plan<FMT, DUAL, BN>;
-    auto k = scaled_gemm_kernel<FMT, DUAL, BN>;
+    using P = Plan<FMT, DUAL, BN, SPLIT>;
+    auto k = scaled_gemm_kernel<FMT, DUAL, BN, SPLIT>;
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = set_shared(k, P::kSmem, ready);
     if (e != cudaSuccess) return e;
-    return launch_dependent(k, ctas, kThreads, P::kSmem, st, a, maps);
+    return launch_dependent_clusters(k, ctas, SPLIT ? 2 : 1, kThreads, P::kSmem, st, a, maps);
 }
 
 template <int FMT, bool DUAL>
@@ -827,6 +894,11 @@ cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
     if (!DUAL && tiles(64) <= sms) bn = 64;
     const long long n = tiles(DUAL ? bn / 2 : bn);
     const int ctas = (int)(n < sms ? n : sms);
+    constexpr int kNarrow = DUAL ? 128 : 64, kStepK = kNv ? 256 : 128;
+    // Half of the K steps on a second CTA, where they are worth the exchange (about 1.5 us).  us, one CTA / two, at
+    // 8, 16 and 32 steps: 1 x 4096 x 2048 NVFP4 4.6 / 5.3, 16 x 4096 x 4096 NVFP4 6.7 / 6.4, 16 x 4096 x 4096 MXFP8 9.1 / 7.6,
+    // 1 x 4096 x 8192 NVFP4 10.7 / 8.6.
+    const bool split = bn == kNarrow && a.R <= 32 && 2 * n <= sms && a.K >= 14 * kStepK;
     Maps maps;
     const uint64_t abytes = kNv ? a.K / 2 : a.K;
     bool ok = make_map_2d(&maps.a32, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, abytes, a.R, kStepBytes, 32,
@@ -846,6 +918,7 @@ cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
             ok = ok && make_map_4bit(&maps.w[i], w, a.K, (uint64_t)a.G * a.N, box);
     }
     if (!ok) return cudaErrorInvalidValue;
+    if (split) return launch_plan<FMT, DUAL, DUAL ? 128 : 64, true>(a, maps, 2 * (int)n, st);
     if (bn == 256) return launch_plan<FMT, DUAL, 256>(a, maps, ctas, st);
     if (bn == 128) return launch_plan<FMT, DUAL, 128>(a, maps, ctas, st);
     if constexpr (!DUAL) return launch_plan<FMT, DUAL, 64>(a, maps, ctas, st);

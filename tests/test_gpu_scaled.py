@@ -372,6 +372,28 @@ def test_gemm_depths(fmt, K, R, N):
     assert (np.abs(y.check() - want) <= product_error(K) * mag).all()
 
 
+@pytest.mark.parametrize("fmt,K", [(NV, 3584), (NV, 3776), (NV, 12288), (M8, 1792), (M8, 4224)])
+@pytest.mark.parametrize("sizes,N", [([1], 72), ([32], 1000), ([3, 0, 1, 7, 0], 264), ([31, 1], 64)])
+def test_gemm_few_rows_long_sums(fmt, K, sizes, N):
+    """Few rows and many K steps (the launch shape that halves them), both output types; the same bits every time."""
+    rng = np.random.default_rng(K + N)
+    G, R = len(sizes), sum(sizes)
+    offsets = np.concatenate([[0], np.cumsum(sizes)[:-1]]).astype(np.int32)
+    a, av = operand(rng, fmt, R, K, list(offsets))
+    w, wv, alpha = weights(rng, fmt, G, N, K)
+    want, mag = grouped(av, wv, list(offsets), alpha)
+    for dt in (torch.float32, torch.bfloat16):
+        y, ws = Out((R, N), dt), workspace()
+        first = None
+        for _ in range(3):
+            qm.moe_scaled_gemm(fmt, a, w, R, N, K, G, gpu(offsets) if G > 1 else None, y.t, ws)
+            first = y.t.clone() if first is None else first
+            assert torch.equal(first, y.t)
+        assert qm.moe_get_device_status(ws) == 0
+        tol = product_error(K) * mag + (2.0 ** -8 * np.abs(want) if dt == torch.bfloat16 else 0)
+        assert (np.abs(y.check() - want) <= tol).all()
+
+
 @pytest.mark.parametrize("fmt", [NV, M8])
 def test_gemm_many_tiles(fmt):
     """More tiles than SMs, several row tiles a group: spot rows and columns."""
@@ -437,7 +459,7 @@ def test_gemm_reports_bad_offsets(off):
 
 @pytest.mark.parametrize("fmt", [NV, M8])
 @pytest.mark.parametrize("groups", ["one_row", "over_a_tile", "empty_groups", "small", "many"])
-@pytest.mark.parametrize("inter,K", [(128, 256), (384, 128), (256, 640)])
+@pytest.mark.parametrize("inter,K", [(128, 256), (384, 128), (256, 640), (128, 3840)])
 def test_swiglu(fmt, groups, inter, K):
     inter = inter + 64 if fmt == NV else inter
     sizes = GROUPS[groups]

@@ -212,3 +212,18 @@ def test_example_runs():
     import scaled_layers
     d = scaled_layers.run(dataclasses.replace(SMALL, hidden=512), tokens=48, layers=3)
     assert len(d) == 3 and all(0 < v < 0.5 for v in d)
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_waits_that_run_out_are_reported(T):
+    """A limit of one poll on the in-kernel waits: MOE_ERR_TIMEOUT in the status word, the kernels return, and the same
+    workspace serves the next call."""
+    host, layer = make(SMALL, NV)
+    x = tensor_x(SMALL, T, 2)
+    want = forward(layer, x, T)[0]
+    y, ws = torch.empty_like(want), qm.scaled_workspace(layer.cfg, NV, T)
+    short = qm.config_of(SMALL, wait_polls=1)
+    qm.moe_scaled_forward(short, layer.w, x, T, None, None, y, None, None, None, ws)
+    assert qm.moe_get_device_status(ws) == qm.MOE_ERR_TIMEOUT
+    qm.moe_scaled_forward(layer.cfg, layer.w, x, T, None, None, y, None, None, None, ws)
+    assert qm.moe_get_device_status(ws) == 0 and torch.equal(y, want)
