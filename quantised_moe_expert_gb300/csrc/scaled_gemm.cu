@@ -42,7 +42,9 @@ struct Plan {
     static constexpr int kABytes = 128 * kStepBytes, kBBytes = BN * kStepBytes;
     static constexpr int kBTxBytes = kNv ? kBBytes : kBBytes / 2;   // a widened copy counts the codes, not the padding
     static constexpr int kSfaBytes = kTilesK * kScaleTile, kSfbBytes = kChunks * kTilesK * kScaleTile;
-    static constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
+    // shared memory: the stages' codes (whole 1024-byte swizzle atoms), then their scales
+    static constexpr int kCodeBytes = kABytes + kBBytes, kSfBytes = kSfaBytes + kSfbBytes;
+    static_assert(kCodeBytes % 1024 == 0, "swizzle atoms");
     static constexpr int kStages = BN == 256 ? (DUAL || !kNv ? 4 : 3) : BN == 128 ? 5 : 7;
     static constexpr int kStaged = BN == 256 && !kNv ? 32 : 64;      // columns an epilogue warp stages at a time
     static constexpr int kOutBytes = DUAL || BN == 64 ? 0 : 8 * 32 * kStaged * 2;
@@ -50,7 +52,8 @@ struct Plan {
     static constexpr int kSfCols = 4 * kTilesK * (1 + kChunks);   // tensor-memory columns of a stage's scales
     static constexpr int kPartCols = (DUAL ? 2 : 1) * kOutN / 2;     // accumulator columns of an epilogue warp
     static constexpr int kPartBytes = SPLIT ? 2 * 32 * kPartCols * 4 : 0;   // the other CTA's sums (32 rows)
-    static constexpr int kSmem = kStages * kStageBytes + kOutBytes + kPartBytes + 1024;
+    static constexpr int kSfAt = kStages * kCodeBytes, kOutAt = kSfAt + kStages * kSfBytes, kPartAt = kOutAt + kOutBytes;
+    static constexpr int kSmem = kPartAt + kPartBytes + 1024;
     static_assert(kAccs * BN + kStages * kSfCols <= 512, "tensor memory");
 };
 
@@ -374,7 +377,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                     if (leader) fail();
                     break;
                 }
-                const uint32_t base = smem0 + st * P::kStageBytes, bar = smem_u32(&sh.full[st]);
+                const uint32_t base = smem0 + st * P::kCodeBytes, bar = smem_u32(&sh.full[st]);
                 if (warp == 0) {
                     if (leader) {
                         mbar_arrive_expect_tx(bar, boxes * 32 * kStepBytes + P::kBTxBytes);
@@ -390,7 +393,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                     }
                 } else if (leader) {
                     const int bytes = min(P::kTilesK, ct - ks * P::kTilesK) * kScaleTile;
-                    const uint32_t sfa = base + P::kABytes + P::kBBytes, sfb = sfa + P::kSfaBytes;
+                    const uint32_t sfa = smem0 + P::kSfAt + st * P::kSfBytes, sfb = sfa + P::kSfaBytes;
                     const size_t k0 = (size_t)ks * P::kTilesK * kScaleTile;
                     mbar_arrive_expect_tx(bar, bytes * (second ? 3 : 2));
                     bulk_load(sfb, pb + k0, bytes, bar);
@@ -429,9 +432,9 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.full[st]), ph, a.wait_limit, abort));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t base = smem0 + st * P::kStageBytes;
+                const uint32_t base = smem0 + st * P::kCodeBytes;
                 const uint32_t sfa = sf0 + st * P::kSfCols, sfb = sfa + 4 * P::kTilesK + sub;
-                const uint32_t sfa_s = base + P::kABytes + P::kBBytes, sfb_s = sfa_s + P::kSfaBytes;
+                const uint32_t sfa_s = smem0 + P::kSfAt + st * P::kSfBytes, sfb_s = sfa_s + P::kSfaBytes;
 #pragma unroll
                 for (int j = 0; j < P::kTilesK; ++j) {
                     tmem_cp_scales<1>(sfa + 4 * j, desc_scales(sfa_s + j * kScaleTile), leader);
@@ -503,7 +506,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             };
             const float4 *part = nullptr;
             if constexpr (SPLIT) {
-                float4 *const mine = reinterpret_cast<float4 *>(smem + P::kStages * P::kStageBytes + P::kOutBytes) + half * 8 * P::kPartCols;
+                float4 *const mine = reinterpret_cast<float4 *>(smem + P::kPartAt) + half * 8 * P::kPartCols;
                 if (rank) {
                     if (any) {
                         const uint32_t to = mapa_u32(smem_u32(mine), 0) + lane * 16;
@@ -535,7 +538,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 release();
             } else if constexpr (!DUAL) {
                 store_rows<kCols, P::kStaged>(a, d, (size_t)t.row0 + quad * 32, t.rows - quad * 32, col0, s0, lane,
-                                  smem + P::kStages * P::kStageBytes + (warp - 4) * (P::kOutBytes / 8), part, release);
+                                  smem + P::kOutAt + (warp - 4) * (P::kOutBytes / 8), part, release);
             } else {
                 uint32_t u[kCols / 16][16], u2[kCols / 16][16];          // gate and up products
 #pragma unroll
@@ -627,10 +630,11 @@ struct PairPlan {
     static constexpr int kABytes = 128 * kStepBytes, kBBytes = 128 * kStepBytes;
     static constexpr int kBTxBytes = kNv ? kBBytes : kBBytes / 2;
     static constexpr int kSfBytes = kTilesK * kScaleTile;                   // one row tile's scales of a step
-    static constexpr int kStageBytes = kABytes + kBBytes + 3 * kSfBytes;
+    static constexpr int kCodeBytes = kABytes + kBBytes;
     static constexpr int kStages = kNv ? 5 : 6;
     static constexpr int kSfCols = 4 * kTilesK * 3;
-    static constexpr int kSmem = kStages * kStageBytes + 16384 + 1024;
+    static constexpr int kSfAt = kStages * kCodeBytes, kOutAt = kSfAt + kStages * 3 * kSfBytes;
+    static constexpr int kSmem = kOutAt + 16384 + 1024;
     static_assert(256 + kStages * kSfCols <= 512, "tensor memory");
 };
 constexpr int kPairRows = 256;
@@ -707,7 +711,7 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                     if (leader) fail();
                     break;
                 }
-                const uint32_t base = smem0 + st * P::kStageBytes, bar = mapa_u32(smem_u32(&sh.full[st]), 0);
+                const uint32_t base = smem0 + st * P::kCodeBytes, bar = mapa_u32(smem_u32(&sh.full[st]), 0);
                 if (warp == 0) {
                     if (leader) {
                         if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[st]), 2 * (P::kABytes + P::kBTxBytes));
@@ -715,7 +719,7 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                         tma_load_2d_pair(base, &maps.a, ks * kStepBytes, arow, bar);
                     }
                 } else if (leader) {
-                    const uint32_t sf = base + P::kABytes + P::kBBytes;
+                    const uint32_t sf = smem0 + P::kSfAt + st * 3 * P::kSfBytes;
                     if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[st]), 2 * 3 * P::kSfBytes);
                     tma_load_2d_pair(sf, &maps.sa, 0, sa + ks * P::kTilesK, bar);
                     tma_load_2d_pair(sf + P::kSfBytes, &maps.sw, 0, sw + ks * P::kTilesK, bar);
@@ -750,7 +754,7 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait_cluster(smem_u32(&sh.full[st]), ph, a.wait_limit, abort));
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t base = smem0 + st * P::kStageBytes, sf = base + P::kABytes + P::kBBytes;
+                const uint32_t base = smem0 + st * P::kCodeBytes, sf = smem0 + P::kSfAt + st * 3 * P::kSfBytes;
                 const uint32_t sfa = sf0 + st * P::kSfCols, sfb = sfa + 4 * P::kTilesK;
 #pragma unroll
                 for (int j = 0; j < P::kTilesK; ++j) {
@@ -807,7 +811,7 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             };
             if (any)
                 store_rows<128, 32>(a, tmem + half * 128 + ((uint32_t)(quad * 32) << 16), (size_t)t.row0 + r0, t.rows - r0, col0, s, lane,
-                                smem + P::kStages * P::kStageBytes + (warp - 4) * 2048, nullptr, release);
+                                smem + P::kOutAt + (warp - 4) * 2048, nullptr, release);
             else release();
             aph ^= 1;
         }
