@@ -272,17 +272,18 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
     } else
 #pragma unroll
     for (int c = 0; c < COLS; c += STAGED) {
-        // row r's chunk k at (k ^ r) % kChunks of its STAGED * 2 bytes: no bank is met twice in a phase
+        // row r's chunk k at k ^ r (rows of 128 bytes) or k ^ r / 2 (of 64) of the row: no bank is met twice in a phase
+        constexpr int kShift = STAGED == 32 ? 1 : 0;
 #pragma unroll
         for (int k = 0; k < kChunks; ++k)
-            *reinterpret_cast<uint4 *>(stage + lane * (STAGED * 2) + ((k ^ lane) % kChunks) * 16) =
+            *reinterpret_cast<uint4 *>(stage + lane * (STAGED * 2) + ((k ^ (lane >> kShift)) % kChunks) * 16) =
                 make_uint4(w[c / 2 + 4 * k], w[c / 2 + 4 * k + 1], w[c / 2 + 4 * k + 2], w[c / 2 + 4 * k + 3]);
         __syncwarp();
         const int k = lane % kChunks;
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
             const int r = i * (32 / kChunks) + lane / kChunks;
-            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * (STAGED * 2) + ((k ^ r) % kChunks) * 16);
+            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * (STAGED * 2) + ((k ^ (r >> kShift)) % kChunks) * 16);
             if (r < rows && col0 + c + 8 * k < a.N) *reinterpret_cast<uint4 *>(y + (size_t)r * a.N + c + 8 * k) = v;
         }
         __syncwarp();
