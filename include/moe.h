@@ -381,8 +381,9 @@ typedef struct moe_scaled_mat {
  *   y_out      bf16 [T, n] y rounded once, or NULL
  *   format, q  y as MOE_SCALED_NVFP4 (q->row_scale required) or
  *              MOE_SCALED_MXFP8 rows, one group; format 0 and q NULL for none.
- * The codes are rounded from the fp32 y, not from y_out.  n: a multiple of the
- * format's block (8 without one), at most 16384. */
+ * The codes are rounded from the fp32 y, not from y_out.  The sum of squares is
+ * an fp32 sum: |s| has to stay below about 1e19 / sqrt(n).  n: a multiple of
+ * the format's block (8 without one), at most 16384. */
 MOE_API int moe_add_rmsnorm(const uint16_t *x, const uint16_t *residual, const uint16_t *weight, float weight_offset,
                             float eps, int T, int n, uint16_t *sum_out, uint16_t *y_out, int format,
                             const moe_scaled_rows *q, void *stream);
@@ -424,8 +425,8 @@ MOE_API int moe_scaled_gemm(int format, const moe_scaled_rows *a, const moe_scal
 
 /* Two grouped products and SwiGLU: h = silu(a . gate_g^T) * (a . up_g^T) with both
  * products' factors, quantised to the rows' own format for the next product.
- *   h_scale  NVFP4: fp32 [G] calibrated factor g of h (fold it into the next
- *            matrices' alpha); MXFP8: NULL
+ *   h_scale  NVFP4: fp32 [G] calibrated factor g > 0 of h (fold it into the next
+ *            matrices' alpha; h beyond 2688 g saturates); MXFP8: NULL
  *   h        [R, inter] rows, same groups; h->row_scale must be NULL
  * inter: a multiple of 64 (NVFP4) or 128 (MXFP8). */
 MOE_API int moe_scaled_swiglu(int format, const moe_scaled_rows *a, const moe_scaled_mat *gate, const moe_scaled_mat *up,

@@ -9,7 +9,9 @@
 // each thread holds CH segments of 8 elements (one 16-byte load of bf16), neighbouring threads
 // neighbouring segments, so loads, code stores and bf16 stores are coalesced and a block's maximum is
 // one or two shuffles; the four scale bytes of a column tile are ORed over their lanes and written as
-// one word.
+// one word.  Measured: norm of 32768 x 2048 with residual to bf16 and MXFP8 (604 MB) 89.4 us, 6.76 TB/s, the rate
+// of a plain copy; 777 x 5120 7.8 us; one row 1.9 us behind another launch; 512 rows of 2048 into 9 expert-sorted
+// copies each 4.0 us.
 #include "scaled.cuh"
 #include "tc_ptx.cuh"
 
@@ -151,7 +153,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     // The successor may come in at once; beside a full grid that writes many copies a row only when the rows
     // are read, since its waiting blocks slow that one (512 rows into 9 copies each: 5.2 us against 4.0; the
     // norm of 777 x 5120 is faster with it, 7.9 us against 8.4).
-    const bool early = !a.ids || gridDim.x <= kEarlyBlocks;
+    const bool early = NORM || !a.ids || gridDim.x <= kEarlyBlocks;
     if (early) tc::pdl_trigger();
     tc::pdl_wait();
     const int tr = threadIdx.x % TPR;
