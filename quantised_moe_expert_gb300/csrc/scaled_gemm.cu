@@ -888,13 +888,14 @@ cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
     if constexpr (!DUAL) {
         // A pair of CTAs a tile: groups of 256 rows and more on average, a tile for every pair of SMs, and K steps
         // enough to pay for the longer way of a tile's first and last step.  us, one CTA / a pair: 8192 x 8192 x
-        // 4096 NVFP4 (16 steps) 119 / 105, MXFP8 (32) 192 / 156, 4096 x 4096 x 2048 NVFP4 (8) 23.7 / 23.8, 8192 x
-        // 2048 x 512 (2) 12.9 / 16.9; 1024 x 4096 x 4096 (64 pair tiles for 76 pairs) 10.6 / 11.0.
+        // 4096 NVFP4 (16 steps) 119 / 105, MXFP8 (32) 192 / 156, 8192 x 8192 x 2048 NVFP4 (8) 72.6 / 64.7, 4096 x 4096 x
+        // 1024 MXFP8 (8) 20.3 / 19.8; 5627 x 3400 x 896 MXFP8 (7) 22.1 / 22.3, 8192 x 2048 x 512 (4) 13.7 / 15.4;
+        // 1024 x 4096 x 4096 NVFP4 (64 pair tiles for 76 pairs) 10.6 / 11.0.
         using P = PairPlan<FMT>;
         const long long pairs = (a.R / kPairRows) * ((long long)(a.N + 255) / 256), ct = scaled_col_tiles(FMT, a.K);
         const bool coords = ((long long)a.G * ((a.N + kScaleRows - 1) / kScaleRows) + 1) * ct < 0x7FFFFFFFll &&
                             ((long long)a.R / kScaleRows + a.G + 1) * ct < 0x7FFFFFFFll;   // scale tiles as 32-bit coordinates
-        if (a.R / a.G >= kPairRows && pairs >= sms / 2 && a.K >= 12 * P::kStepK && coords) return launch_pair<FMT>(a, sms / 2, st);
+        if (a.R / a.G >= kPairRows && pairs >= sms / 2 && a.K >= 8 * P::kStepK && coords) return launch_pair<FMT>(a, sms / 2, st);
     }
     // The widest tile, or the narrowest of which there is at most one an SM.  us at 64 / 128 / 256 columns: 1 x 16384
     // x 2048 NVFP4 (256, 128, 64 tiles) 6.9 / 5.2 / 5.9, 512 x 4096 x 4096 (256, 128, 64) 11.6 / 7.9 / 10.4, 64 x 8192

@@ -410,7 +410,7 @@ def test_gemm_many_tiles(fmt):
     assert (np.abs(first - want) <= product_error(K) * mag).all()
 
 
-@pytest.mark.parametrize("fmt,K", [(NV, 2112), (M8, 1408)])
+@pytest.mark.parametrize("fmt,K", [(NV, 2112), (M8, 1408), (NV, 4416), (M8, 2304)])
 @pytest.mark.parametrize("offsets", [None, [0, 0, 257, 1500]])
 def test_gemm_large_groups(fmt, K, offsets):
     """Groups of many row tiles (the launch shape for them), rows and outputs that end inside a tile."""
