@@ -20,8 +20,8 @@
 // read every tile four times from shared memory: 8192 x 8192 x 4096 117 us against 112 us.)
 //
 // Bounds and measurements (hidden 2048, inter 512, 257 groups): 512 tokens, NVFP4, the gate/up pair 51 us (6.1 TB/s
-// of weights and rows) and the down products 32 us (5.5 TB/s): HBM.  4096 tokens, MXFP8, 93 and 66 us: the copy that
-// widens the 4-bit codes, 32 bytes of shared memory a cycle.  One token, 9 groups, 7.4 and 4.4 us: launch, and 300
+// of weights and rows) and the down products 32 us (5.5 TB/s): HBM.  4096 tokens, MXFP8, 93 and 66 us: the copies
+// that widen the 4-bit codes, about 32 bytes of shared memory a cycle.  One token, 9 groups, 7.4 and 4.4 us: launch, and 300
 // to 430 ns a K step for the issue of its scale copies and MMAs.  8192 x 8192 x 4096 NVFP4 101 us, 5.4 PFLOP/s: refilling
 // stages from L2 (see the pair below).
 #include "scaled.cuh"
