@@ -52,8 +52,8 @@ struct Plan {
     static constexpr int kCodeBytes = kABytes + kBBytes, kSfBytes = kSfaBytes + kSfbBytes;
     static_assert(kCodeBytes % 1024 == 0, "swizzle atoms");
     static constexpr int kStages = BN == 256 ? (DUAL || !kNv ? 4 : 3) : BN == 128 ? 5 : 7;
-    static constexpr int kStaged = BN == 256 && !kNv ? 32 : 64;      // columns an epilogue warp stages at a time
-    static constexpr int kOutBytes = DUAL || BN == 64 ? 0 : 8 * 32 * kStaged * 2;
+    static constexpr int kStaged = BN == 256 && !kNv ? 64 : 128;     // bytes of a row that an epilogue warp stages at a time
+    static constexpr int kOutBytes = DUAL || BN == 64 ? 0 : 8 * 32 * kStaged;
     static constexpr int kAccs = BN == 256 ? 1 : 2;          // accumulator buffers
     static constexpr int kSfCols = 4 * kTilesK * (1 + kChunks);   // tensor-memory columns of a stage's scales
     static constexpr int kPartCols = (DUAL ? 2 : 1) * kOutN / 2;     // accumulator columns of an epilogue warp
@@ -203,16 +203,6 @@ __device__ __forceinline__ void mma_scaled(uint32_t d, uint64_t adesc, uint64_t 
 
 __device__ __forceinline__ float silu(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
-// 16 accumulators times s, as fp32: the first n (a multiple of 8).
-__device__ __forceinline__ void store_f32(float *p, const uint32_t (&v)[16], float s, int n)
-{
-#pragma unroll
-    for (int i = 0; i < 16; i += 4)
-        if (i < n)
-            *reinterpret_cast<float4 *>(p + i) = make_float4(__uint_as_float(v[i]) * s, __uint_as_float(v[i + 1]) * s,
-                                                             __uint_as_float(v[i + 2]) * s, __uint_as_float(v[i + 3]) * s);
-}
-
 // Adds the other CTA's sums of 16 columns from `col` on to this row's: part[column / 4][row], or null.
 __device__ __forceinline__ void add_part(uint32_t (&u)[16], const float4 *part, int col, int lane)
 {
@@ -227,15 +217,41 @@ __device__ __forceinline__ void add_part(uint32_t (&u)[16], const float4 *part, 
     }
 }
 
+// 32 rows of ROW_BYTES (64 or 128), a lane a row in 16-byte chunks w[], to rows `pitch` bytes apart from `dst` on, the
+// first `rows` rows and `chunks` chunks of each, through `stage`: 4 or 8 lanes write a row's bytes together.
+template <int ROW_BYTES>
+__device__ __forceinline__ void store_staged(uint8_t *dst, size_t pitch, const uint32_t *w, int rows, int chunks, int lane, uint8_t *stage)
+{
+    // row r's chunk k at k ^ r (rows of 128 bytes) or k ^ r / 2 (of 64) of the row: no bank is met twice in a phase
+    constexpr int kChunks = ROW_BYTES / 16, kShift = ROW_BYTES == 64 ? 1 : 0;
+#pragma unroll
+    for (int k = 0; k < kChunks; ++k)
+        *reinterpret_cast<uint4 *>(stage + lane * ROW_BYTES + ((k ^ (lane >> kShift)) % kChunks) * 16) =
+            make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    __syncwarp();
+    const int k = lane % kChunks;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int r = i * (32 / kChunks) + lane / kChunks;
+        const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * ROW_BYTES + ((k ^ (r >> kShift)) % kChunks) * 16);
+        if (r < rows && k < chunks) *reinterpret_cast<uint4 *>(dst + r * pitch + 16 * k) = v;
+    }
+    __syncwarp();
+}
+
 // COLS accumulator columns of the warp's 32 rows (from `row` on, the first `rows` of them exist) to y;
-// release() once they are in registers.  bf16 outputs go through `stage`, the warp's part of shared memory,
-// STAGED columns at a time (64, or 32 where another stage of operands fits then), so that 8 or 4 lanes write a
-// row's bytes together: a lane of its own row touches 32 lines in every store, which costs the load/store
-// unit a cycle a line or more (4300 cycles a 128 x 256 tile, more than its products at K = 512).
-template <int COLS, int STAGED, class Release>
+// release() once they are in registers.  Outputs go through `stage`, the warp's part of shared memory, STAGE bytes
+// a row at a time (128, or 64 where another stage of operands fits then): a lane of its own row touches 32
+// lines in every store, which costs the load/store unit a cycle a line or more (4300 cycles a 128 x 256 tile
+// of bf16, more than its products at K = 512; the routed layer of 4096 tokens, whose down products are 302 MB
+// of fp32, took 363 us with such stores, against 283).
+template <int COLS, int STAGE, class Release>
 __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, size_t row, int rows, int col0, float s, int lane,
                                            uint8_t *stage, const float4 *part, Release release)
 {
+    constexpr int kBatch = COLS < 64 ? COLS : 64;
+    const size_t pitch = (size_t)a.N * (a.y_f32 ? 4 : 2);
+    uint8_t *y = static_cast<uint8_t *>(a.y) + row * pitch + (size_t)col0 * (a.y_f32 ? 4 : 2);
     if (a.y_f32) {
         uint32_t u[COLS / 16][16];
 #pragma unroll
@@ -243,13 +259,28 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
         tmem_ld_wait();
         release();
 #pragma unroll
-        for (int i = 0; i < COLS / 16; ++i) add_part(u[i], part, 16 * i, lane);
+        for (int i = 0; i < COLS / 16; ++i) {
+            add_part(u[i], part, 16 * i, lane);
 #pragma unroll
-        for (int i = 0; i < COLS / 16; ++i)
-            if (lane < rows) store_f32(static_cast<float *>(a.y) + (row + lane) * a.N + col0 + 16 * i, u[i], s, a.N - col0 - 16 * i);
+            for (int k = 0; k < 16; ++k) u[i][k] = __float_as_uint(__uint_as_float(u[i][k]) * s);
+        }
+        if constexpr (COLS < 64) {                         // few tiles: the shortest way (0.15 us of 4.7 at one token)
+#pragma unroll
+            for (int i = 0; i < COLS; i += 4)
+                if (lane < rows && col0 + i < a.N)
+                    *reinterpret_cast<uint4 *>(y + lane * pitch + 4 * i) =
+                        make_uint4(u[i / 16][i % 16], u[i / 16][i % 16 + 1], u[i / 16][i % 16 + 2], u[i / 16][i % 16 + 3]);
+        } else {
+#pragma unroll
+            for (int c = 0; c < COLS; c += STAGE / 4) {
+                uint32_t w[STAGE / 4];
+#pragma unroll
+                for (int i = 0; i < STAGE / 4; ++i) w[i] = u[(c + i) / 16][i % 16];
+                store_staged<STAGE>(y + 4 * c, pitch, w, rows, (a.N - col0 - c) / 4, lane, stage);
+            }
+        }
         return;
     }
-    constexpr int kBatch = COLS < 64 ? COLS : 64, kChunks = STAGED / 8;      // 16-byte chunks of a row
     uint32_t w[COLS / 2];
 #pragma unroll
     for (int c = 0; c < COLS; c += kBatch) {
@@ -267,32 +298,19 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
         }
     }
     release();
-    uint16_t *y = static_cast<uint16_t *>(a.y) + row * a.N + col0;
-    if constexpr (COLS < 64) {                             // few tiles: the shortest way (0.15 us of 4.7 at one token)
-        if (lane < rows) {
+    if constexpr (COLS < 64) {
 #pragma unroll
-            for (int i = 0; i < COLS / 2; i += 4)
-                if (col0 + 2 * i < a.N)
-                    *reinterpret_cast<uint4 *>(y + (size_t)lane * a.N + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+        for (int i = 0; i < COLS / 2; i += 4)
+            if (lane < rows && col0 + 2 * i < a.N)
+                *reinterpret_cast<uint4 *>(y + lane * pitch + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else {
+#pragma unroll
+        for (int c = 0; c < COLS / 2; c += STAGE / 4) {
+            uint32_t v[STAGE / 4];
+#pragma unroll
+            for (int i = 0; i < STAGE / 4; ++i) v[i] = w[c + i];
+            store_staged<STAGE>(y + 4 * c, pitch, v, rows, (a.N - col0 - 2 * c) / 8, lane, stage);
         }
-    } else
-#pragma unroll
-    for (int c = 0; c < COLS; c += STAGED) {
-        // row r's chunk k at k ^ r (rows of 128 bytes) or k ^ r / 2 (of 64) of the row: no bank is met twice in a phase
-        constexpr int kShift = STAGED == 32 ? 1 : 0;
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k)
-            *reinterpret_cast<uint4 *>(stage + lane * (STAGED * 2) + ((k ^ (lane >> kShift)) % kChunks) * 16) =
-                make_uint4(w[c / 2 + 4 * k], w[c / 2 + 4 * k + 1], w[c / 2 + 4 * k + 2], w[c / 2 + 4 * k + 3]);
-        __syncwarp();
-        const int k = lane % kChunks;
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-            const int r = i * (32 / kChunks) + lane / kChunks;
-            const uint4 v = *reinterpret_cast<const uint4 *>(stage + r * (STAGED * 2) + ((k ^ (r >> kShift)) % kChunks) * 16);
-            if (r < rows && col0 + c + 8 * k < a.N) *reinterpret_cast<uint4 *>(y + (size_t)r * a.N + c + 8 * k) = v;
-        }
-        __syncwarp();
     }
 }
 
@@ -817,7 +835,7 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 if (lane == 0) mbar_arrive_cluster(empty);
             };
             if (any)
-                store_rows<128, 32>(a, tmem + half * 128 + ((uint32_t)(quad * 32) << 16), (size_t)t.row0 + r0, t.rows - r0, col0, s, lane,
+                store_rows<128, 64>(a, tmem + half * 128 + ((uint32_t)(quad * 32) << 16), (size_t)t.row0 + r0, t.rows - r0, col0, s, lane,
                                 smem + P::kOutAt + (warp - 4) * 2048, nullptr, release);
             else release();
             aph ^= 1;
