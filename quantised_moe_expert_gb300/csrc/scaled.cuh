@@ -4,6 +4,8 @@
 
 #include "moe_common.cuh"
 
+#include <atomic>
+
 namespace qmoe {
 
 // Elements per block, codes per byte and columns of a K step of each format.
@@ -126,6 +128,18 @@ cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block
     return launch_dependent_clusters(kernel, grid, 1, block, smem, st, args...);
 }
 
+// Once per kernel and device: its dynamic shared memory (`ready`: the devices on which that is done).
+template <class K>
+cudaError_t set_shared(K kernel, int bytes, std::atomic<uint64_t> &ready)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev < 64 && (ready.load(std::memory_order_relaxed) >> dev & 1))) return e;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
+    return e;
+}
+
 // ---------------------------------------------------------------- kernel arguments
 
 // Rows to block-scaled rows (scaled_rows.cu).
@@ -163,5 +177,6 @@ struct ScaledGemmArgs {
     long long wait_limit;
 };
 cudaError_t launch_scaled_gemm(const ScaledGemmArgs &a, int fmt, bool swiglu, cudaStream_t st);
+cudaError_t launch_scaled_vec(const ScaledGemmArgs &a, int fmt, bool swiglu, cudaStream_t st);   // few rows (scaled_vec.cu)
 
 }  // namespace qmoe

@@ -21,8 +21,9 @@
 //
 // Bounds and measurements (hidden 2048, inter 512, 257 groups): 512 tokens, NVFP4, the gate/up pair 51 us (6.1 TB/s
 // of weights and rows) and the down products 32 us (5.5 TB/s): HBM.  4096 tokens, MXFP8, 93 and 66 us: the copies
-// that widen the 4-bit codes, about 32 bytes of shared memory a cycle.  One token, 9 groups, 7.4 and 4.4 us: launch, and 300
-// to 430 ns a K step for the issue of its scale copies and MMAs.  8192 x 8192 x 4096 NVFP4 101 us, 5.4 PFLOP/s: refilling
+// that widen the 4-bit codes, about 32 bytes of shared memory a cycle.  Small products are paced by 300 to 430 ns a
+// K step for the issue of its scale copies and MMAs (16 x 4096 x 2048 NVFP4 4.5 us); those of fewest rows go to
+// scaled_vec.cu.  8192 x 8192 x 4096 NVFP4 101 us, 5.4 PFLOP/s: refilling
 // stages from L2 (see the pair below).
 #include "scaled.cuh"
 #include "tc_ptx.cuh"
@@ -846,18 +847,6 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     if (warp == 3) tmem_dealloc_pair(tmem, 512);
 }
 
-// Once per kernel and device: its dynamic shared memory (`ready`: the devices on which that is done).
-template <class K>
-cudaError_t set_shared(K kernel, int bytes, std::atomic<uint64_t> &ready)
-{
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e != cudaSuccess || (dev < 64 && (ready.load(std::memory_order_relaxed) >> dev & 1))) return e;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e == cudaSuccess && dev < 64) ready.fetch_or(1ull << dev, std::memory_order_relaxed);
-    return e;
-}
-
 // Scale tiles as rows of 128 32-bit words, in boxes of `box` tiles.
 bool make_map_scales(CUtensorMap *m, const uint8_t *p, uint64_t tiles, uint32_t box)
 {
@@ -959,6 +948,13 @@ cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
 
 cudaError_t launch_scaled_gemm(const ScaledGemmArgs &a, int fmt, bool swiglu, cudaStream_t st)
 {
+    // Few rows a row at a time (scaled_vec.cu): up to 10240 outputs, twice that where groups would share no tiles anyway.
+    // us, tiles / rows: 1 x 4096 x 2048 (4096 outputs) NVFP4 4.5 / 3.0, MXFP8 5.9 / 2.8; 2 x 4096 x 2048 (8192) 4.5 / 3.8, 5.8 / 3.5;
+    // 2 x 4096 x 8192 (8192) 8.5 / 8.5, 11.4 / 7.9; 4 x 4096 x 2048 (16384) 4.5 / 6.4, 5.9 / 5.9; the SwiGLU of 1, 2 and 3 tokens
+    // of 9 experts each, inter 512 (9216, 18432, 27648 gate and up outputs) 7.4 / 5.0, 7.9 / 6.9, 9.3 / 11.2.  A single
+    // step (K <= 256) stays with the tiles, whose steps have nothing to queue behind (4096 outputs: 2.8 / 1.9).
+    const long long outputs = (long long)a.R * ((a.N + 31) / 32 * 32) * (swiglu ? 2 : 1);
+    if (a.K > 256 && outputs <= (a.offsets ? 20480 : 10240)) return launch_scaled_vec(a, fmt, swiglu, st);
     if (fmt == MOE_SCALED_NVFP4)
         return swiglu ? launch_fmt<MOE_SCALED_NVFP4, true>(a, st) : launch_fmt<MOE_SCALED_NVFP4, false>(a, st);
     return swiglu ? launch_fmt<MOE_SCALED_MXFP8, true>(a, st) : launch_fmt<MOE_SCALED_MXFP8, false>(a, st);
