@@ -14,11 +14,11 @@
 // byte's two codes an instruction, 64 lanes a cycle) is most of the work: a warp has two tiles of weights for each
 // conversion of its activations.
 //
-// 1 x 4096 x 2048: NVFP4 3.0 us (1.6 TB/s from L2), MXFP8 2.8, against 4.5 and 5.9 of a tile; 1 x 4096 x 8192 NVFP4 6.7 against
-// 8.5.  One token of 9 experts, hidden 2048, inter 512: 5.0 and 3.8 us against 7.4 and 4.4.  1.9 us are launch to
-// launch, 0.5 the search for a row's group.  Ways that were slower: packed fp16 FMAs (4.0 where this takes 3.0), byte dot
-// products of looked-up codes (4.3), m16n8k32 of E4M3 (4.7), the activations converted once into shared
-// memory (3.8), the scales fetched by column tiles into shared memory (+0.5 us at K = 512).
+// 1 x 4096 x 2048: 2.8 us in either format (1.7 TB/s from L2), against 4.5 (NVFP4) and 5.9 of a tile; 1 x 4096 x 8192 NVFP4 6.7
+// against 8.5.  One token of 9 experts, hidden 2048, inter 512, NVFP4: 4.7 and 3.7 us against 7.4 and 4.4.  1.9 us are
+// launch to launch, 0.5 the search for a row's group.  Ways that were slower, where this took 3.0 us: packed fp16 FMAs
+// (4.0), byte dot products of looked-up codes (4.3), m16n8k32 of E4M3 (4.7), the activations converted once into
+// shared memory (3.8); the scales fetched by column tiles into shared memory cost 0.5 us at K = 512.
 #include "scaled.cuh"
 #include "tc_ptx.cuh"
 
@@ -80,39 +80,48 @@ __device__ __forceinline__ uint32_t load_scales(const uint8_t *p)
 // A CTA has 32 outputs of one row.  A warp has two tiles of 16 weight rows, the CTA's or a gate tile and its up tile; S
 // warps share them, taking their steps in turn.
 template <int FMT, bool DUAL, int S, int kAhead>
-__global__ void __launch_bounds__(32 * (DUAL ? 2 : 1) * S)
+__global__ void __launch_bounds__(32 * (DUAL ? 2 : 1) * S, DUAL && S == 4 && kAhead == 2 ? 2 : 1)
 scaled_vec_kernel(const __grid_constant__ ScaledGemmArgs a, int blocks)
 {
     constexpr bool kNv = FMT == MOE_SCALED_NVFP4;
     constexpr int kMats = DUAL ? 2 : 1, kWarps = kMats * S, kThreads = 32 * kWarps, kX = kNv ? 1 : 2;
-    __shared__ uint32_t count[kWarps];
+    __shared__ uint32_t count[kWarps], begin[kWarps];
     __shared__ float part[S][kMats][kOutputs];
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int row = blockIdx.x / blocks, block = blockIdx.x - row * blocks, n0 = block * kOutputs;
     pdl_wait();
 
-    // the row's group: as many groups start at or before it, less one; malformed offsets in the upper half
+    // the row's group: as many groups start at or before it, less one, the last of them at `start`; malformed offsets
+    // counted in the upper half
     int g = 0, start = 0;
     if (a.offsets) {
-        uint32_t c = 0;
+        uint32_t c = 0, m = 0;
         for (int i = threadIdx.x; i < a.G; i += kThreads) {
             const int o = a.offsets[i], next = i + 1 < a.G ? a.offsets[i + 1] : a.R;
+            m = o <= row ? max(m, (uint32_t)o) : m;
             c += (o <= row) + ((o < 0 || o > a.R || next < o) ? 1u << 16 : 0u);
         }
         c = __reduce_add_sync(0xFFFFFFFFu, c);
-        if (lane == 0) count[warp] = c;
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
+        if (lane == 0) {
+            count[warp] = c;
+            begin[warp] = m;
+        }
         __syncthreads();
-        c = 0;
+        c = m = 0;
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) c += count[i];
+        for (int i = 0; i < kWarps; ++i) {
+            c += count[i];
+            m = max(m, begin[i]);
+        }
         if (c >> 16) {
             if (blockIdx.x == 0 && threadIdx.x == 0) record_status(a.status, MOE_ERR_DEVICE);
             return;
         }
         if (c == 0) return;                                                       // before the first group
         g = (int)c - 1;
-        start = a.offsets[g];
+        start = (int)m;
     }
 
     const int slice = warp / kMats, first = DUAL ? (warp & 1) * 16 : 0;
@@ -267,14 +276,16 @@ cudaError_t launch_vec(const ScaledGemmArgs &a, cudaStream_t st)
 template <int FMT, bool DUAL>
 cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
 {
-    // Warps that share a tile's steps, and steps that each loads together.  With an SM to itself a CTA takes more
-    // warps: 1 x 2048 x 512 1.9 us with (4, 1), 2.3 with (2, 2), but 18 rows of experts' down products 5.5 and 4.2; the SwiGLU
-    // of one token 4.9 with (8, 2), 5.2 with (4, 2), that of two 8.8 and 6.7.
-    const int steps = (a.K + kChunk - 1) / kChunk;
-    const bool spread = (long long)a.R * ((a.N + kOutputs - 1) / kOutputs) <= device_sm_count();
-    if (steps <= 4) return spread ? launch_vec<FMT, DUAL, 4, 1>(a, st) : launch_vec<FMT, DUAL, 2, 2>(a, st);
-    if (steps <= 8 || (DUAL && !spread)) return launch_vec<FMT, DUAL, 4, 2>(a, st);
-    return launch_vec<FMT, DUAL, 8, 2>(a, st);
+    // Warps that share a tile's steps, and steps that each loads together.  Short sums: more warps while all CTAs
+    // run at once (9 rows of experts' down products behind their SwiGLU 8.4 us with (4, 1), 9.0 with (2, 2); 18 rows 5.5 and 4.2 by
+    // themselves).  The SwiGLU with an SM for every CTA, few warps that load far ahead, else two CTAs an SM: one token's 4.7
+    // us with (4, 4), 5.0 with (8, 2), 5.2 with (4, 2); two tokens' 8.8 with (8, 2), 6.7 with (4, 2).
+    const int steps = (a.K + kChunk - 1) / kChunk, sms = device_sm_count();
+    const long long ctas = (long long)a.R * ((a.N + kOutputs - 1) / kOutputs);
+    if (steps <= 4) return ctas <= 4 * sms ? launch_vec<FMT, DUAL, 4, 1>(a, st) : launch_vec<FMT, DUAL, 2, 2>(a, st);
+    if (steps <= 8 || (DUAL && ctas > sms)) return launch_vec<FMT, DUAL, 4, 2>(a, st);
+    if constexpr (DUAL) return launch_vec<FMT, DUAL, 4, 4>(a, st);
+    else return launch_vec<FMT, DUAL, 8, 2>(a, st);
 }
 
 }  // namespace

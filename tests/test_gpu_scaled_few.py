@@ -41,7 +41,7 @@ def test_gemm_few_many_groups(monkeypatch, fmt, K):
 
 @pytest.mark.parametrize("fmt", [NV, M8])
 @pytest.mark.parametrize("R,G,N", [(1, 1, 4864), (1, 1, 4872), (1, 1, 10240), (1, 1, 10248), (2, 1, 5120), (3, 1, 3416), (10, 10, 2048),
-                                   (10, 10, 2056), (1, 3, 20480)])
+                                   (10, 10, 2056), (1, 3, 20480), (10, 10, 4096), (10, 10, 4104)])
 @pytest.mark.parametrize("K", [384, 640, 1152])
 def test_gemm_around_the_limits(fmt, R, G, N, K):
     """A CTA for every SM and more; as many outputs as run a row at a time and a few more."""
