@@ -250,7 +250,7 @@ template <int COLS, int STAGE, class Release>
 __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, size_t row, int rows, int col0, float s, int lane,
                                            uint8_t *stage, const float4 *part, Release release)
 {
-    constexpr int kBatch = COLS < 64 ? COLS : 64;
+    constexpr int kBatch = COLS;
     const size_t pitch = (size_t)a.N * (a.y_f32 ? 4 : 2);
     uint8_t *y = static_cast<uint8_t *>(a.y) + row * pitch + (size_t)col0 * (a.y_f32 ? 4 : 2);
     if (a.y_f32) {
@@ -289,6 +289,7 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
 #pragma unroll
         for (int i = 0; i < kBatch / 16; ++i) tmem_ld16(d + c + 16 * i, u[i]);
         tmem_ld_wait();
+        release();
 #pragma unroll
         for (int i = 0; i < kBatch / 16; ++i) add_part(u[i], part, c + 16 * i, lane);
 #pragma unroll
@@ -298,7 +299,6 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
             w[c / 2 + i] = *reinterpret_cast<const uint32_t *>(&b);
         }
     }
-    release();
     if constexpr (COLS < 64) {
 #pragma unroll
         for (int i = 0; i < COLS / 2; i += 4)
@@ -512,17 +512,20 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         uint32_t aph = 0;
         for (int tile = first_tile; tile < total; tile += stride) {
             const Tile t = tile_at<kScaleRows>(a, sh, tile, n_tiles);
+            const int r = quad * 32 + lane, col0 = t.nt * P::kOutN + half * kCols;
+            const uint32_t d = tmem + acc * BN + half * kCols + ((uint32_t)(quad * 32) << 16);
+            const bool any = quad * 32 < t.rows && col0 < a.N, live = any && r < t.rows;
+            const size_t row = (size_t)t.row0 + r;
+            // factors on their way under the products
+            const float rs = live && a.a_row_scale ? __ldg(a.a_row_scale + row) : 1.0f;
+            const float s0 = rs * (a.alpha[0] ? __ldg(a.alpha[0] + t.g) : 1.0f);
+            const float s1 = DUAL ? rs * (a.alpha[1] ? __ldg(a.alpha[1] + t.g) : 1.0f) : 1.0f;
+            const float ginv = DUAL && P::kNv ? __fdiv_rn(1.0f, __ldg(a.h_gscale + t.g)) : 1.0f;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.acc_full[acc]), aph, a.wait_limit, abort))) {
                 if (lane == 0) fail();
                 break;
             }
             tc_fence_after();
-            const int r = quad * 32 + lane, col0 = t.nt * P::kOutN + half * kCols;
-            const uint32_t d = tmem + acc * BN + half * kCols + ((uint32_t)(quad * 32) << 16);
-            const bool any = quad * 32 < t.rows && col0 < a.N, live = any && r < t.rows;
-            const size_t row = (size_t)t.row0 + r;
-            const float rs = live && a.a_row_scale ? __ldg(a.a_row_scale + row) : 1.0f;
-            const float s0 = rs * (a.alpha[0] ? __ldg(a.alpha[0] + t.g) : 1.0f);
             // the accumulators go to registers and are free for the next tile's products before anything is
             // computed from them or stored
             auto release = [&]() {
@@ -579,9 +582,6 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                     add_part(u[i], part, 16 * i, lane);
                     add_part(u2[i], part, kCols + 16 * i, lane);
                 }
-                const float s1 = rs * (a.alpha[1] ? __ldg(a.alpha[1] + t.g) : 1.0f);
-                float ginv = 1.0f;
-                if (P::kNv) ginv = __fdiv_rn(1.0f, __ldg(a.h_gscale + t.g));
                 const int hct = scaled_col_tiles(FMT, a.N);
                 const long long srow = (long long)t.srow_tile * kScaleRows + r;
                 constexpr int kBlk = scaled_block(FMT), kWords = kCols / (P::kNv ? 8 : 4);
@@ -821,15 +821,15 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         const uint32_t empty = mapa_u32(smem_u32(&sh.acc_empty[0]), 0);
         for (int tile = first_tile; tile < total; tile += stride) {
             const Tile t = tile_at<kPairRows>(a, sh, tile, n_tiles);
+            const int r0 = rank * 128 + quad * 32, r = r0 + lane, col0 = t.nt * 256 + half * 128;
+            const bool any = r0 < t.rows && col0 < a.N, live = any && r < t.rows;
+            const size_t row = (size_t)t.row0 + r;
+            const float s = (live && a.a_row_scale ? __ldg(a.a_row_scale + row) : 1.0f) * (a.alpha[0] ? __ldg(a.alpha[0] + t.g) : 1.0f);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(smem_u32(&sh.acc_full[0]), aph, a.wait_limit, abort))) {
                 if (lane == 0) fail();
                 break;
             }
             tc_fence_after();
-            const int r0 = rank * 128 + quad * 32, r = r0 + lane, col0 = t.nt * 256 + half * 128;
-            const bool any = r0 < t.rows && col0 < a.N, live = any && r < t.rows;
-            const size_t row = (size_t)t.row0 + r;
-            const float s = (live && a.a_row_scale ? __ldg(a.a_row_scale + row) : 1.0f) * (a.alpha[0] ? __ldg(a.alpha[0] + t.g) : 1.0f);
             auto release = [&]() {
                 tc_fence_before();
                 __syncwarp();
