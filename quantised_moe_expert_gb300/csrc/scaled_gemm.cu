@@ -52,13 +52,13 @@ struct Plan {
     // shared memory: the stages' codes (whole 1024-byte swizzle atoms), then their scales
     static constexpr int kCodeBytes = kABytes + kBBytes, kSfBytes = kSfaBytes + kSfbBytes;
     static_assert(kCodeBytes % 1024 == 0, "swizzle atoms");
-    static constexpr int kStages = BN == 256 ? (DUAL || !kNv ? 4 : 3) : BN == 128 ? 5 : 7;
+    static constexpr int kStages = BN == 256 ? (DUAL || !kNv ? 4 : 3) : BN == 128 ? (DUAL && SPLIT && kNv ? 4 : 5) : 7;
     static constexpr int kStaged = BN == 256 && !kNv ? 64 : 128;     // bytes of a row that an epilogue warp stages at a time
     static constexpr int kOutBytes = DUAL || BN == 64 ? 0 : 8 * 32 * kStaged;
     static constexpr int kAccs = BN == 256 ? 1 : 2;          // accumulator buffers
     static constexpr int kSfCols = 4 * kTilesK * (1 + kChunks);   // tensor-memory columns of a stage's scales
     static constexpr int kPartCols = (DUAL ? 2 : 1) * kOutN / 2;     // accumulator columns of an epilogue warp
-    static constexpr int kPartBytes = SPLIT ? 2 * 32 * kPartCols * 4 : 0;   // the other CTA's sums (32 rows)
+    static constexpr int kPartBytes = SPLIT ? 128 * kPartCols * 4 : 0;   // the other CTA's sums of half of the columns
     static constexpr int kSfAt = kStages * kCodeBytes, kOutAt = kSfAt + kStages * kSfBytes, kPartAt = kOutAt + kOutBytes;
     static constexpr int kSmem = kPartAt + kPartBytes + 1024;
     static_assert(kAccs * BN + kStages * kSfCols <= 512, "tensor memory");
@@ -69,7 +69,7 @@ struct Maps {
 };
 
 struct Shared {
-    uint64_t full[8], empty[8], acc_full[2], acc_empty[2], part[2], drain;
+    uint64_t full[8], empty[8], acc_full[2], acc_empty[2], part[4], drain;
     uint32_t tmem;
     int abort;
     int bad, groups, row_tiles;                              // malformed offsets; groups with rows; their row tiles
@@ -315,9 +315,9 @@ __device__ __forceinline__ void store_rows(const ScaledGemmArgs &a, uint32_t d, 
     }
 }
 
-// SPLIT: few rows (at most 32) on no more tiles than half the SMs, where the K steps one after the other are
-// the time: two CTAs (a cluster) take half of a tile's steps each, and the second hands its sums to the first
-// through that one's shared memory.
+// SPLIT: no more tiles than half the SMs, where the K steps one after the other are the time: two CTAs (a
+// cluster) take half of a tile's steps each, hand each other half of the columns' sums through shared memory and
+// finish the other half.
 template <int FMT, bool DUAL, int BN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_constant__ Maps maps)
@@ -350,8 +350,7 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             mbar_init(smem_u32(&sh.acc_empty[i]), 8);
         }
         mbar_init(smem_u32(&sh.drain), 1);
-        mbar_init(smem_u32(&sh.part[0]), 1);
-        mbar_init(smem_u32(&sh.part[1]), 1);
+        for (int i = 0; i < 4; ++i) mbar_init(smem_u32(&sh.part[i]), 1);
         sh.abort = 0;
         sh.bad = 0;
         sh.row_tiles = (a.R + kScaleRows - 1) / kScaleRows;
@@ -535,10 +534,11 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             };
             const float4 *part = nullptr;
             if constexpr (SPLIT) {
-                float4 *const mine = reinterpret_cast<float4 *>(smem + P::kPartAt) + half * 8 * P::kPartCols;
-                if (rank) {
+                // each CTA finishes half of the columns and hands the other half's sums over
+                float4 *const mine = reinterpret_cast<float4 *>(smem + P::kPartAt) + quad * 8 * P::kPartCols;
+                if (half != rank) {
                     if (any) {
-                        const uint32_t to = mapa_u32(smem_u32(mine), 0) + lane * 16;
+                        const uint32_t to = mapa_u32(smem_u32(mine), rank ^ 1) + lane * 16;
 #pragma unroll
                         for (int i = 0; i < P::kPartCols; i += 16) {
                             uint32_t u[16];
@@ -550,13 +550,13 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                         }
                         fence_cluster();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(mapa_u32(smem_u32(&sh.part[half]), 0));
+                        if (lane == 0) mbar_arrive_cluster(mapa_u32(smem_u32(&sh.part[quad]), rank ^ 1));
                     }
                     release();
-                    break;                                                // the tile is the first CTA's from here on
+                    break;                                                // these columns are the other CTA's from here on
                 }
                 if (any) {
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(smem_u32(&sh.part[half]), 0, a.wait_limit, abort))) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(smem_u32(&sh.part[quad]), 0, a.wait_limit, abort))) {
                         if (lane == 0) fail();
                         break;
                     }
@@ -868,6 +868,7 @@ cudaError_t launch_pair(const ScaledGemmArgs &a, int clusters, cudaStream_t st)
                        : make_map_4bit(&maps.w, a.w_codes[0], a.K, (uint64_t)a.G * a.N, 128));
     if (!ok) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> ready{0};
+    static_assert(P::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
     const cudaError_t e = set_shared(scaled_pair_kernel<FMT>, P::kSmem, ready);
     if (e != cudaSuccess) return e;
     return launch_dependent_clusters(scaled_pair_kernel<FMT>, 2 * clusters, 2, kThreads, P::kSmem, st, a, maps);
@@ -878,6 +879,7 @@ cudaError_t launch_plan(const ScaledGemmArgs &a, const Maps &maps, int ctas, cud
 {
     using P = Plan<FMT, DUAL, BN, SPLIT>;
     auto k = scaled_gemm_kernel<FMT, DUAL, BN, SPLIT>;
+    static_assert(P::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = set_shared(k, P::kSmem, ready);
     if (e != cudaSuccess) return e;
@@ -914,10 +916,11 @@ cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
     const long long n = tiles(DUAL ? bn / 2 : bn);
     const int ctas = (int)(n < sms ? n : sms);
     constexpr int kNarrow = DUAL ? 128 : 64, kStepK = kNv ? 256 : 128;
-    // Half of the K steps on a second CTA, where they are worth the exchange (about 1.5 us).  us, one CTA / two, at
-    // 8, 16 and 32 steps: 1 x 4096 x 2048 NVFP4 4.6 / 5.3, 16 x 4096 x 4096 NVFP4 6.7 / 6.4, 16 x 4096 x 4096 MXFP8 9.1 / 7.6,
-    // 1 x 4096 x 8192 NVFP4 10.7 / 8.6.
-    const bool split = bn == kNarrow && a.R <= 32 && 2 * n <= sms && a.K >= 14 * kStepK;
+    // Half of the K steps on a second CTA, where they are worth the exchange (about 1 us, and the clusters start later
+    // behind another launch).  us, one CTA / two, with the quantisation of the rows, at 14, 20 and 32 steps: 16 x 4096 NVFP4
+    // 7.4 / 7.1, 9.2 / 8.2, 12.5 / 10.2, MXFP8 6.8 / 6.7, 8.1 / 7.4, 10.6 / 8.8; 301 x 1000 NVFP4 8.6 / 8.9, 10.8 / 9.8, 14.1 / 12.0, MXFP8
+    // 7.5 / 8.1, 8.9 / 9.3, 11.6 / 10.8.
+    const bool split = bn == kNarrow && 2 * n <= sms && a.K >= (a.R <= 64 ? 14 : 24) * kStepK;
     Maps maps;
     const uint64_t abytes = kNv ? a.K / 2 : a.K;
     bool ok = make_map_2d(&maps.a32, a.a_codes, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, abytes, a.R, kStepBytes, 32,
@@ -937,7 +940,7 @@ cudaError_t launch_fmt(const ScaledGemmArgs &a, cudaStream_t st)
             ok = ok && make_map_4bit(&maps.w[i], w, a.K, (uint64_t)a.G * a.N, box);
     }
     if (!ok) return cudaErrorInvalidValue;
-    if (split) return launch_plan<FMT, DUAL, DUAL ? 128 : 64, true>(a, maps, 2 * (int)n, st);
+    if (split) return launch_plan<FMT, DUAL, kNarrow, true>(a, maps, 2 * (int)n, st);
     if (bn == 256) return launch_plan<FMT, DUAL, 256>(a, maps, ctas, st);
     if (bn == 128) return launch_plan<FMT, DUAL, 128>(a, maps, ctas, st);
     if constexpr (!DUAL) return launch_plan<FMT, DUAL, 64>(a, maps, ctas, st);

@@ -72,6 +72,16 @@ def test_swiglu_long_sums(monkeypatch, fmt, K, sizes):
     T.test_swiglu(fmt, "few", 512, K)
 
 
+@pytest.mark.parametrize("fmt,K", [(NV, 3648), (NV, 6208), (M8, 1920), (M8, 3200)])
+@pytest.mark.parametrize("sizes", [[33], [64], [60, 4], [301], [130, 0, 3]])
+def test_long_sums_of_more_rows(monkeypatch, fmt, K, sizes):
+    """K steps shared by two CTAs for every number of rows in a tile, and groups of several tiles."""
+    monkeypatch.setitem(T.GROUPS, "few", sizes)
+    T.test_gemm(fmt, "few", 328, K)
+    if K > 3648 or fmt == M8:
+        T.test_swiglu(fmt, "few", 256, K)
+
+
 @pytest.mark.parametrize("fmt", [NV, M8])
 def test_few_rows_before_the_first_group(fmt):
     """Rows before the first group belong to none and are left as they are."""
