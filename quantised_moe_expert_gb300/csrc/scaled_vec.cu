@@ -15,8 +15,8 @@
 // conversion of its activations.
 //
 // 1 x 4096 x 2048: 2.8 us in either format (1.7 TB/s from L2), against 4.5 (NVFP4) and 5.9 of a tile; 1 x 4096 x 8192 NVFP4 6.7
-// against 8.5.  One token of 9 experts, hidden 2048, inter 512, NVFP4: 4.7 and 3.7 us against 7.4 and 4.4.  1.9 us are
-// launch to launch, 0.5 the search for a row's group.  Ways that were slower, where this took 3.0 us: packed fp16 FMAs
+// against 8.5.  One token of 9 experts, hidden 2048, inter 512, NVFP4: 4.5 and 3.7 us against 7.4 and 4.4.  1.9 us are
+// launch to launch, 0.4 the search for a row's group.  Ways that were slower, where this took 3.0 us: packed fp16 FMAs
 // (4.0), byte dot products of looked-up codes (4.3), m16n8k32 of E4M3 (4.7), the activations converted once into
 // shared memory (3.8); the scales fetched by column tiles into shared memory cost 0.5 us at K = 512.
 #include "scaled.cuh"
@@ -97,10 +97,20 @@ scaled_vec_kernel(const __grid_constant__ ScaledGemmArgs a, int blocks)
     int g = 0, start = 0;
     if (a.offsets) {
         uint32_t c = 0, m = 0;
-        for (int i = threadIdx.x; i < a.G; i += kThreads) {
-            const int o = a.offsets[i], next = i + 1 < a.G ? a.offsets[i + 1] : a.R;
-            m = o <= row ? max(m, (uint32_t)o) : m;
-            c += (o <= row) + ((o < 0 || o > a.R || next < o) ? 1u << 16 : 0u);
+        constexpr int kPer = kThreads < 512 ? 512 / kThreads : 1;       // loads on their way together
+        for (int i0 = threadIdx.x; i0 < a.G; i0 += kThreads * kPer) {
+            int o[kPer], next[kPer];
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                const int i = i0 + j * kThreads;
+                o[j] = i < a.G ? a.offsets[i] : a.R;
+                next[j] = i + 1 < a.G ? a.offsets[i + 1] : a.R;
+            }
+#pragma unroll
+            for (int j = 0; j < kPer; ++j) {
+                m = o[j] <= row ? max(m, (uint32_t)o[j]) : m;
+                c += (o[j] <= row) + ((o[j] < 0 || o[j] > a.R || next[j] < o[j]) ? 1u << 16 : 0u);
+            }
         }
         c = __reduce_add_sync(0xFFFFFFFFu, c);
         m = __reduce_max_sync(0xFFFFFFFFu, m);
