@@ -419,7 +419,9 @@ MOE_API int moe_tile_scales(int format, const uint8_t *src, int G, int N, int n,
  *            expert as group E).  With an entry outside [0, R] or below its
  *            predecessor nothing is computed (MOE_ERR_DEVICE is reported).
  * K: a multiple of 64 (NVFP4) or 128 (MXFP8), at most 65536; N: a multiple of 8;
- * G <= 1024; R <= 2^21 rows.  R == 0 enqueues nothing. */
+ * G <= 1024; R <= 2^21 rows.  R == 0 enqueues nothing.
+ * The same call gives the same bits; sizes select the kernels (few rows run
+ * without tiles), so the last bits of a row's sums can depend on R. */
 MOE_API int moe_scaled_gemm(int format, const moe_scaled_rows *a, const moe_scaled_mat *w, int R, int N, int K, int G,
                             const int32_t *offsets, void *y, int y_f32, void *ws, size_t ws_bytes, void *stream);
 
