@@ -493,14 +493,13 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 aph ^= 1;
             }
         }
-        if (!ok) {
-            if (leader) {
-                fail();
-                mma_commit(smem_u32(&sh.drain));
-            }
-            __syncwarp();
-            mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
+        // the products end before the CTA leaves, whoever gave up: an epilogue that did waits for none of them
+        if (leader) {
+            if (!ok) fail();
+            mma_commit(smem_u32(&sh.drain));
         }
+        __syncwarp();
+        mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
     } else if (warp >= 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         // ---- accumulators to outputs
@@ -805,14 +804,13 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             if (leader) mma_commit_pair(smem_u32(&sh.acc_full[0]));
             aph ^= 1;
         }
-        if (!ok) {
-            if (leader) {
-                fail();
-                mma_commit_pair(smem_u32(&sh.drain));
-            }
-            __syncwarp();
-            mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
+        // the products end before the pair leaves, whoever gave up
+        if (leader) {
+            if (!ok) fail();
+            mma_commit_pair(smem_u32(&sh.drain));
         }
+        __syncwarp();
+        mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
     } else if (warp >= 4) {
         // ---- accumulators to outputs: each CTA its own rows
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -843,7 +841,9 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         }
     }
     __syncthreads();
-    cluster_sync();                                                   // nothing of the pair is in flight any more
+    cluster_sync();                                                   // nothing of the pair is issued any more
+    // commits arrive in both CTAs: the last of them, of all products, is there before the second one's shared memory goes
+    if (rank == 1 && warp == 1) mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
     if (warp == 3) tmem_dealloc_pair(tmem, 512);
 }
 
