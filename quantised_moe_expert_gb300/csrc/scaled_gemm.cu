@@ -73,6 +73,7 @@ struct Shared {
     uint32_t tmem;
     int abort;
     int bad, groups, row_tiles;                              // malformed offsets; groups with rows; their row tiles
+    int gave_up, issued[2][2];                               // a pair's: whether any of its waits ran out; copies [CTA][codes, scales]
     int2 warp_sum[kThreads / 32];
     int2 group[kMaxGroups + 1];                              // those groups: row tiles before it, start << 10 | group
 };
@@ -694,7 +695,7 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         mbar_init(smem_u32(&sh.acc_full[0]), 1);
         mbar_init(smem_u32(&sh.acc_empty[0]), 16);                    // the epilogue warps of both CTAs
         mbar_init(smem_u32(&sh.drain), 1);
-        sh.abort = 0;
+        sh.abort = sh.gave_up = 0;
         sh.bad = 0;
         sh.row_tiles = (a.R + kPairRows - 1) / kPairRows;
         fence_mbar_init();
@@ -717,6 +718,9 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     auto fail = [&]() {
         record_status(a.status, MOE_ERR_TIMEOUT);
         *abort = 1;
+    };
+    auto tell_pair = [&]() {
+        for (uint32_t c = 0; c < 2; ++c) st_cluster_u32(mapa_u32(smem_u32(&sh.gave_up), c), 1);
     };
 
     if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
@@ -757,13 +761,9 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
                 }
             }
         }
-        // the newest copy of each stage lands before the pair leaves, whoever gave up
-        for (int i = 0; rank == 0 && i < min(issued, P::kStages); ++i) {
-            if (--st < 0) {
-                st = P::kStages - 1;
-                ph ^= 1;
-            }
-            mbar_wait(smem_u32(&sh.full[st]), ph, 1 << 20, nullptr);
+        if (leader) {
+            st_cluster_u32(mapa_u32(smem_u32(&sh.issued[rank][warp >> 1]), 0), issued);
+            if (!ok) tell_pair();
         }
     } else if (warp == 1 && rank == 0) {
         // ---- MMAs of the pair
@@ -806,7 +806,10 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
         }
         // the products end before the pair leaves, whoever gave up
         if (leader) {
-            if (!ok) fail();
+            if (!ok) {
+                fail();
+                tell_pair();
+            }
             mma_commit_pair(smem_u32(&sh.drain));
         }
         __syncwarp();
@@ -844,6 +847,17 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
     cluster_sync();                                                   // nothing of the pair is issued any more
     // commits arrive in both CTAs: the last of them, of all products, is there before the second one's shared memory goes
     if (rank == 1 && warp == 1) mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
+    if (sh.gave_up) {
+        // Where nobody gave up, the products have waited for every copy of both CTAs.  Else the newest copy of each stage may
+        // still be on its way, whichever of the four warps asked for it: none is more than the stages ahead of another.  A
+        // stage that not all four asked for does not complete, and its wait runs out long after its copies have landed.
+        if (rank == 0 && warp == 0) {
+            const int n = max(max(sh.issued[0][0], sh.issued[0][1]), max(sh.issued[1][0], sh.issued[1][1])), i = n - 1 - lane;
+            if (lane < min(n, P::kStages)) mbar_wait(smem_u32(&sh.full[i % P::kStages]), i / P::kStages & 1, 1 << 20, nullptr);
+        }
+        __syncthreads();
+        cluster_sync();
+    }
     if (warp == 3) tmem_dealloc_pair(tmem, 512);
 }
 

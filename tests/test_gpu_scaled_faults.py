@@ -1,5 +1,5 @@
 """Block-scaled products whose in-kernel waits run out: reported, the kernels return, and what they leave serves the next
-call.  Sizes reach every launch shape that waits (tiles, halves of the K steps on two CTAs); limits from a
+call.  Sizes reach every launch shape that waits (tiles, halves of the K steps on two CTAs, pairs of CTAs); limits from a
 single poll up end the roles of a CTA at different places.  Nothing here traps, faults or hangs the GPU."""
 import numpy as np
 import pytest
@@ -13,10 +13,12 @@ from . import scaled_ref as S
 pytestmark = pytest.mark.gpu
 
 NV, M8 = S.NV, S.M8
-# tokens, hidden, inter (two experts, one pick each): both products in tiles; the SwiGLU's K steps on two CTAs each
+# tokens, hidden, inter (two experts, one pick each): both products in tiles; the SwiGLU's K steps on two CTAs each; the down
+# products by pairs of CTAs (512 rows a group)
 SIZES = {
     "tiles": {NV: (700, 512, 192), M8: (700, 512, 256)},
     "split": {NV: (64, 4096, 256), M8: (64, 4096, 256)},
+    "pairs": {NV: (1024, 8192, 2048), M8: (1024, 8192, 1024)},
 }
 
 
@@ -69,7 +71,7 @@ def test_waits_that_run_out(fmt, size):
 
 
 @pytest.mark.parametrize("fmt", [NV, M8])
-@pytest.mark.parametrize("R,N,K", [(300, 520, 128), (64, 512, 3840)])
+@pytest.mark.parametrize("R,N,K", [(300, 520, 128), (64, 512, 3840), (3001, 2008, 2304)])
 @pytest.mark.parametrize("bad", [(0, 0.5, 0.4), (-3, 0.2, 0.4), (0, 0.2, 1.5)])
 def test_bad_offsets_in_every_launch_shape(fmt, R, N, K, bad):
     """Offsets that decrease or leave the rows: reported, nothing is computed."""
