@@ -100,7 +100,10 @@ __device__ __forceinline__ float nvfp4_row_factor(uint32_t amax_bits)
 
 // Every kernel of this family lets its successor in the stream start early (griddepcontrol.launch_dependents)
 // and reads or writes memory only after griddepcontrol.wait, in every block: a successor's set-up (barriers,
-// tensor memory, tensor maps) runs under its predecessor's tail.  A norm of one row behind another: 2.6 us from
+// tensor memory, tensor maps) runs under its predecessor's tail.  So a kernel is there while its predecessor still
+// writes: whatever an earlier launch may have written (offsets, picks, factors, weights) is read by plain loads, never
+// through the read-only path (__ldg, const __restrict__), which is for memory that nobody writes while the kernel
+// runs and whose loads the compiler may move above the wait.  A norm of one row behind another: 2.6 us from
 // launch to launch without, 1.9 us with.
 template <class... P, class... A>
 cudaError_t launch_dependent_clusters(void (*kernel)(P...), unsigned grid, unsigned cluster, unsigned block, size_t smem,

@@ -123,7 +123,7 @@ __device__ __forceinline__ void build_table(const ScaledGemmArgs &a, Shared &sh,
     const int g0 = threadIdx.x * kPer;
     int o[kPer + 1];
 #pragma unroll
-    for (int i = 0; i <= kPer; ++i) o[i] = g0 + i < a.G ? __ldg(a.offsets + g0 + i) : a.R;
+    for (int i = 0; i <= kPer; ++i) o[i] = g0 + i < a.G ? a.offsets[g0 + i] : a.R;
     int2 n = make_int2(0, 0);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -516,10 +516,10 @@ scaled_gemm_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             const bool any = quad * 32 < t.rows && col0 < a.N, live = any && r < t.rows;
             const size_t row = (size_t)t.row0 + r;
             // factors on their way under the products
-            const float rs = live && a.a_row_scale ? __ldg(a.a_row_scale + row) : 1.0f;
-            const float s0 = rs * (a.alpha[0] ? __ldg(a.alpha[0] + t.g) : 1.0f);
-            const float s1 = DUAL ? rs * (a.alpha[1] ? __ldg(a.alpha[1] + t.g) : 1.0f) : 1.0f;
-            const float ginv = DUAL && P::kNv ? __fdiv_rn(1.0f, __ldg(a.h_gscale + t.g)) : 1.0f;
+            const float rs = live && a.a_row_scale ? a.a_row_scale[row] : 1.0f;
+            const float s0 = rs * (a.alpha[0] ? a.alpha[0][t.g] : 1.0f);
+            const float s1 = DUAL ? rs * (a.alpha[1] ? a.alpha[1][t.g] : 1.0f) : 1.0f;
+            const float ginv = DUAL && P::kNv ? __fdiv_rn(1.0f, a.h_gscale[t.g]) : 1.0f;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.acc_full[acc]), aph, a.wait_limit, abort))) {
                 if (lane == 0) fail();
                 break;
@@ -825,7 +825,7 @@ scaled_pair_kernel(const __grid_constant__ ScaledGemmArgs a, const __grid_consta
             const int r0 = rank * 128 + quad * 32, r = r0 + lane, col0 = t.nt * 256 + half * 128;
             const bool any = r0 < t.rows && col0 < a.N, live = any && r < t.rows;
             const size_t row = (size_t)t.row0 + r;
-            const float s = (live && a.a_row_scale ? __ldg(a.a_row_scale + row) : 1.0f) * (a.alpha[0] ? __ldg(a.alpha[0] + t.g) : 1.0f);
+            const float s = (live && a.a_row_scale ? a.a_row_scale[row] : 1.0f) * (a.alpha[0] ? a.alpha[0][t.g] : 1.0f);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_cluster(smem_u32(&sh.acc_full[0]), aph, a.wait_limit, abort))) {
                 if (lane == 0) fail();
                 break;

@@ -133,8 +133,8 @@ __device__ __forceinline__ Dest routed_dest(const RowArgs &a, int t, int j)
     const int Tk = a.T * a.k;
     if (j == a.k)                                       // the shared expert's group: token order
         return Dest{(long long)Tk + t, (long long)group_row_tile(Tk, a.E) * kScaleRows + t};
-    const int f = t * a.k + j, g = __ldg(a.ids + f), r = __ldg(a.inv_perm + f);
-    const int off = g >= 0 && g < a.E ? __ldg(a.offsets + g) : -1;
+    const int f = t * a.k + j, g = a.ids[f], r = a.inv_perm[f];
+    const int off = g >= 0 && g < a.E ? a.offsets[g] : -1;
     if (off < 0 || off > r || r >= Tk) {
         record_status(a.status, MOE_ERR_DEVICE);
         return Dest{-1, 0};
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
                 wv[c] = make_uint4(0u, 0u, 0u, 0u);
                 if (on && a.residual)
                     raw[c] = add_bf16(raw[c], __ldcs(reinterpret_cast<const uint4 *>(a.residual + (size_t)t * a.n) + seg));
-                if (on) wv[c] = a.weight ? __ldg(reinterpret_cast<const uint4 *>(a.weight) + seg)
+                if (on) wv[c] = a.weight ? reinterpret_cast<const uint4 *>(a.weight)[seg]
                                          : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
             }
         }
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
         }
         float g = 1.f, ginv = 1.f;
         if (FMT == MOE_SCALED_NVFP4) {
-            if (a.gscale) g = live ? __ldg(a.gscale + group) : 1.f;
+            if (a.gscale) g = live ? a.gscale[group] : 1.f;
             else g = nvfp4_row_factor(row_max<TPR>(__float_as_uint(row_amax) & 0x7FFFFFFFu, mbuf));
             ginv = __fdiv_rn(1.0f, g);
         }
@@ -333,8 +333,8 @@ cudaError_t launch_fmt(const RowArgs &a, cudaStream_t st)
 }
 
 // One thread per word of four scales of a row.
-__global__ void tile_scales_kernel(const uint8_t *__restrict__ src, uint8_t *__restrict__ dst, int nb, int ct, int N,
-                                   int row_tiles, size_t words)
+__global__ void tile_scales_kernel(const uint8_t *src, uint8_t *dst, int nb, int ct, int N, int row_tiles,
+                                   size_t words)
 {
     tc::pdl_trigger();
     tc::pdl_wait();
