@@ -71,6 +71,18 @@ __device__ __forceinline__ void from_scales(uint32_t b, float (&s)[2])
         s[0] = __uint_as_float(h << 16);
     }
 }
+// acc + d fx fw.  Two E4M3 scales have an exact product; that of two powers of two can leave fp32's range where the sum
+// does not (and make a NaN of a sum of zero), so the smaller one comes first: d is a multiple of 2^-10, which 2^-127
+// takes to a subnormal exactly, and what then overflows or is rounded does so in the sum too.  A NaN scale stays.
+template <bool NV>
+__device__ __forceinline__ float scaled_add(float d, float fx, float fw, float acc)
+{
+    if (NV) return fmaf(d, fx * fw, acc);
+    float lo, hi;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(lo) : "f"(fx), "f"(fw));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(hi) : "f"(fx), "f"(fw));
+    return fmaf(d * lo, hi, acc);
+}
 template <bool NV>
 __device__ __forceinline__ uint32_t load_scales(const uint8_t *p)
 {
@@ -213,7 +225,7 @@ scaled_vec_kernel(const __grid_constant__ ScaledGemmArgs a, int blocks)
                     float f[2];
                     from_scales<kNv>(e[k][t][o], f);
 #pragma unroll
-                    for (int j = 0; j < (kNv ? 2 : 1); ++j) acc[t][o] = fmaf(d[t][j][2 * o], fx[j] * f[j], acc[t][o]);
+                    for (int j = 0; j < (kNv ? 2 : 1); ++j) acc[t][o] = scaled_add<kNv>(d[t][j][2 * o], fx[j], f[j], acc[t][o]);
                 }
         }
     }

@@ -164,3 +164,27 @@ def test_few_rows_weights_past_32_bits():
     wv = S.dequantise(NV, S.unpack(NV, wc[G - 1][cols].cpu().numpy()), wsc[gpu(S.scale_index(NV, K, wr).reshape(-1))].cpu().numpy().reshape(len(cols), -1))
     want, mag = av @ wv.T, np.abs(av) @ np.abs(wv).T
     assert (np.abs(y[:, cols].cpu().numpy() - want) <= product_error(K) * mag).all()
+
+
+@pytest.mark.parametrize("ea,ew,small", [(120, 20, False), (127, 127, False), (10, 118, False), (120, 8, True), (64, 64, True), (-127, -24, False),
+                                         (-100, -45, False), (-127, 127, False), (127, -127, True)])
+def test_few_rows_scales_past_fp32(ea, ew, small):
+    """Power-of-two scales whose product leaves fp32's range although the sums stay within it: blocks of zero codes give zero,
+    small codes (or the smallest sums) their value, but for the rounding of subnormal
+    sums, one step of 2^-149 a block."""
+    R, N, K = 2, 40, 512
+    rng = np.random.default_rng(abs(ea + ew))
+    ac, wc = np.zeros((R, K), np.uint8), rng.integers(0, 16, (N, K)).astype(np.uint8)
+    if small:
+        ac[:, 64:96] = rng.integers(0, 3, (R, 32)) + 128 * rng.integers(0, 2, (R, 32))          # 0, 2^-9, 2^-8 and their negatives
+    elif ea + ew < 100:
+        ac[:] = rng.integers(0, 127, (R, K))
+    sa, sw = np.full((R, K // 32), ea + 127, np.uint8), np.full((N, K // 32), ew + 127, np.uint8)
+    a = qm.scaled_rows(gpu(S.pack(M8, ac)), gpu(S.tile(M8, sa, S.scale_rows([0], R), R // 128 + 1, 0xFF)), None)
+    w = qm.scaled_mat(gpu(S.pack(M4, wc).reshape(1, N, -1)), gpu(S.weight_tiles(M4, sw.reshape(1, N, -1))), None)
+    av, wv = S.dequantise(M8, ac, sa, None), S.dequantise(M4, wc, sw, None)
+    want, mag = av @ wv.T, np.abs(av) @ np.abs(wv).T
+    assert mag.max() < 3e38 and (mag.max() > 0) == bool(ac.any())
+    y, ws = Out((R, N), torch.float32), workspace()
+    qm.moe_scaled_gemm(M8, a, w, R, N, K, 1, None, y.t, ws)
+    assert (np.abs(y.check() - want) <= product_error(K) * mag + K // 32 * 2.0 ** -149).all()
