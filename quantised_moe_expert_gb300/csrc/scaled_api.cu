@@ -85,7 +85,7 @@ int moe_quantize(int format, const void *x, int x_f32, int T, int n, int groups,
     if (T < 0 || n <= 0 || groups <= 0 || T > kMaxRows || (x_f32 != 0 && x_f32 != 1) || T % groups) return MOE_ERR_INVALID_ARG;
     if (!known_format(format)) return MOE_ERR_UNSUPPORTED;
     if (n % scaled_block(format) || n > (1 << 20)) return MOE_ERR_UNSUPPORTED;
-    if (format == MOE_SCALED_NVFP4 && n > kMaxRowLength) return MOE_ERR_UNSUPPORTED;
+    if (format == MOE_SCALED_NVFP4 && !gscale && n > kMaxRowLength) return MOE_ERR_UNSUPPORTED;
     if (!aligned(x) || !rows_ok(q, format) || !aligned_or_null(gscale, 4)) return MOE_ERR_INVALID_ARG;
     if (format == MOE_SCALED_NVFP4 ? (gscale == nullptr) == (q->row_scale == nullptr) : gscale != nullptr)
         return MOE_ERR_INVALID_ARG;

@@ -142,8 +142,9 @@ __device__ __forceinline__ Dest routed_dest(const RowArgs &a, int t, int j)
     return Dest{r, (long long)group_row_tile(off, g) * kScaleRows + (r - off)};
 }
 
-// FMT 0: no block-scaled output (norm only).
-template <int FMT, bool NORM, bool F32, int TPR, int CH>
+// FMT 0: no block-scaled output (norm only).  PANELS: rows longer than TPR * CH segments, a panel at a time: where nothing is
+// needed of the rest of the row (no norm, no factor of its own).
+template <int FMT, bool NORM, bool F32, int TPR, int CH, bool PANELS>
 __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ RowArgs a)
 {
     constexpr int kBlk = FMT == MOE_SCALED_NVFP4 ? 16 : 32;   // elements per scale
@@ -163,9 +164,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     const int copies = a.ids ? a.k + a.has_shared : 1;
     const int nseg = a.n / 8, ct = scaled_col_tiles(FMT ? FMT : MOE_SCALED_NVFP4, a.n);
     const int group = a.rows_per_group ? t / a.rows_per_group : 0;
-    // rows that need nothing of the rest of their row take it in panels of TPR * CH segments
-    constexpr bool kWhole = NORM || FMT == MOE_SCALED_NVFP4;
-    for (int seg0 = 0; seg0 < (kWhole ? 1 : nseg); seg0 += TPR * CH) {
+    for (int seg0 = 0; seg0 < (PANELS ? nseg : 1); seg0 += TPR * CH) {
         F2 v[CH][4];
         float amax[CH];
         uint4 raw[CH], wv[CH];
@@ -246,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
         }
         float g = 1.f, ginv = 1.f;
         if (FMT == MOE_SCALED_NVFP4) {
-            if (a.gscale) g = live ? a.gscale[group] : 1.f;
+            if (PANELS || a.gscale) g = live ? a.gscale[group] : 1.f;
             else g = nvfp4_row_factor(row_max<TPR>(__float_as_uint(row_amax) & 0x7FFFFFFFu, mbuf));
             ginv = __fdiv_rn(1.0f, g);
         }
@@ -308,11 +307,11 @@ __global__ void __launch_bounds__(kThreads) rows_kernel(const __grid_constant__ 
     }
 }
 
-template <int FMT, bool NORM, bool F32, int TPR, int CH>
+template <int FMT, bool NORM, bool F32, int TPR, int CH, bool PANELS = false>
 cudaError_t launch_one(const RowArgs &a, cudaStream_t st)
 {
     const int rows = kThreads / TPR;
-    return launch_dependent(rows_kernel<FMT, NORM, F32, TPR, CH>, (unsigned)((a.T + rows - 1) / rows), kThreads, 0, st, a);
+    return launch_dependent(rows_kernel<FMT, NORM, F32, TPR, CH, PANELS>, (unsigned)((a.T + rows - 1) / rows), kThreads, 0, st, a);
 }
 
 // Threads a row and segments a thread.  Few rows: a segment a thread, for the shortest way through (T = 1,
@@ -328,7 +327,9 @@ cudaError_t launch_fmt(const RowArgs &a, cudaStream_t st)
     const int ch = (nseg + kThreads - 1) / kThreads;
     if (ch <= 1) return launch_one<FMT, NORM, F32, 256, 1>(a, st);
     if (ch <= 2) return launch_one<FMT, NORM, F32, 256, 2>(a, st);
-    if (ch <= 4 || !(NORM || FMT == MOE_SCALED_NVFP4)) return launch_one<FMT, NORM, F32, 256, 4>(a, st);
+    if (ch <= 4) return launch_one<FMT, NORM, F32, 256, 4>(a, st);
+    if constexpr (!NORM)
+        if (FMT != MOE_SCALED_NVFP4 || a.gscale) return launch_one<FMT, NORM, F32, 256, 4, true>(a, st);
     return launch_one<FMT, NORM, F32, 256, 8>(a, st);
 }
 

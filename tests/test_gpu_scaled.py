@@ -571,3 +571,25 @@ def test_gemm_offsets_past_32_bits():
         want, mag = av @ wv.T, np.abs(av) @ np.abs(wv).T
         got = y[rows][:, cols].float().cpu().numpy()
         assert (np.abs(got - want) <= product_error(K) * mag + 2.0 ** -8 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("T,G,n", [(2, 2, 16400), (3, 1, 20496), (260, 2, 24592), (1, 1, 65536)])
+@pytest.mark.parametrize("f32", [0, 1])
+def test_quantize_long_rows_with_a_given_factor(T, G, n, f32):
+    """NVFP4 rows longer than a block of threads holds, as a product's K or a weight matrix may be."""
+    rng = np.random.default_rng(n + T)
+    x = random_rows(rng, T, n, wide=False)
+    if f32:
+        x = (x * (1 + rng.random((T, n), np.float32) * 2 ** -8)).astype(np.float32)
+    x[0, n // 2:n // 2 + 32] = 0
+    g = (np.abs(x).reshape(G, -1).max(1) / 2688 * np.array([1, 3])[:G]).astype(np.float32)
+    codes = Out((T, n // 2), torch.uint8)
+    scales = Out((G * -(-(T // G) // 128) * S.col_tiles(NV, n) * 512,), torch.uint8)
+    qm.moe_quantize(NV, gpu(x) if f32 else gpu(bits(x)), T, n, G, gpu(g), qm.scaled_rows(codes.t, scales.t))
+    want_c, want_s, _ = S.quantise(NV, x, g.repeat(T // G))
+    r = np.arange(T)
+    srows = r // (T // G) * -(-(T // G) // 128) * 128 + r % (T // G)
+    assert np.array_equal(scales.check()[S.scale_index(NV, n, srows)], want_s)
+    got = S.unpack(NV, codes.check())
+    zero = S.decode(NV, want_c) == 0
+    assert np.array_equal(got[~zero], want_c[~zero]) and (S.decode(NV, got[zero]) == 0).all()

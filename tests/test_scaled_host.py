@@ -157,3 +157,10 @@ def test_layer_workspace_size(lib, fmt, kw, expect):
         assert lib.moe_workspace_size(ctypes.byref(cfg), 16, ctypes.byref(plain)) == OK and n.value > plain.value
         assert lib.moe_scaled_workspace_size(ctypes.byref(cfg), fmt, -1, ctypes.byref(n)) == INVALID
         assert lib.moe_scaled_workspace_size(ctypes.byref(cfg), fmt, 16, None) == INVALID
+
+
+@pytest.mark.parametrize("n,expect", [(16400, OK), (65536, OK), (1 << 20, OK), ((1 << 20) + 16, UNSUPPORTED)])
+def test_quantize_long_rows_with_a_given_factor(lib, n, expect):
+    """Only rows whose factor comes from the whole row are limited to what a kernel keeps of one."""
+    assert quantize(lib, fmt=NV, gscale=FAKE, n=n) == expect
+    assert quantize(lib, fmt=NV, q=rows(row_scale=FAKE), n=n) == UNSUPPORTED
