@@ -394,7 +394,7 @@ MOE_API int moe_add_rmsnorm(const uint16_t *x, const uint16_t *residual, const u
  *   gscale  NVFP4: fp32 [groups] given factor g of each group's rows
  *           (q->row_scale is not written), or NULL: a factor per row, written to
  *           q->row_scale.  Other formats: NULL.
- * n: a multiple of the block; at most 16384 for NVFP4 without gscale. */
+ * n: a multiple of the block, at most 2^20, or 16384 for NVFP4 without gscale. */
 MOE_API int moe_quantize(int format, const void *x, int x_f32, int T, int n, int groups, const float *gscale,
                          const moe_scaled_rows *q, void *stream);
 
@@ -402,7 +402,8 @@ MOE_API int moe_quantize(int format, const void *x, int x_f32, int T, int n, int
  * inv_perm, offsets as from moe_route and moe_permute) and, with has_shared, into
  * row T*k + t of the shared expert's group E: the rows of a grouped product over
  * E + has_shared groups.  format: NVFP4 (row factors) or MXFP8.  Picks that the
- * arguments place outside the rows are reported (MOE_ERR_DEVICE) and not written. */
+ * arguments place outside the rows are reported (MOE_ERR_DEVICE) and not written.
+ * n: a multiple of the block, at most 2^20, or 16384 for NVFP4. */
 MOE_API int moe_quantize_routed(int format, const uint16_t *x, int T, int n, int k, int E, int has_shared,
                                 const int32_t *ids, const int32_t *inv_perm, const int32_t *offsets,
                                 const moe_scaled_rows *q, void *ws, size_t ws_bytes, void *stream);

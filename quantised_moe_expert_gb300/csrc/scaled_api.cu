@@ -109,7 +109,7 @@ int moe_quantize_routed(int format, const uint16_t *x, int T, int n, int k, int 
 {
     if (T < 0 || n <= 0 || k <= 0 || E <= 0 || T > kMaxTokens || (has_shared != 0 && has_shared != 1)) return MOE_ERR_INVALID_ARG;
     if (!activation_format(format) || k > kMaxTopK || E + has_shared > kMaxGroups) return MOE_ERR_UNSUPPORTED;
-    if (n % scaled_block(format) || n > kMaxRowLength) return MOE_ERR_UNSUPPORTED;
+    if (n % scaled_block(format) || n > (format == MOE_SCALED_NVFP4 ? kMaxRowLength : 1 << 20)) return MOE_ERR_UNSUPPORTED;
     if (!aligned(x) || !aligned(ids, 4) || !aligned(inv_perm, 4) || !aligned(offsets, 4) || !rows_ok(q, format))
         return MOE_ERR_INVALID_ARG;
     if (format == MOE_SCALED_NVFP4 && !q->row_scale) return MOE_ERR_INVALID_ARG;

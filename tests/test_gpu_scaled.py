@@ -593,3 +593,9 @@ def test_quantize_long_rows_with_a_given_factor(T, G, n, f32):
     got = S.unpack(NV, codes.check())
     zero = S.decode(NV, want_c) == 0
     assert np.array_equal(got[~zero], want_c[~zero]) and (S.decode(NV, got[zero]) == 0).all()
+
+
+@pytest.mark.parametrize("T,n,E,k,shared", [(1, 16416, 8, 2, 1), (7, 20480, 16, 3, 0), (40, 32768, 8, 2, 1)])
+def test_quantize_routed_long_rows(T, n, E, k, shared):
+    """MXFP8 rows of more than one panel, each of them into all of the row's copies."""
+    test_quantize_routed(M8, T, n, E, k, shared)

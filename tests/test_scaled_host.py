@@ -164,3 +164,9 @@ def test_quantize_long_rows_with_a_given_factor(lib, n, expect):
     """Only rows whose factor comes from the whole row are limited to what a kernel keeps of one."""
     assert quantize(lib, fmt=NV, gscale=FAKE, n=n) == expect
     assert quantize(lib, fmt=NV, q=rows(row_scale=FAKE), n=n) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("fmt,n,expect", [(M8, 16416, OK), (M8, 1 << 20, OK), (M8, (1 << 20) + 32, UNSUPPORTED), (NV, 16384, OK),
+                                          (NV, 16400, UNSUPPORTED)])
+def test_quantize_routed_row_lengths(lib, fmt, n, expect):
+    assert routed(lib, fmt=fmt, q=rows(row_scale=FAKE if fmt == NV else None), n=n) == expect
