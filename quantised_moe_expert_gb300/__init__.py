@@ -332,10 +332,27 @@ def moe_decode_timeline(cfg, T, ws, stream=None, max_ctas: int = 256) -> np.ndar
 
 
 # The block-scaled operators are microseconds on the device at small sizes, so their bindings do no more than
-# they have to: no ctypes objects for pointers, the stream's handle and not its object.
+# they have to: no ctypes objects for pointers, the stream's handle and not its object.  The library sees addresses
+# alone, so what a tensor holds is checked here.
 
-def _addr(t):
-    return None if t is None else t.data_ptr()
+_BITS16 = frozenset((torch.bfloat16, torch.int16, torch.uint16))   # bf16 values, or their bits
+_BITS16_F32 = _BITS16 | {torch.float32}
+_F32, _I32 = frozenset((torch.float32,)), frozenset((torch.int32,))
+
+
+def _dense(fn, t, types):
+    """Address of a dense tensor of one of these types."""
+    if t.dtype not in types or not t.is_contiguous():
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+    return t.data_ptr()
+
+
+def _dense_or_none(fn, t, types):
+    if t is None:
+        return None
+    if t.dtype not in types or not t.is_contiguous():
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+    return t.data_ptr()
 
 
 def _handle(stream):
@@ -345,46 +362,58 @@ def _handle(stream):
 
 
 def moe_add_rmsnorm(x, residual, weight, weight_offset, eps, T, n, sum_out, y_out, fmt, q, stream=None):
-    rc = (_lib or load()).moe_add_rmsnorm(x.data_ptr(), _addr(residual), _addr(weight), weight_offset, eps, T, n,
-                                          _addr(sum_out), _addr(y_out), fmt, q, _handle(stream))
+    fn = "moe_add_rmsnorm"
+    rc = (_lib or load()).moe_add_rmsnorm(_dense(fn, x, _BITS16), _dense_or_none(fn, residual, _BITS16),
+                                          _dense_or_none(fn, weight, _BITS16), weight_offset, eps, T, n,
+                                          _dense_or_none(fn, sum_out, _BITS16), _dense_or_none(fn, y_out, _BITS16), fmt, q,
+                                          _handle(stream))
     if rc:
-        raise MoeError("moe_add_rmsnorm", rc)
+        raise MoeError(fn, rc)
 
 
 def moe_quantize(fmt, x, T, n, groups, gscale, q, stream=None):
-    """x: a bf16 (or int16 bits) or float32 tensor."""
-    rc = (_lib or load()).moe_quantize(fmt, x.data_ptr(), x.dtype == torch.float32, T, n, groups, _addr(gscale), q,
-                                       _handle(stream))
+    """x: a bf16 (or its bits, as a 16-bit integer) or float32 tensor."""
+    fn = "moe_quantize"
+    rc = (_lib or load()).moe_quantize(fmt, _dense(fn, x, _BITS16_F32), x.dtype == torch.float32, T, n, groups,
+                                       _dense_or_none(fn, gscale, _F32), q, _handle(stream))
     if rc:
-        raise MoeError("moe_quantize", rc)
+        raise MoeError(fn, rc)
 
 
 def moe_quantize_routed(fmt, x, T, n, k, E, has_shared, ids, inv_perm, offsets, q, ws, stream=None):
-    rc = (_lib or load()).moe_quantize_routed(fmt, x.data_ptr(), T, n, k, E, has_shared, ids.data_ptr(), inv_perm.data_ptr(),
-                                              offsets.data_ptr(), q, ws.data_ptr(), ws.nbytes, _handle(stream))
+    fn = "moe_quantize_routed"
+    rc = (_lib or load()).moe_quantize_routed(fmt, _dense(fn, x, _BITS16), T, n, k, E, has_shared, _dense(fn, ids, _I32),
+                                              _dense(fn, inv_perm, _I32), _dense(fn, offsets, _I32), q, ws.data_ptr(), ws.nbytes,
+                                              _handle(stream))
     if rc:
-        raise MoeError("moe_quantize_routed", rc)
+        raise MoeError(fn, rc)
 
 
 def moe_tile_scales(fmt, src, G, N, n, dst, stream=None):
+    """src, dst: tensors of one byte an element."""
+    fn = "moe_tile_scales"
+    if src.itemsize != 1 or dst.itemsize != 1 or not src.is_contiguous() or not dst.is_contiguous():
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
     rc = (_lib or load()).moe_tile_scales(fmt, src.data_ptr(), G, N, n, dst.data_ptr(), _handle(stream))
     if rc:
-        raise MoeError("moe_tile_scales", rc)
+        raise MoeError(fn, rc)
 
 
 def moe_scaled_gemm(fmt, a, w, R, N, K, G, offsets, y, ws, stream=None):
-    """y: a bf16 (or int16 bits) or float32 tensor [R, N]."""
-    rc = (_lib or load()).moe_scaled_gemm(fmt, a, w, R, N, K, G, _addr(offsets), y.data_ptr(), y.dtype == torch.float32,
-                                          ws.data_ptr(), ws.nbytes, _handle(stream))
+    """y: a bf16 (or its bits, as a 16-bit integer) or float32 tensor [R, N]."""
+    fn = "moe_scaled_gemm"
+    rc = (_lib or load()).moe_scaled_gemm(fmt, a, w, R, N, K, G, _dense_or_none(fn, offsets, _I32), _dense(fn, y, _BITS16_F32),
+                                          y.dtype == torch.float32, ws.data_ptr(), ws.nbytes, _handle(stream))
     if rc:
-        raise MoeError("moe_scaled_gemm", rc)
+        raise MoeError(fn, rc)
 
 
 def moe_scaled_swiglu(fmt, a, gate, up, R, inter, K, G, offsets, h_scale, h, ws, stream=None):
-    rc = (_lib or load()).moe_scaled_swiglu(fmt, a, gate, up, R, inter, K, G, _addr(offsets), _addr(h_scale), h,
-                                            ws.data_ptr(), ws.nbytes, _handle(stream))
+    fn = "moe_scaled_swiglu"
+    rc = (_lib or load()).moe_scaled_swiglu(fmt, a, gate, up, R, inter, K, G, _dense_or_none(fn, offsets, _I32),
+                                            _dense_or_none(fn, h_scale, _F32), h, ws.data_ptr(), ws.nbytes, _handle(stream))
     if rc:
-        raise MoeError("moe_scaled_swiglu", rc)
+        raise MoeError(fn, rc)
 
 
 def moe_scaled_workspace_size(cfg: moe_config, fmt: int, T: int) -> int:
@@ -394,16 +423,27 @@ def moe_scaled_workspace_size(cfg: moe_config, fmt: int, T: int) -> int:
 
 
 def moe_scaled_forward(cfg, w, x, T, router_bias, logits_in, y, ids_out, p_out, w_shared_out, ws, stream=None):
+    fn = "moe_scaled_forward"
+    for t, types in ((x, _BITS16), (y, _BITS16), (router_bias, _F32), (logits_in, _F32), (ids_out, _I32), (p_out, _BITS16),
+                     (w_shared_out, _BITS16)):
+        _dense_or_none(fn, t, types)
     rc = load().moe_scaled_forward(ctypes.byref(cfg), ctypes.byref(w), _ptr(x), T, _ptr(router_bias), _ptr(logits_in), _ptr(y),
                                    _ptr(ids_out), _ptr(p_out), _ptr(w_shared_out), _ptr(ws), ws.numel() * ws.element_size(),
                                    _stream(stream))
-    _check("moe_scaled_forward", rc)
+    _check(fn, rc)
 
 
 # ---------------------------------------------------------------- conveniences
 
+def _dense_bytes(fn, codes, scales, factors):
+    if not codes.is_contiguous() or not scales.is_contiguous():
+        raise MoeError(fn, MOE_ERR_INVALID_ARG)
+    _dense_or_none(fn, factors, _F32)
+
+
 def scaled_rows(codes, scales, row_scale=None) -> moe_scaled_rows:
     """The C description of block-scaled rows held in these tensors (which it keeps alive)."""
+    _dense_bytes("scaled_rows", codes, scales, row_scale)
     r = moe_scaled_rows(_ptr(codes), _ptr(scales), _ptr(row_scale))
     r.tensors = (codes, scales, row_scale)
     return r
@@ -411,6 +451,7 @@ def scaled_rows(codes, scales, row_scale=None) -> moe_scaled_rows:
 
 def scaled_mat(codes, scales, alpha=None) -> moe_scaled_mat:
     """The C description of a stack of block-scaled matrices held in these tensors (which it keeps alive)."""
+    _dense_bytes("scaled_mat", codes, scales, alpha)
     m = moe_scaled_mat(_ptr(codes), _ptr(scales), _ptr(alpha))
     m.tensors = (codes, scales, alpha)
     return m
