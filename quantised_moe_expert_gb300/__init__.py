@@ -480,6 +480,10 @@ class ScaledLayer:
     def __init__(self, shape, fmt, router, v, gate, up, down, h_scale=None):
         """router: DeviceLayer-style tensors (codes, scales, biases); v: bf16 bits [hidden] or None; gate, up, down:
         moe_scaled_mat; h_scale: float32 [G] (NVFP4)."""
+        _dense_or_none("ScaledLayer", v, _BITS16)
+        _dense_or_none("ScaledLayer", h_scale, _F32)
+        if h_scale is not None and h_scale.numel() != shape.n_experts + shape.has_shared:
+            raise MoeError("ScaledLayer", MOE_ERR_INVALID_ARG)
         self.shape, self.fmt, self.cfg = shape, fmt, config_of(shape)
         self.tensors = (router, v, gate, up, down, h_scale)
         self.w = moe_scaled_weights(fmt, moe_qmat(*[_ptr(t) for t in router], None), _ptr(v), gate, up, down, _ptr(h_scale))
@@ -513,8 +517,11 @@ class ScaledLayer:
     @classmethod
     def quantized(cls, host, fmt, gate, up, down, h_scale=None, device="cuda"):
         """host: the layer's shape, router and gate vector; gate, up [G, inter, hidden], down [G, hidden, inter]: float32
-        device tensors, quantised here to NVFP4 (fmt MOE_SCALED_NVFP4) or MXFP4 (MOE_SCALED_MXFP8)."""
+        device tensors, quantised here to NVFP4 (fmt MOE_SCALED_NVFP4) or MXFP4 (MOE_SCALED_MXFP8).  h_scale (NVFP4): as in
+        from_nvfp4."""
         nv = fmt == MOE_SCALED_NVFP4
+        if h_scale is not None:
+            h_scale = h_scale.to(device=device, dtype=torch.float32).contiguous()
 
         def mat(m, factor):
             G, N, n = m.shape

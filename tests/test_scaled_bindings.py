@@ -90,3 +90,31 @@ def test_descriptors(make):
         with pytest.raises(qm.MoeError) as e:
             make(*bad)
         assert e.value.status == qm.MOE_ERR_INVALID_ARG
+
+
+SHAPE = synth.LayerShape(hidden=128, inter=64, n_experts=4, top_k=2, fmt="nvfp4")
+
+
+@pytest.mark.parametrize("h_scale", [torch.full((5,), 0.5, dtype=torch.float16), torch.full((5,), 0.5, dtype=torch.float64),
+                                     torch.tensor([0.5]).expand(5), torch.full((5,), 0.5)], ids=["fp16", "fp64", "expanded", "fp32"])
+def test_quantized_layer_takes_any_calibration(monkeypatch, h_scale):
+    """The kernels read fp32 factors of h, one after the other, whatever the calibration came in."""
+    monkeypatch.setattr(qm, "moe_quantize", lambda *a: None)
+    G, H, I = 5, SHAPE.hidden, SHAPE.inter
+    gen = torch.Generator().manual_seed(0)
+    gate, up, down = (torch.randn(s, generator=gen) for s in ((G, I, H), (G, I, H), (G, H, I)))
+    layer = qm.ScaledLayer.quantized(synth.make_weights(SHAPE, 1), NV, gate, up, down, h_scale, device="cpu")
+    held = layer.tensors[5]
+    assert held.dtype == torch.float32 and held.is_contiguous() and torch.equal(held, torch.full((G,), 0.5))
+    assert layer.w.h_scale == held.data_ptr()
+    assert torch.equal(layer.tensors[4].tensors[2], (down.abs().amax((1, 2)) / 2688) * 0.5)
+
+
+def test_layer_refuses_factors_it_would_misread():
+    router = [U, Y, Y]
+    five = F[:5]
+    qm.ScaledLayer(SHAPE, NV, router, Y, MAT, MAT, MAT, five)
+    for v, h_scale in ((Y, five.double()), (Y, F[:10:2]), (F, five), (Y[::2], five), (Y, F[:4]), (Y, F[:1])):
+        with pytest.raises(qm.MoeError) as e:
+            qm.ScaledLayer(SHAPE, NV, router, v, MAT, MAT, MAT, h_scale)
+        assert e.value.status == qm.MOE_ERR_INVALID_ARG
