@@ -188,3 +188,28 @@ def test_few_rows_scales_past_fp32(ea, ew, small):
     y, ws = Out((R, N), torch.float32), workspace()
     qm.moe_scaled_gemm(M8, a, w, R, N, K, 1, None, y.t, ws)
     assert (np.abs(y.check() - want) <= product_error(K) * mag + K // 32 * 2.0 ** -149).all()
+
+
+@pytest.mark.parametrize("fmt,K", [(NV, 64), (NV, 128), (NV, 192), (NV, 256), (M8, 128), (M8, 256)])
+@pytest.mark.parametrize("sizes", SIZES)
+@pytest.mark.parametrize("N", [8, 136, 2056])
+def test_gemm_few_of_a_single_step(monkeypatch, fmt, K, sizes, N):
+    """Sums that one step of a tile would hold, and steps that end inside a warp's."""
+    monkeypatch.setitem(T.GROUPS, "few", SIZES[sizes])
+    T.test_gemm(fmt, "few", N, K)
+
+
+@pytest.mark.parametrize("fmt,K", [(NV, 64), (NV, 256), (M8, 128), (M8, 256)])
+@pytest.mark.parametrize("R,G,N", [(1, 1, 10240), (1, 1, 10248), (20, 1, 512), (20, 1, 520), (40, 33, 1024), (40, 33, 1032)])
+def test_single_steps_around_the_limits(fmt, K, R, G, N):
+    """As many outputs as run a row at a time and a few more."""
+    test_gemm_around_the_limits(fmt, R, G, N, K)
+
+
+@pytest.mark.parametrize("fmt", [NV, M8])
+@pytest.mark.parametrize("sizes", ["one", "apart", "holes"])
+@pytest.mark.parametrize("inter", [128, 640])
+def test_swiglu_few_of_a_single_step(monkeypatch, fmt, sizes, inter):
+    monkeypatch.setitem(T.GROUPS, "few", SIZES[sizes])
+    for K in (128, 256):
+        T.test_swiglu(fmt, "few", inter, K)
