@@ -971,10 +971,11 @@ cudaError_t launch_scaled_gemm(const ScaledGemmArgs &a, int fmt, bool swiglu, cu
     // of 9 experts each, inter 512 (9216, 18432, 27648 gate and up outputs) NVFP4 7.4 / 4.7, 7.9 / 6.7, 9.3 / 11.2; their down
     // products (18432, 36864, 55296) 4.4 / 3.8, 5.0 / 4.2, 6.2 / 6.1.  A single step (K <= 256) the same: K = 256, NVFP4, 1 x 4096
     // 2.4 / 1.7, 1 x 10240 2.6 / 2.2, 9 groups' rows x 2048 3.6 / 2.9, 40 x 1024 5.4 / 4.1; K = 128, MXFP8, 2.3 / 1.6, 2.5 / 2.0,
-    // 3.5 / 2.7, 5.0 / 4.1.  The SwiGLU alone keeps its single steps in tiles (one token's of inter 512 4.2 / 2.5): hidden <= 256 is
+    // 3.5 / 2.7, 5.0 / 4.1; but where rows must share groups their tiles are few (1280 x 32 to 20 x 2048 in 3 groups 3.1 to 3.6 / 4.0,
+    // at half as many outputs 3.1 to 3.6 / 3.2).  The SwiGLU alone keeps its single steps in tiles (one token's of inter 512 4.2 / 2.5): hidden <= 256 is
     // a test's size, and there a layer's bounded waits are to be met at one token too.
     const long long outputs = (long long)a.R * ((a.N + 31) / 32 * 32) * (swiglu ? 2 : 1);
-    const int most = !a.offsets ? 10240 : a.K <= 512 ? 40960 : 20480;
+    const int most = !a.offsets ? 10240 : a.K <= 512 && (a.K > 256 || a.G >= a.R) ? 40960 : 20480;
     if (outputs <= most && !(swiglu && a.K <= 256)) return launch_scaled_vec(a, fmt, swiglu, st);
     if (fmt == MOE_SCALED_NVFP4)
         return swiglu ? launch_fmt<MOE_SCALED_NVFP4, true>(a, st) : launch_fmt<MOE_SCALED_NVFP4, false>(a, st);

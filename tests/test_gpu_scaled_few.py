@@ -213,3 +213,10 @@ def test_swiglu_few_of_a_single_step(monkeypatch, fmt, sizes, inter):
     monkeypatch.setitem(T.GROUPS, "few", SIZES[sizes])
     for K in (128, 256):
         T.test_swiglu(fmt, "few", inter, K)
+
+
+@pytest.mark.parametrize("fmt,K", [(NV, 64), (NV, 256), (M8, 128)])
+@pytest.mark.parametrize("R,G,N", [(20, 33, 2048), (20, 33, 2056), (20, 19, 1024), (20, 19, 1032), (640, 3, 32), (640, 3, 40)])
+def test_single_steps_of_more_and_fewer_groups_than_rows(fmt, K, R, G, N):
+    """The limit is another where rows must share groups."""
+    test_gemm_around_the_limits(fmt, R, G, N, K)
