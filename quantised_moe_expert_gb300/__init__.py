@@ -536,8 +536,8 @@ class ScaledLayer:
 
 
 def calibrate_h_scale(layer: DeviceLayer, x: torch.Tensor, margin: float = 1.0) -> torch.Tensor:
-    """The NVFP4 factor of h of every expert (shared expert last) from a batch of tokens: the largest |h| the layer
-    computes on x, over all experts, times margin, over 2688."""
+    """The NVFP4 factor of h, the same for every expert (shared expert last), from a batch of tokens: the largest |h| the
+    layer computes on x, over all experts, times margin, over 2688."""
     T, s = x.shape[0], layer.shape
     ws = workspace(layer.cfg, T, x.device)
     i32 = lambda *n: torch.empty(n, dtype=torch.int32, device=x.device)

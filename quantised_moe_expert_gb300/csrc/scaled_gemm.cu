@@ -21,10 +21,12 @@
 //
 // Bounds and measurements (hidden 2048, inter 512, 257 groups): 512 tokens, NVFP4, the gate/up pair 51 us (6.1 TB/s
 // of weights and rows) and the down products 32 us (5.5 TB/s): HBM.  4096 tokens, MXFP8, 93 and 66 us: the copies
-// that widen the 4-bit codes, about 32 bytes of shared memory a cycle.  Small products are paced by 300 to 430 ns a
-// K step for the issue of its scale copies and MMAs (16 x 4096 x 2048 NVFP4 4.5 us); those of fewest rows go to
-// scaled_vec.cu.  8192 x 8192 x 4096 NVFP4 101 us, 5.4 PFLOP/s: refilling
-// stages from L2 (see the pair below).
+// that widen the 4-bit codes, about 32 bytes of shared memory a cycle, and in the down products (4 steps a tile) the
+// change of tile as well.  Small products: 0.28 to 0.30 us a K step (NVFP4, 16 rows; the issue of its 8 scale copies and
+// 4 MMAs, some 460 cycles, is most of it) or 0.21 to 0.23 (MXFP8, whose 2 copies and 4 MMAs would take 0.13: what paces
+// it has not been found), behind a launch (16 x 4096 x 2048 NVFP4 4.5 us); those of fewest rows go to scaled_vec.cu.
+// 8192 x 8192 x 4096 NVFP4 100 us, 5.5 PFLOP/s: of 13,100 cycles a tile 8,000 of products, 2,300 until the last
+// tile's accumulators are read and 2,700 for full stages (see the pair below).
 #include "scaled.cuh"
 #include "tc_ptx.cuh"
 #include "tma_host.cuh"
