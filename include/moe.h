@@ -464,6 +464,141 @@ MOE_API int moe_scaled_forward(const moe_config *cfg, const moe_scaled_weights *
                                const float *router_bias, const float *logits_in, uint16_t *y, int32_t *ids_out,
                                uint16_t *p_out, uint16_t *w_shared_out, void *ws, size_t ws_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * 16-bit operators: the layer's products on bf16 matrices (before they are
+ * quantised, or to train them), the norms around it, and the backward pass of
+ * each.  They stand beside the block-scaled operators and share their groups:
+ * rows sorted by group, group g's rows offsets[g] .. offsets[g + 1] - 1 (the
+ * last group's end at R - 1); rows before offsets[0] belong to no group and are
+ * neither read nor written.  offsets with an entry outside [0, R] or below its
+ * predecessor: nothing is computed and MOE_ERR_DEVICE is reported.
+ * All rows, matrices and vectors are bf16 and dense unless a parameter says
+ * otherwise; products, sums and statistics are fp32 and rounded once, to the
+ * type that is written.  Pointers 16-byte aligned (offsets, inv_perm 4-byte).
+ * With no rows, pointers to rows may be NULL.  Outputs must not overlap inputs
+ * except where that is allowed.  ws as for the block-scaled operators (a
+ * header of MOE_SCALED_WS_BYTES), and more where a size function says so.
+ * Non-finite values reach the outputs that their formulas use them in, and no
+ * other row's.  The same call gives the same bits; sizes select the kernels, so a
+ * row's last bits can depend on R. */
+enum moe_activation {
+    MOE_ACT_NONE = 0,
+    MOE_ACT_SILU = 1,     /* v sigmoid(v) */
+    MOE_ACT_GELU = 2,     /* tanh form: v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+    MOE_ACT_RELU = 3,
+    MOE_ACT_SIGMOID = 4   /* gates of moe_gated_norm only */
+};
+
+/* Grouped product with an epilogue:
+ *   pre = a w_g^T + a2 w2_g^T + bias_g,  y = act(pre) + residual
+ *   a            [R, K]
+ *   w            [G, N, K], or with w_transposed = 1 [G, K, N]: the input gradient of a product
+ *                with the matrices [G, N', K'] is this with N = K', K = N'
+ *   a2, w2       a second pair of the same sizes (both or neither): the input gradient
+ *                of a gate/up pair in one sum
+ *   bias         [G, N] or NULL
+ *   residual     [R, N] or NULL; may be y itself
+ *   pre_out      [R, N] or NULL: pre, rounded, as moe_act_grad takes it
+ *   y            [R, N], fp32 with y_f32 = 1
+ * N, K: multiples of 8, K at most 65536, N at most 2^20; G <= 1024; R <= 2^21.
+ * offsets may be NULL when G == 1.  R == 0 enqueues nothing. */
+MOE_API int moe_gemm(const uint16_t *a, const uint16_t *w, const uint16_t *a2, const uint16_t *w2, int w_transposed, int R,
+                     int N, int K, int G, const int32_t *offsets, const uint16_t *bias, int act, const uint16_t *residual,
+                     uint16_t *pre_out, void *y, int y_f32, void *ws, size_t ws_bytes, void *stream);
+
+/* Gated pair: g = a gate^T + gate_bias, u = a up^T + up_bias, h = act(g) u, from
+ * the unrounded g and u.
+ *   gate, up            [G, inter, K]
+ *   gate_bias, up_bias  [G, inter] or NULL
+ *   gate_out, up_out    [R, inter] or NULL (both or neither): g and u, rounded
+ *   h                   [R, inter]
+ * Sizes as in moe_gemm. */
+MOE_API int moe_gemm_glu(const uint16_t *a, const uint16_t *gate, const uint16_t *up, const uint16_t *gate_bias,
+                         const uint16_t *up_bias, int act, int R, int inter, int K, int G, const int32_t *offsets,
+                         uint16_t *gate_out, uint16_t *up_out, uint16_t *h, void *ws, size_t ws_bytes, void *stream);
+
+/* Weight gradient of a grouped product: dw_g = dy_g^T x_g and db_g = the column
+ * sums of dy_g over the group's rows (zero for a group without rows).
+ *   dy [R, N], x [R, K]
+ *   dw [G, N, K], db [G, N] or NULL: bf16, or fp32 with f32 = 1
+ *   accumulate  1: added to what dw and db hold (f32 only)
+ * Sizes as in moe_gemm, N at most 2^20 and K at most 65536. */
+MOE_API int moe_gemm_wgrad(const uint16_t *dy, const uint16_t *x, int R, int N, int K, int G, const int32_t *offsets,
+                           int accumulate, void *dw, void *db, int f32, void *ws, size_t ws_bytes, void *stream);
+
+/* Gradient through an activation, element by element over R rows of N:
+ *   up NULL:  dpre = dy act'(pre)
+ *   else      dpre = dy up act'(pre), dup = dy act(pre)     (a gated pair)
+ * dpre may be dy or pre itself, dup may be dy, up or pre (but not dpre).
+ * N: a multiple of 8. */
+MOE_API int moe_act_grad(int act, const uint16_t *dy, const uint16_t *pre, const uint16_t *up, int R, int N, uint16_t *dpre,
+                         uint16_t *dup, void *stream);
+
+/* T rows of n elements of x into the expert-sorted rows of their k picks, y[inv_perm[t k + j]] = x[t], and with
+ * has_shared into row T k + t (the shared expert's group).  inv_perm as from moe_permute; an entry outside
+ * [0, T k) is reported (MOE_ERR_DEVICE) and its row not written.  n: a multiple of 8, at most 2^20.  The backward pass is
+ * moe_weighted_sum without weights. */
+MOE_API int moe_dispatch(const uint16_t *x, int T, int n, int k, int has_shared, const int32_t *inv_perm, uint16_t *y,
+                         void *ws, size_t ws_bytes, void *stream);
+
+/* y[t] = sum_j p[t, j] rows[inv_perm[t k + j]] + w_shared[t] rows[T k + t], picks in
+ * order, rounded once.
+ *   rows      [T k + T has_shared, n]
+ *   p         [T, k], or NULL: ones (then w_shared NULL too)
+ *   w_shared  [T]; NULL with has_shared == 0, or without p
+ * An inv_perm entry outside [0, T k) is reported and its term left out. */
+MOE_API int moe_weighted_sum(const uint16_t *rows, int T, int n, int k, int has_shared, const int32_t *inv_perm,
+                             const uint16_t *p, const uint16_t *w_shared, uint16_t *y, void *ws, size_t ws_bytes, void *stream);
+
+/* Its backward pass, from dy [T, n]:
+ *   drows      [T k + T has_shared, n]: p[t, j] dy[t] in row inv_perm[t k + j], w_shared[t] dy[t] in row T k + t; may be rows
+ *   dp         fp32 [T, k] or NULL: dy[t] . rows[inv_perm[t k + j]] (0 where the entry is out of range)
+ *   dw_shared  fp32 [T] or NULL
+ * rows may be NULL when dp and dw_shared are.  drows' rows that no entry names are not written. */
+MOE_API int moe_weighted_sum_grad(const uint16_t *dy, const uint16_t *rows, int T, int n, int k, int has_shared,
+                                  const int32_t *inv_perm, const uint16_t *p, const uint16_t *w_shared, uint16_t *drows,
+                                  float *dp, float *dw_shared, void *ws, size_t ws_bytes, void *stream);
+
+/* Shapes of a gate. */
+enum moe_gate_shape {
+    MOE_GATE_NONE = 0,
+    MOE_GATE_ROW = 1,      /* [T], one value a token */
+    MOE_GATE_CHANNEL = 2,  /* [n], a scale per channel */
+    MOE_GATE_FULL = 3      /* [T, n] */
+};
+
+/* The norm after a block, its gate, the residual add and the norm before the next block, of T rows of n elements:
+ *   b = x rsqrt(mean(x^2) + eps) (weight_offset + post_weight)     (b = x without post_norm)
+ *   s = bf16(residual + scale f(gate) b)
+ *   y = s rsqrt(mean(s^2) + eps) (weight_offset + pre_weight)
+ *   gate          its shape gate_shape; NULL with MOE_GATE_NONE
+ *   gate_act      f: MOE_ACT_NONE, MOE_ACT_SILU or MOE_ACT_SIGMOID (NONE without a gate)
+ *   residual      [T, n] or NULL
+ *   post_weight, pre_weight  [n] or NULL for none (no offset either); post_weight NULL without post_norm
+ *   sum_out       [T, n] s, or NULL; may be x or residual itself
+ *   y_out         [T, n] or NULL
+ * The sums of squares are fp32 sums: |x| and |s| have to stay below about 1e19 / sqrt(n).
+ * n: a multiple of 8, at most 8192. */
+MOE_API int moe_gated_norm(const uint16_t *x, const uint16_t *residual, const uint16_t *gate, int gate_shape, int gate_act,
+                           float scale, int post_norm, const uint16_t *post_weight, const uint16_t *pre_weight,
+                           float weight_offset, float eps, int T, int n, uint16_t *sum_out, uint16_t *y_out, void *stream);
+
+/* Bytes of workspace moe_gated_norm_grad needs (T >= 0, n as there). */
+MOE_API int moe_gated_norm_workspace_size(int T, int n, size_t *bytes);
+
+/* Its backward pass.  x, gate, weights and factors as there; sum is the s that it gave.
+ *   dy, dsum    [T, n] gradients of y and of s (from the next residual add); either may be NULL (zero), not both
+ *   dx          [T, n]; may be x, dy or dsum itself
+ *   dresidual   [T, n] or NULL: the gradient of s as a whole; may be sum, dy or dsum itself (but not dx)
+ *   dgate       the gate's gradient, or NULL: bf16 [T, n] (FULL), fp32 [T] (ROW), fp32 [n] (CHANNEL)
+ *   dpost_weight, dpre_weight  fp32 [n] or NULL; dpost_weight only with post_norm, dpre_weight only with dy
+ * Sums over rows are taken in a fixed order that depends on T and n.  With T == 0 the sums over rows are set to zero. */
+MOE_API int moe_gated_norm_grad(const uint16_t *x, const uint16_t *sum, const uint16_t *gate, int gate_shape, int gate_act,
+                                float scale, int post_norm, const uint16_t *post_weight, const uint16_t *pre_weight,
+                                float weight_offset, float eps, int T, int n, const uint16_t *dy, const uint16_t *dsum,
+                                uint16_t *dx, uint16_t *dresidual, void *dgate, float *dpost_weight, float *dpre_weight,
+                                void *ws, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

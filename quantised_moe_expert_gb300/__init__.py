@@ -38,12 +38,25 @@ MOE_SCALED_MXFP8 = 2
 MOE_SCALED_MXFP4 = 3
 MOE_SCALED_WS_BYTES = 512
 
+MOE_ACT_NONE = 0
+MOE_ACT_SILU = 1
+MOE_ACT_GELU = 2
+MOE_ACT_RELU = 3
+MOE_ACT_SIGMOID = 4
+
+MOE_GATE_NONE = 0
+MOE_GATE_ROW = 1
+MOE_GATE_CHANNEL = 2
+MOE_GATE_FULL = 3
+
 EXPORTED = ("moe_status_string", "moe_check_config", "moe_workspace_size", "moe_route", "moe_permute",
             "moe_expert_ffn", "moe_combine", "moe_forward", "moe_get_device_status", "moe_pack_down",
             "moe_expert_stages",
             "moe_decode_timeline", "moe_forward_decode_static",
             "moe_add_rmsnorm", "moe_quantize", "moe_quantize_routed", "moe_tile_scales", "moe_scaled_gemm",
-            "moe_scaled_swiglu", "moe_scaled_workspace_size", "moe_scaled_forward")
+            "moe_scaled_swiglu", "moe_scaled_workspace_size", "moe_scaled_forward",
+            "moe_gemm", "moe_gemm_glu", "moe_gemm_wgrad", "moe_act_grad", "moe_dispatch", "moe_weighted_sum",
+            "moe_weighted_sum_grad", "moe_gated_norm", "moe_gated_norm_workspace_size", "moe_gated_norm_grad")
 
 
 class MoeError(RuntimeError):
@@ -136,6 +149,18 @@ def load(build: bool = True):
         lib.moe_scaled_workspace_size.argtypes = [P(moe_config), _I, _I, P(ctypes.c_size_t)]
         lib.moe_scaled_forward.argtypes = [P(moe_config), P(moe_scaled_weights), _VP, _I, _VP, _VP, _VP, _VP, _VP, _VP, _VP,
                                            _SZ, _VP]
+        V, I = [_VP], [_I]
+        lib.moe_gemm.argtypes = V * 4 + I * 5 + V * 2 + I + V * 3 + I + V + [_SZ] + V
+        lib.moe_gemm_glu.argtypes = V * 5 + I * 5 + V * 5 + [_SZ] + V
+        lib.moe_gemm_wgrad.argtypes = V * 2 + I * 4 + V + I + V * 2 + I + V + [_SZ] + V
+        lib.moe_act_grad.argtypes = I + V * 3 + I * 2 + V * 3
+        lib.moe_dispatch.argtypes = V + I * 4 + V * 3 + [_SZ] + V
+        lib.moe_weighted_sum.argtypes = V + I * 4 + V * 5 + [_SZ] + V
+        lib.moe_weighted_sum_grad.argtypes = V * 2 + I * 4 + V * 7 + [_SZ] + V
+        norm = I * 2 + [F] + I + V * 2 + [F, F] + I * 2
+        lib.moe_gated_norm.argtypes = V * 3 + norm + V * 3
+        lib.moe_gated_norm_workspace_size.argtypes = [_I, _I, P(ctypes.c_size_t)]
+        lib.moe_gated_norm_grad.argtypes = V * 3 + norm + V * 8 + [_SZ] + V
         for name in EXPORTED:
             if name != "moe_status_string":
                 getattr(lib, name).restype = ctypes.c_int
@@ -431,6 +456,113 @@ def moe_scaled_forward(cfg, w, x, T, router_bias, logits_in, y, ids_out, p_out, 
                                    _ptr(ids_out), _ptr(p_out), _ptr(w_shared_out), _ptr(ws), ws.numel() * ws.element_size(),
                                    _stream(stream))
     _check(fn, rc)
+
+
+# The 16-bit operators: the same rules.
+
+def moe_gemm(a, w, a2, w2, w_transposed, R, N, K, G, offsets, bias, act, residual, pre_out, y, ws, stream=None):
+    """y: a bf16 (or its bits, as a 16-bit integer) or float32 tensor [R, N]."""
+    fn = "moe_gemm"
+    rc = (_lib or load()).moe_gemm(_dense(fn, a, _BITS16), _dense(fn, w, _BITS16), _dense_or_none(fn, a2, _BITS16),
+                                   _dense_or_none(fn, w2, _BITS16), w_transposed, R, N, K, G, _dense_or_none(fn, offsets, _I32),
+                                   _dense_or_none(fn, bias, _BITS16), act, _dense_or_none(fn, residual, _BITS16),
+                                   _dense_or_none(fn, pre_out, _BITS16), _dense(fn, y, _BITS16_F32), y.dtype == torch.float32,
+                                   ws.data_ptr(), ws.nbytes, _handle(stream))
+    if rc:
+        raise MoeError(fn, rc)
+
+
+def moe_gemm_glu(a, gate, up, gate_bias, up_bias, act, R, inter, K, G, offsets, gate_out, up_out, h, ws, stream=None):
+    fn = "moe_gemm_glu"
+    rc = (_lib or load()).moe_gemm_glu(_dense(fn, a, _BITS16), _dense(fn, gate, _BITS16), _dense(fn, up, _BITS16),
+                                       _dense_or_none(fn, gate_bias, _BITS16), _dense_or_none(fn, up_bias, _BITS16), act, R, inter, K,
+                                       G, _dense_or_none(fn, offsets, _I32), _dense_or_none(fn, gate_out, _BITS16),
+                                       _dense_or_none(fn, up_out, _BITS16), _dense(fn, h, _BITS16), ws.data_ptr(), ws.nbytes,
+                                       _handle(stream))
+    if rc:
+        raise MoeError(fn, rc)
+
+
+def moe_gemm_wgrad(dy, x, R, N, K, G, offsets, accumulate, dw, db, ws, stream=None):
+    """dw, db: both bf16 (or their bits) or both float32."""
+    fn = "moe_gemm_wgrad"
+    f32 = dw.dtype == torch.float32
+    types = _F32 if f32 else _BITS16
+    rc = (_lib or load()).moe_gemm_wgrad(_dense(fn, dy, _BITS16), _dense(fn, x, _BITS16), R, N, K, G, _dense_or_none(fn, offsets, _I32),
+                                         accumulate, _dense(fn, dw, types), _dense_or_none(fn, db, types), f32, ws.data_ptr(),
+                                         ws.nbytes, _handle(stream))
+    if rc:
+        raise MoeError(fn, rc)
+
+
+def moe_act_grad(act, dy, pre, up, R, N, dpre, dup, stream=None):
+    fn = "moe_act_grad"
+    rc = (_lib or load()).moe_act_grad(act, _dense(fn, dy, _BITS16), _dense(fn, pre, _BITS16), _dense_or_none(fn, up, _BITS16), R, N,
+                                       _dense(fn, dpre, _BITS16), _dense_or_none(fn, dup, _BITS16), _handle(stream))
+    if rc:
+        raise MoeError(fn, rc)
+
+
+def moe_dispatch(x, T, n, k, has_shared, inv_perm, y, ws, stream=None):
+    fn = "moe_dispatch"
+    rc = (_lib or load()).moe_dispatch(_dense(fn, x, _BITS16), T, n, k, has_shared, _dense(fn, inv_perm, _I32), _dense(fn, y, _BITS16),
+                                       ws.data_ptr(), ws.nbytes, _handle(stream))
+    if rc:
+        raise MoeError(fn, rc)
+
+
+def moe_weighted_sum(rows, T, n, k, has_shared, inv_perm, p, w_shared, y, ws, stream=None):
+    fn = "moe_weighted_sum"
+    rc = (_lib or load()).moe_weighted_sum(_dense(fn, rows, _BITS16), T, n, k, has_shared, _dense(fn, inv_perm, _I32),
+                                           _dense_or_none(fn, p, _BITS16), _dense_or_none(fn, w_shared, _BITS16),
+                                           _dense(fn, y, _BITS16), ws.data_ptr(), ws.nbytes, _handle(stream))
+    if rc:
+        raise MoeError(fn, rc)
+
+
+def moe_weighted_sum_grad(dy, rows, T, n, k, has_shared, inv_perm, p, w_shared, drows, dp, dw_shared, ws, stream=None):
+    fn = "moe_weighted_sum_grad"
+    rc = (_lib or load()).moe_weighted_sum_grad(_dense(fn, dy, _BITS16), _dense_or_none(fn, rows, _BITS16), T, n, k, has_shared,
+                                                _dense(fn, inv_perm, _I32), _dense(fn, p, _BITS16),
+                                                _dense_or_none(fn, w_shared, _BITS16), _dense(fn, drows, _BITS16),
+                                                _dense_or_none(fn, dp, _F32), _dense_or_none(fn, dw_shared, _F32), ws.data_ptr(),
+                                                ws.nbytes, _handle(stream))
+    if rc:
+        raise MoeError(fn, rc)
+
+
+def moe_gated_norm(x, residual, gate, gate_shape, gate_act, scale, post_norm, post_weight, pre_weight, weight_offset, eps, T, n,
+                   sum_out, y_out, stream=None):
+    fn = "moe_gated_norm"
+    rc = (_lib or load()).moe_gated_norm(_dense(fn, x, _BITS16), _dense_or_none(fn, residual, _BITS16),
+                                         _dense_or_none(fn, gate, _BITS16), gate_shape, gate_act, scale, post_norm,
+                                         _dense_or_none(fn, post_weight, _BITS16), _dense_or_none(fn, pre_weight, _BITS16),
+                                         weight_offset, eps, T, n, _dense_or_none(fn, sum_out, _BITS16),
+                                         _dense_or_none(fn, y_out, _BITS16), _handle(stream))
+    if rc:
+        raise MoeError(fn, rc)
+
+
+def moe_gated_norm_workspace_size(T: int, n: int) -> int:
+    size = ctypes.c_size_t(0)
+    _check("moe_gated_norm_workspace_size", load().moe_gated_norm_workspace_size(T, n, ctypes.byref(size)))
+    return size.value
+
+
+def moe_gated_norm_grad(x, sum, gate, gate_shape, gate_act, scale, post_norm, post_weight, pre_weight, weight_offset, eps, T, n,
+                        dy, dsum, dx, dresidual, dgate, dpost_weight, dpre_weight, ws, stream=None):
+    """dgate: bf16 (or its bits) with MOE_GATE_FULL, else float32."""
+    fn = "moe_gated_norm_grad"
+    rc = (_lib or load()).moe_gated_norm_grad(_dense(fn, x, _BITS16), _dense(fn, sum, _BITS16), _dense_or_none(fn, gate, _BITS16),
+                                              gate_shape, gate_act, scale, post_norm, _dense_or_none(fn, post_weight, _BITS16),
+                                              _dense_or_none(fn, pre_weight, _BITS16), weight_offset, eps, T, n,
+                                              _dense_or_none(fn, dy, _BITS16), _dense_or_none(fn, dsum, _BITS16),
+                                              _dense(fn, dx, _BITS16), _dense_or_none(fn, dresidual, _BITS16),
+                                              _dense_or_none(fn, dgate, _BITS16 if gate_shape == MOE_GATE_FULL else _F32),
+                                              _dense_or_none(fn, dpost_weight, _F32), _dense_or_none(fn, dpre_weight, _F32),
+                                              ws.data_ptr(), ws.nbytes, _handle(stream))
+    if rc:
+        raise MoeError(fn, rc)
 
 
 # ---------------------------------------------------------------- conveniences
