@@ -1,165 +1,901 @@
-// Grouped products of bf16 rows with bf16 matrices, 32-bit sums, with their epilogue, and their weight gradients.
+// Grouped products of bf16 rows with bf16 matrices on the tensor cores, with their epilogue, and their weight gradients.
 //
-//   y[r] = act(sum over the pairs of a[r] w_g^T + bias_g) + residual[r]     (GLU: act(a gate_g^T + ..) (a up_g^T + ..))
-//   dw_g = sum over the group's rows of dy[r]^T x[r],  db_g = sum of dy[r]
+//   NT  y[r, n]  = act(sum over the pairs of a[r] . w_g[n] + bias_g[n]) + residual[r, n]      w [G, N, K]
+//       GLU: y[r, n] = act(a[r] . gate_g[n] + ..) (a[r] . up_g[n] + ..)
+//   NN  the same with w [G, K, N]: the input gradient of an NT product
+//   TN  dw_g[n, k] (+)= sum over group g's rows r of dy[r, n] x[r, k]
 //
-// Tiles of 64 x 64 outputs on the fp32 units, operands through shared memory 16 elements deep.
+// All sums are fp32, in tensor memory.  An operand whose rows run along the sum (K-major: a, w of NT) is copied as rows of 64
+// elements, one whose rows run across it (MN-major: w of NN, dy, x of TN) as blocks of 64 columns x 64 terms; either is 128-byte
+// swizzled shared memory that tcgen05.mma reads in place, so no operand is ever transposed.
+// Tiles of 128 outputs' rows x BN columns, 64 terms a step, in a ring of stages; two accumulators, so that a tile leaves
+// tensor memory under the next one's products.  Where a group's rows end inside a tile the rest is computed and not
+// written (NT, NN); where they end inside a step of a sum (TN) a warp overwrites the rest of both operands with zeros
+// before the products read it, since those rows are other groups' and may hold anything.
+//
+// One CTA per SM walks over the tiles: warp 0 copies (TMA), warp 1 issues the products, warp 2 clears the ends of sums,
+// warps 4-11 read the accumulators and write.
 #include "bf16.cuh"
 #include "tc_ptx.cuh"
+#include "tma_host.cuh"
 
 namespace qmoe {
 namespace {
 
-using tc::pdl_trigger;
-using tc::pdl_wait;
+using namespace tc;
 
-constexpr int kThreads = 256, kTile = 64, kDeep = 16, kMaxGroups = 1024;
+constexpr int kThreads = 384;
+constexpr int kMaxGroups = 1024;
+constexpr int kStep = 64;                          // terms of a step: 128 bytes of a K-major row
+constexpr int kBlockBytes = 64 * 128;              // an MN-major block: 64 terms x 64 columns
+enum Kind { kNT, kNN, kTN };
 
-// Checks the offsets; every thread takes part.  False (and a report): nothing is computed.
-__device__ __forceinline__ bool offsets_ok(const int32_t *offsets, int G, int R, int *status)
+template <int KIND, bool DUAL, int BN, bool PAIR>
+struct Plan {
+    static constexpr int kOutN = DUAL ? BN / 2 : BN;                 // output columns of a tile
+    static constexpr int kRows = PAIR ? 256 : 128;                   // output rows of a tile
+    static constexpr int kHeld = PAIR ? BN / 2 : BN;                 // columns of the second operand in this CTA
+    static constexpr int kABytes = 128 * 128, kBBytes = kHeld * 128, kStageBytes = kABytes + kBBytes;
+    static constexpr int kStages = PAIR ? 6 : BN == 256 ? 4 : BN == 128 ? 6 : 8;
+    static constexpr int kStaged = 64;                               // bytes of a row that an epilogue warp stages at a time
+    static constexpr int kOutBytes = 8 * 32 * kStaged;
+    static constexpr int kOutAt = kStages * kStageBytes, kSmem = kOutAt + kOutBytes + 1024;
+};
+
+struct Maps {
+    CUtensorMap a[2], a32[2], w[2];                  // first operand(s) in whole and in 32-row boxes, second operand(s)
+};
+
+// What a launch computes.
+struct ProductArgs {
+    const int32_t *offsets;
+    const uint16_t *bias[2], *residual;
+    uint16_t *pre[2];
+    void *y;
+    int *status;
+    int R, M, N, K, G;                               // rows; TN: output rows of a matrix; output columns; terms (NT, NN)
+    int pairs, act, y_f32, accumulate;
+    long long wait_limit;
+};
+
+struct Shared {
+    uint64_t full[8], empty[8], tail[8], cleared[8], acc_full[2], acc_empty[2], drain;
+    uint32_t tmem;
+    int abort;
+    int bad, groups, row_tiles;                      // malformed offsets; groups with rows; their row tiles
+    int gave_up, issued[2];                          // a pair's: whether any of its waits ran out; copies of each CTA
+    int2 warp_sum[kThreads / 32];
+    int2 group[kMaxGroups + 1];                      // NT, NN: those groups: row tiles before it, start << 10 | group; TN: offsets
+};
+
+constexpr int kGroupBits = 10;
+static_assert(kMaxGroups == 1 << kGroupBits, "the table's packing");
+
+struct Tile {
+    int g, row0, rows, col0;                         // first output row (of all rows; TN: of the matrix), how many, first column
+    int first, terms;                                // TN: first row of the sum, rows of it
+};
+
+// The groups with rows and the tiles before each (NT, NN), or the groups' first rows (TN).  Every thread takes part.
+template <int KIND, int ROWS>
+__device__ __forceinline__ void build_table(const ProductArgs &a, Shared &sh, int warp, int lane)
 {
-    int bad = 0;
-    for (int i = threadIdx.x; i < G; i += kThreads) {
-        const int o = offsets[i], next = i + 1 < G ? offsets[i + 1] : R;
-        bad |= o < 0 || o > R || next < o;
+    constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
+    const int g0 = threadIdx.x * kPer;
+    int o[kPer + 1];
+#pragma unroll
+    for (int i = 0; i <= kPer; ++i) o[i] = g0 + i < a.G ? a.offsets[g0 + i] : a.R;
+    int2 n = make_int2(0, 0);
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (o[i] < 0 || o[i] > a.R || o[i + 1] < o[i]) sh.bad = 1;
+        if (KIND == kTN && g0 + i <= a.G) sh.group[g0 + i].x = o[i];
+        n.x += (max(o[i + 1] - o[i], 0) + ROWS - 1) / ROWS;
+        n.y += o[i + 1] > o[i];
     }
-    bad = __syncthreads_or(bad);
-    if (bad && threadIdx.x == 0 && blockIdx.x == 0) record_status(status, MOE_ERR_DEVICE);
-    return !bad;
+    if (KIND == kTN) {
+        if (threadIdx.x == 0) sh.group[a.G].x = a.R;
+        __syncthreads();
+        if (threadIdx.x == 0 && sh.bad) {
+            sh.row_tiles = 0;
+            record_status(a.status, MOE_ERR_DEVICE);
+        }
+        return;
+    }
+    int2 incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int x = __shfl_up_sync(0xFFFFFFFFu, incl.x, d), y = __shfl_up_sync(0xFFFFFFFFu, incl.y, d);
+        if (lane >= d) {
+            incl.x += x;
+            incl.y += y;
+        }
+    }
+    if (lane == 31) sh.warp_sum[warp] = incl;
+    __syncthreads();
+    int2 base = make_int2(incl.x - n.x, incl.y - n.y);
+    for (int w = 0; w < warp; ++w) {
+        base.x += sh.warp_sum[w].x;
+        base.y += sh.warp_sum[w].y;
+    }
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        if (o[i + 1] <= o[i] || sh.bad) continue;
+        sh.group[base.y] = make_int2(base.x, o[i] << kGroupBits | (g0 + i));
+        base.x += (o[i + 1] - o[i] + ROWS - 1) / ROWS;
+        base.y += 1;
+    }
+    if (threadIdx.x == kThreads - 1) {
+        sh.groups = base.y;
+        sh.row_tiles = sh.bad ? 0 : base.x;
+        if (!sh.bad) sh.group[base.y] = make_int2(base.x, (int)((uint32_t)a.R << kGroupBits));
+        if (sh.bad) record_status(a.status, MOE_ERR_DEVICE);
+    }
 }
 
-__device__ __forceinline__ float load16(const uint16_t *p, size_t row, size_t pitch, int col)
+// Tile `tile`: column tiles of a row tile follow each other.
+template <int KIND, int ROWS, int OUT_N>
+__device__ __forceinline__ Tile tile_at(const ProductArgs &a, const Shared &sh, int tile, int n_tiles)
 {
-    return bf16_bits_to_float(p[row * pitch + col]);
+    const int mt = tile / n_tiles;
+    Tile t;
+    t.col0 = (tile - mt * n_tiles) * OUT_N;
+    t.first = t.terms = 0;
+    if (KIND == kTN) {
+        const int per = (a.M + ROWS - 1) / ROWS;
+        t.g = mt / per;
+        t.row0 = (mt - t.g * per) * ROWS;
+        t.rows = min(a.M - t.row0, ROWS);
+        t.first = a.offsets ? sh.group[t.g].x : 0;
+        t.terms = (a.offsets ? sh.group[t.g + 1].x : a.R) - t.first;
+        return t;
+    }
+    if (!a.offsets) {
+        t.g = 0;
+        t.row0 = mt * ROWS;
+        t.rows = min(a.R - t.row0, ROWS);
+        return t;
+    }
+    int lo = 0, hi = sh.groups;                              // the last entry whose first tile is not past mt
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (sh.group[mid].x <= mt) lo = mid;
+        else hi = mid;
+    }
+    const int2 e = sh.group[lo];
+    const int start = (int)((uint32_t)e.y >> kGroupBits), end = (int)((uint32_t)sh.group[lo + 1].y >> kGroupBits), m = mt - e.x;
+    t.g = e.y & (kMaxGroups - 1);
+    t.row0 = start + m * ROWS;
+    t.rows = min(end - t.row0, ROWS);
+    return t;
 }
 
-__global__ void __launch_bounds__(kThreads) gemm_kernel(const __grid_constant__ GemmArgs a)
+// ------------------------------------------------------------------ descriptors
+
+// An MN-major operand in the 128-byte swizzle: blocks of 64 columns (rows of 128 bytes, one term a row), 8 terms 1024 bytes
+// apart (stride byte offset), the next 64 columns a block further (leading byte offset).
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr)
 {
-    __shared__ float sa[kDeep][kTile + 1], sw[2][kDeep][kTile + 1];
-    __shared__ int sh[3];
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(kBlockBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+// kind::f16 with bf16 operands: D f32 [4,6) = 1, A and B bf16 [7,10), [10,13) = 1, A and B MN-major [15], [16].
+template <int KIND>
+__host__ __device__ constexpr uint32_t idesc_bf16(uint32_t m, uint32_t n)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (KIND == kTN ? 1u << 15 : 0u) | (KIND != kNT ? 1u << 16 : 0u) | ((n >> 3) << 17) |
+           ((m >> 4) << 24);
+}
+template <int CG>
+__device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate, uint32_t issue)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::%6.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issue), "n"(CG)
+        : "memory");
+}
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// ------------------------------------------------------------------ epilogue
+
+// 32 rows of 64 bytes, a lane a row in 16-byte chunks, to rows `pitch` bytes apart from `dst` on, the first `rows` rows and
+// `chunks` chunks of each, through `stage`: 4 lanes write a row's bytes together.  Row r's chunk k lies at k ^ r / 2 of the
+// row, so that no bank is met twice in a phase.  ADD: fp32 values added to what is there.
+template <bool ADD>
+__device__ __forceinline__ void store_staged(uint8_t *dst, size_t pitch, const uint32_t *w, int rows, int chunks, int lane, uint8_t *stage)
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((k ^ (lane >> 1)) & 3) * 16) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    __syncwarp();
+    const int k = lane & 3;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 4;
+        uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((k ^ (r >> 1)) & 3) * 16);
+        if (r < rows && k < chunks) {
+            uint4 *p = reinterpret_cast<uint4 *>(dst + r * pitch + 16 * k);
+            if (ADD) {
+                const uint4 o = *p;
+                v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(o.x));
+                v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(o.y));
+                v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(o.z));
+                v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(o.w));
+            }
+            *p = v;
+        }
+    }
+    __syncwarp();
+}
+// The other way: the lane's row of up to 64 bytes.
+__device__ __forceinline__ void load_staged(uint32_t *w, const uint8_t *src, size_t pitch, int rows, int chunks, int lane, uint8_t *stage)
+{
+    const int k = lane & 3;
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 4;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (r < rows && k < chunks) v[i] = *reinterpret_cast<const uint4 *>(src + r * pitch + 16 * k);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = i * 8 + lane / 4;
+        *reinterpret_cast<uint4 *>(stage + r * 64 + ((k ^ (r >> 1)) & 3) * 16) = v[i];
+    }
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(stage + lane * 64 + ((j ^ (lane >> 1)) & 3) * 16);
+        w[4 * j] = u.x;
+        w[4 * j + 1] = u.y;
+        w[4 * j + 2] = u.z;
+        w[4 * j + 3] = u.w;
+    }
+    __syncwarp();
+}
+
+template <int N>
+__device__ __forceinline__ void pack_row(const float (&v)[N], uint32_t (&w)[N / 2])
+{
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+}
+
+// Adds the bias of 32 columns from `col` on (of which `cols` exist) to a row.
+__device__ __forceinline__ void add_bias(float (&v)[32], const uint16_t *bias, int cols)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (8 * i >= cols) break;
+        const uint4 b = reinterpret_cast<const uint4 *>(bias)[i];
+        const uint32_t u[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[8 * i + 2 * k] += bf16_lo(u[k]);
+            v[8 * i + 2 * k + 1] += bf16_hi(u[k]);
+        }
+    }
+}
+__device__ __forceinline__ void apply(int act, float (&v)[32])
+{
+    switch (act) {
+    case MOE_ACT_SILU:
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_value(MOE_ACT_SILU, v[i]);
+        break;
+    case MOE_ACT_GELU:
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_value(MOE_ACT_GELU, v[i]);
+        break;
+    case MOE_ACT_RELU:
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = act_value(MOE_ACT_RELU, v[i]);
+        break;
+    default: break;
+    }
+}
+
+// The warp's 32 rows x COLS columns of a tile from the accumulators (second: those of the up products) to the outputs, 32
+// columns at a time; release() once the accumulators are read.  row: the first row's index in the outputs, of which
+// `rows` exist; cols: columns from col0 on that exist; empty: a sum without terms.
+template <int KIND, bool DUAL, int COLS, class Release>
+__device__ __forceinline__ void finish(const ProductArgs &a, uint32_t d, uint32_t second, int g, size_t row, int rows, int col0, bool empty,
+                                       int lane, uint8_t *stage, Release release)
+{
+    const size_t n = a.N;
+#pragma unroll 1
+    for (int c = 0; c < COLS; c += 32) {
+        float v[32], u[32];
+        {
+            uint32_t r0[16], r1[16], s0[16], s1[16];
+            tmem_ld16(d + c, r0);
+            tmem_ld16(d + c + 16, r1);
+            if (DUAL) {
+                tmem_ld16(second + c, s0);
+                tmem_ld16(second + c + 16, s1);
+            }
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                v[i] = __uint_as_float(r0[i]);
+                v[16 + i] = __uint_as_float(r1[i]);
+                if (DUAL) {
+                    u[i] = __uint_as_float(s0[i]);
+                    u[16 + i] = __uint_as_float(s1[i]);
+                }
+            }
+        }
+        if (c + 32 >= COLS) release();
+        const int col = col0 + c, cols = a.N - col;
+        if (cols <= 0) continue;
+        const size_t at = row * n + col;
+        uint32_t w[16];
+        if (KIND == kTN) {
+            if (empty) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = 0.f;
+            }
+        } else {
+            if (a.bias[0]) add_bias(v, a.bias[0] + g * n + col, cols);
+            if (DUAL && a.bias[1]) add_bias(u, a.bias[1] + g * n + col, cols);
+            if (a.pre[0]) {
+                pack_row(v, w);
+                store_staged<false>(reinterpret_cast<uint8_t *>(a.pre[0] + at), n * 2, w, rows, cols / 8, lane, stage);
+            }
+            if (DUAL && a.pre[1]) {
+                pack_row(u, w);
+                store_staged<false>(reinterpret_cast<uint8_t *>(a.pre[1] + at), n * 2, w, rows, cols / 8, lane, stage);
+            }
+            apply(a.act, v);
+            if (DUAL) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] *= u[i];
+            }
+            if (!DUAL && a.residual) {
+                load_staged(w, reinterpret_cast<const uint8_t *>(a.residual + at), n * 2, rows, cols / 8, lane, stage);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    v[2 * i] += bf16_lo(w[i]);
+                    v[2 * i + 1] += bf16_hi(w[i]);
+                }
+            }
+        }
+        if (!DUAL && a.y_f32) {
+            uint8_t *y = reinterpret_cast<uint8_t *>(static_cast<float *>(a.y) + at);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[16 * h + i]);
+                if (KIND == kTN && a.accumulate) store_staged<true>(y + 64 * h, n * 4, w, rows, cols / 4 - 4 * h, lane, stage);
+                else store_staged<false>(y + 64 * h, n * 4, w, rows, cols / 4 - 4 * h, lane, stage);
+            }
+        } else {
+            pack_row(v, w);
+            store_staged<false>(reinterpret_cast<uint8_t *>(static_cast<uint16_t *>(a.y) + at), n * 2, w, rows, cols / 8, lane, stage);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ the kernel
+//
+// PAIR: two SMs share a tile of 256 x 256 (cta_group::2): each holds its own 128 rows of the first operand and half of the
+// second's columns, so that a step brings an SM 32 KB in place of 48 KB for the same products.  The first CTA issues the
+// products of both; a stage's copies complete on its barrier, and its commits arrive in both.  A step whose end has to
+// be cleared completes on each CTA's own barrier first, and counts once both have cleared their part.
+
+template <int KIND, bool DUAL, int BN, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1)
+product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Maps maps)
+{
+    using P = Plan<KIND, DUAL, BN, PAIR>;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ Shared sh;
+    uint8_t *smem = align_smem_1024(smem_raw);
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    const int rank = PAIR ? (int)cluster_ctarank() : 0;
+    const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x, stride = PAIR ? gridDim.x >> 1 : gridDim.x;
+    const int n_tiles = (a.N + P::kOutN - 1) / P::kOutN, k_steps = (a.K + kStep - 1) / kStep;
+
     pdl_trigger();
+    if (threadIdx.x == 0) {
+        prefetch_map(&maps.a[0]);
+        prefetch_map(&maps.w[0]);
+        if (DUAL) prefetch_map(&maps.w[1]);
+        for (int i = 0; i < P::kStages; ++i) {
+            mbar_init(smem_u32(&sh.full[i]), 1);
+            mbar_init(smem_u32(&sh.empty[i]), 1);
+            mbar_init(smem_u32(&sh.tail[i]), 1);
+            mbar_init(smem_u32(&sh.cleared[i]), 2);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&sh.acc_full[i]), 1);
+            mbar_init(smem_u32(&sh.acc_empty[i]), PAIR ? 16 : 8);
+        }
+        mbar_init(smem_u32(&sh.drain), 1);
+        sh.abort = sh.gave_up = 0;
+        sh.bad = 0;
+        sh.row_tiles = KIND == kTN ? a.G * ((a.M + P::kRows - 1) / P::kRows) : (a.R + P::kRows - 1) / P::kRows;
+        fence_mbar_init();
+    }
+    if (warp == 3) {
+        if (PAIR) {
+            tmem_alloc_pair(smem_u32(&sh.tmem), 512);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(&sh.tmem), 512);
+            tmem_relinquish();
+        }
+    }
+    __syncthreads();
+    if (PAIR) cluster_arrive();
     pdl_wait();
-    const int n_tiles = (a.N + kTile - 1) / kTile, mt = blockIdx.x / n_tiles, n0 = (blockIdx.x - mt * n_tiles) * kTile;
-    int g = 0, row0 = mt * kTile, end = a.R;
-    if (a.offsets) {
-        if (!offsets_ok(a.offsets, a.G, a.R, a.status)) return;
-        if (threadIdx.x == 0) {
-            int left = mt;
-            sh[0] = -1;
-            for (int i = 0; i < a.G; ++i) {
-                const int o = a.offsets[i], e = i + 1 < a.G ? a.offsets[i + 1] : a.R, tiles = (e - o + kTile - 1) / kTile;
-                if (left < tiles) {
-                    sh[0] = i;
-                    sh[1] = o + left * kTile;
-                    sh[2] = e;
+    if (a.offsets) build_table<KIND, P::kRows>(a, sh, warp, lane);
+    tc_fence_before();
+    __syncthreads();
+    if (PAIR) cluster_wait();                                         // the barriers of both CTAs are there
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem, 0);
+    const int total = __shfl_sync(0xFFFFFFFFu, sh.row_tiles * n_tiles, 0);
+    volatile int *abort = &sh.abort;
+    const uint32_t smem0 = smem_u32(smem);
+    auto fail = [&]() {
+        record_status(a.status, MOE_ERR_TIMEOUT);
+        *abort = 1;
+    };
+    auto tell_pair = [&]() {
+        for (uint32_t c = 0; c < 2; ++c) st_cluster_u32(mapa_u32(smem_u32(&sh.gave_up), c), 1);
+    };
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xFFFFFFFFu, PAIR ? mbar_wait_cluster(bar, parity, a.wait_limit, abort) : mbar_wait(bar, parity, a.wait_limit, abort));
+    };
+    auto steps_of = [&](const Tile &t) { return KIND == kTN ? (t.terms + kStep - 1) / kStep : a.pairs * k_steps; };
+    // the last step of a sum that ends inside it, before the last of all rows (past which the copies bring zeros)
+    auto to_clear = [&](const Tile &t) { return KIND == kTN && t.terms % kStep != 0 && t.first + t.terms < a.R; };
+
+    // A role's warp walks its loop as a whole and only the issuing instructions are one lane's (scaled_gemm.cu).
+    // registers: 384 x 168 at launch, redistributed by warpgroup to 104 and 2 x 200 (the same total)
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == 0) {
+        // ---- copies, each CTA its own
+        const bool leader = elect_one();
+        int st = 0, issued = 0;
+        uint32_t ph = 0;
+        bool ok = true;
+        for (int tile = first_tile; ok && tile < total; tile += stride) {
+            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
+            const int steps = steps_of(t), row = t.row0 + rank * 128, mine = t.rows - rank * 128;
+            const int boxes = mine > 96 || PAIR ? 4 : (mine + 31) / 32;
+            // the second operand's columns of this CTA, and how many blocks of 64 of them exist
+            const int c0 = t.col0 + rank * P::kHeld, blocks = min(P::kHeld / 64, PAIR ? P::kHeld / 64 : (a.N - c0 + 63) / 64);
+            const bool clear = to_clear(t);
+            for (int ks = 0; ks < steps; ++ks) {
+                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.empty[st]), ph ^ 1, a.wait_limit, abort));
+                if (!ok) {
+                    if (leader) fail();
                     break;
                 }
-                left -= tiles;
-            }
-        }
-        __syncthreads();
-        g = sh[0];
-        if (g < 0) return;
-        row0 = sh[1];
-        end = sh[2];
-    }
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[2][4][4] = {};
-    for (int pair = 0; pair < a.pairs; ++pair) {
-        for (int k0 = 0; k0 < a.K; k0 += kDeep) {
-            for (int i = threadIdx.x; i < kTile * kDeep; i += kThreads) {
-                const int r = i / kDeep, k = i % kDeep;
-                sa[k][r] = row0 + r < end && k0 + k < a.K ? load16(a.a[pair], row0 + r, a.K, k0 + k) : 0.f;
-            }
-            for (int m = 0; m < (a.glu ? 2 : 1); ++m) {
-                const uint16_t *w = a.w[a.glu ? m : pair] + (size_t)g * a.N * a.K;
-                for (int i = threadIdx.x; i < kTile * kDeep; i += kThreads) {
-                    const int n = a.w_kn ? i % kTile : i / kDeep, k = a.w_kn ? i / kTile : i % kDeep;
-                    const bool in = n0 + n < a.N && k0 + k < a.K;
-                    sw[m][k][n] = !in ? 0.f : a.w_kn ? load16(w, k0 + k, a.N, n0 + n) : load16(w, n0 + n, a.K, k0 + k);
+                const uint32_t base = smem0 + st * P::kStageBytes, b = base + P::kABytes;
+                const bool tail = clear && ks == steps - 1;
+                if (leader) {
+                    const uint32_t local = smem_u32(tail ? &sh.tail[st] : &sh.full[st]), bar = PAIR ? mapa_u32(local, tail ? rank : 0) : local;
+                    if (KIND == kTN) {
+                        const int r = t.first + ks * kStep;
+                        if (PAIR) {
+                            if (tail) mbar_arrive_expect_tx(local, P::kStageBytes);
+                            else if (rank == 0) mbar_arrive_expect_tx(local, 2 * P::kStageBytes);
+                            for (int i = 0; i < 2; ++i) tma_load_2d_pair(base + i * kBlockBytes, &maps.a[0], row + 64 * i, r, bar);
+                            for (int i = 0; i < P::kHeld / 64; ++i) tma_load_2d_pair(b + i * kBlockBytes, &maps.w[0], c0 + 64 * i, r, bar);
+                        } else {
+                            const int ablocks = mine > 64 ? 2 : 1;
+                            mbar_arrive_expect_tx(bar, (ablocks + blocks) * kBlockBytes);
+                            for (int i = 0; i < ablocks; ++i) tma_load_2d(base + i * kBlockBytes, &maps.a[0], row + 64 * i, r, bar);
+                            for (int i = 0; i < blocks; ++i) tma_load_2d(b + i * kBlockBytes, &maps.w[0], c0 + 64 * i, r, bar);
+                        }
+                    } else {
+                        const int pair = ks >= k_steps, k = (pair ? ks - k_steps : ks) * kStep;
+                        const int bbytes = KIND == kNN ? blocks * kBlockBytes : P::kBBytes;
+                        if (PAIR) {
+                            if (rank == 0) mbar_arrive_expect_tx(local, 2 * P::kStageBytes);
+                            if (KIND == kNN)
+                                for (int i = 0; i < P::kHeld / 64; ++i) tma_load_3d_pair(b + i * kBlockBytes, &maps.w[pair], c0 + 64 * i, k, t.g, bar);
+                            else
+                                tma_load_2d_pair(b, &maps.w[DUAL ? rank : pair], k, t.g * a.N + (DUAL ? t.col0 : c0), bar);
+                            tma_load_2d_pair(base, &maps.a[pair], k, row, bar);
+                        } else {
+                            mbar_arrive_expect_tx(bar, boxes * 32 * 128 + bbytes);
+                            if (KIND == kNN) {
+                                for (int i = 0; i < blocks; ++i) tma_load_3d(b + i * kBlockBytes, &maps.w[pair], c0 + 64 * i, k, t.g, bar);
+                            } else {
+                                tma_load_2d(b, &maps.w[DUAL ? 0 : pair], k, t.g * a.N + c0, bar);
+                                if (DUAL) tma_load_2d(b + P::kBBytes / 2, &maps.w[1], k, t.g * a.N + c0, bar);
+                            }
+                            if (boxes == 4)
+                                tma_load_2d(base, &maps.a[pair], k, row, bar);
+                            else
+                                for (int i = 0; i < boxes; ++i) tma_load_2d(base + i * 32 * 128, &maps.a32[pair], k, row + 32 * i, bar);
+                        }
+                    }
+                }
+                ++issued;
+                if (++st == P::kStages) {
+                    st = 0;
+                    ph ^= 1;
                 }
             }
-            __syncthreads();
-            for (int k = 0; k < kDeep; ++k)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j) {
-                        acc[0][i][j] = fmaf(sa[k][ty + 16 * i], sw[0][k][tx + 16 * j], acc[0][i][j]);
-                        if (a.glu) acc[1][i][j] = fmaf(sa[k][ty + 16 * i], sw[1][k][tx + 16 * j], acc[1][i][j]);
-                    }
-            __syncthreads();
         }
-    }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int r = row0 + ty + 16 * i, n = n0 + tx + 16 * j;
-            if (r >= end || n >= a.N) continue;
-            const size_t at = (size_t)r * a.N + n;
-            float v[2];
-            for (int m = 0; m < 2; ++m) {
-                v[m] = acc[m][i][j] + (a.bias[m] ? load16(a.bias[m], g, a.N, n) : 0.f);
-                if (a.pre[m]) a.pre[m][at] = float_to_bf16_bits(v[m]);
+        if (PAIR) {
+            if (leader) {
+                st_cluster_u32(mapa_u32(smem_u32(&sh.issued[rank]), 0), issued);
+                if (!ok) tell_pair();
             }
-            float y = act_value(a.act, v[0]);
-            if (a.glu) y *= v[1];
-            if (a.residual) y += bf16_bits_to_float(a.residual[at]);
-            if (a.y_f32) static_cast<float *>(a.y)[at] = y;
-            else static_cast<uint16_t *>(a.y)[at] = float_to_bf16_bits(y);
+        } else {
+            // the newest copy of each stage lands before the CTA leaves, whoever gave up
+            for (int i = 0; i < min(issued, P::kStages); ++i) {
+                if (--st < 0) {
+                    st = P::kStages - 1;
+                    ph ^= 1;
+                }
+                mbar_wait(smem_u32(&sh.full[st]), ph, 1 << 20, nullptr);
+            }
         }
-}
-
-__device__ __forceinline__ void put(void *p, size_t at, int f32, int accumulate, float v)
-{
-    if (f32) static_cast<float *>(p)[at] = accumulate ? static_cast<float *>(p)[at] + v : v;
-    else static_cast<uint16_t *>(p)[at] = float_to_bf16_bits(v);
-}
-
-__global__ void __launch_bounds__(kThreads) wgrad_kernel(const __grid_constant__ WgradArgs a)
-{
-    __shared__ float sd[kDeep][kTile + 1], sx[kDeep][kTile + 1];
-    pdl_trigger();
-    pdl_wait();
-    const int nt = (a.N + kTile - 1) / kTile, kt = (a.K + kTile - 1) / kTile;
-    const int g = blockIdx.x / (nt * kt), n0 = blockIdx.x / kt % nt * kTile, k0 = blockIdx.x % kt * kTile;
-    if (a.offsets && !offsets_ok(a.offsets, a.G, a.R, a.status)) return;
-    const int start = a.offsets ? a.offsets[g] : 0, end = a.offsets && g + 1 < a.G ? a.offsets[g + 1] : a.R;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {}, db = 0.f;
-    for (int r0 = start; r0 < end; r0 += kDeep) {
-        for (int i = threadIdx.x; i < kTile * kDeep; i += kThreads) {
-            const int r = r0 + i / kTile, c = i % kTile;
-            sd[i / kTile][c] = r < end && n0 + c < a.N ? load16(a.dy, r, a.N, n0 + c) : 0.f;
-            sx[i / kTile][c] = r < end && k0 + c < a.K ? load16(a.x, r, a.K, k0 + c) : 0.f;
+    } else if (warp == 1 && rank == 0) {
+        // ---- products
+        const uint32_t leader = elect_one();
+        int st = 0, acc = 0;
+        uint32_t ph = 0, aph = 0, cph = 0;                              // cph: a bit a stage
+        bool ok = true;
+        constexpr uint32_t kId = idesc_bf16<KIND>(P::kRows, BN);
+        for (int tile = first_tile; ok && tile < total; tile += stride) {
+            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
+            const int steps = steps_of(t);
+            const bool clear = to_clear(t);
+            ok = wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1);
+            tc_fence_after();
+            const uint32_t d = tmem + acc * BN;
+            for (int ks = 0; ok && ks < steps; ++ks) {
+                ok = wait(smem_u32(&sh.full[st]), ph);
+                if (PAIR && ok && clear && ks == steps - 1) {
+                    ok = wait(smem_u32(&sh.cleared[st]), cph >> st & 1);
+                    cph ^= 1u << st;
+                }
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t base = smem0 + st * P::kStageBytes;
+                const uint64_t ad = KIND == kTN ? desc_mn(base) : desc_sw128(base);
+                const uint64_t bd = KIND == kNT ? desc_sw128(base + P::kABytes) : desc_mn(base + P::kABytes);
+                // instructions of 16 terms: 32 bytes along K-major rows, 16 rows of MN-major blocks
+                const int left = KIND == kTN ? t.terms - ks * kStep : a.K - (ks >= k_steps ? ks - k_steps : ks) * kStep;
+                const int kk = (left + 15) / 16;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * (KIND == kTN ? 128 : 2), bd + j * (KIND == kNT ? 2 : 128), kId, ks > 0 || j > 0,
+                                           leader & (uint32_t)(j < kk));
+                if (leader) {
+                    if (PAIR) mma_commit_pair(smem_u32(&sh.empty[st]));
+                    else mma_commit(smem_u32(&sh.empty[st]));
+                }
+                if (++st == P::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+            if (!ok) break;
+            if (leader) {
+                if (PAIR) mma_commit_pair(smem_u32(&sh.acc_full[acc]));
+                else mma_commit(smem_u32(&sh.acc_full[acc]));
+            }
+            if (++acc == 2) {
+                acc = 0;
+                aph ^= 1;
+            }
         }
-        __syncthreads();
-        for (int r = 0; r < kDeep; ++r)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sd[r][ty + 16 * i], sx[r][tx + 16 * j], acc[i][j]);
-        if (threadIdx.x < kTile)
-            for (int r = 0; r < kDeep; ++r) db += sd[r][threadIdx.x];
-        __syncthreads();
+        // the products end before the CTA leaves, whoever gave up
+        if (leader) {
+            if (!ok) {
+                fail();
+                if (PAIR) tell_pair();
+            }
+            if (PAIR) mma_commit_pair(smem_u32(&sh.drain));
+            else mma_commit(smem_u32(&sh.drain));
+        }
+        __syncwarp();
+        mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
+    } else if (warp == 2 && KIND == kTN) {
+        // ---- zeros for what the last step of a sum holds of other groups' rows; its copies complete on a barrier of their
+        // own, and the stage's is this warp's to complete
+        int it = 0;
+        uint32_t tph = 0;                                               // a bit a stage
+        for (int tile = first_tile; tile < total; tile += stride) {
+            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
+            it += steps_of(t);
+            if (!to_clear(t)) continue;
+            const int st = (it - 1) % P::kStages;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.tail[st]), tph >> st & 1, a.wait_limit, abort))) {
+                if (lane == 0) {
+                    fail();
+                    if (PAIR) tell_pair();
+                }
+                break;
+            }
+            tph ^= 1u << st;
+            const int lo = t.terms % kStep, n = ((lo + 15) & ~15) - lo;               // rows up to the end of an instruction
+            uint8_t *const base = smem + st * P::kStageBytes;
+            for (int i = lane; i < (2 + P::kHeld / 64) * n * 8; i += 32) {
+                const int block = i / (n * 8), rest = i - block * n * 8;
+                *reinterpret_cast<uint4 *>(base + block * kBlockBytes + (lo + rest / 8) * 128 + rest % 8 * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(mapa_u32(smem_u32(&sh.cleared[st]), 0));
+                if (rank == 0) mbar_arrive(smem_u32(&sh.full[st]));
+            }
+        }
+    } else if (warp >= 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        // ---- accumulators to outputs: two warps share a quarter of the rows, each with half of the output columns
+        constexpr int kCols = P::kOutN / 2;
+        const int quad = warp & 3, half = (warp - 4) >> 2;
+        int acc = 0;
+        uint32_t aph = 0;
+        for (int tile = first_tile; tile < total; tile += stride) {
+            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
+            const int r0 = rank * 128 + quad * 32, col0 = t.col0 + half * kCols;
+            const uint32_t d = tmem + acc * BN + half * kCols + ((uint32_t)(quad * 32) << 16);
+            if (!wait(smem_u32(&sh.acc_full[acc]), aph)) {
+                if (lane == 0) fail();
+                break;
+            }
+            tc_fence_after();
+            const uint32_t empty = smem_u32(&sh.acc_empty[acc]);
+            auto release = [&]() {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster(mapa_u32(empty, 0));
+                    else mbar_arrive(empty);
+                }
+            };
+            if (r0 < t.rows && col0 < a.N)
+                finish<KIND, DUAL, kCols>(a, d, d + BN / 2, t.g, (size_t)(KIND == kTN ? (size_t)t.g * a.M : 0) + t.row0 + r0, t.rows - r0, col0,
+                                          KIND == kTN && t.terms == 0, lane, smem + P::kOutAt + (warp - 4) * (P::kOutBytes / 8), release);
+            else
+                release();
+            if (++acc == 2) {
+                acc = 0;
+                aph ^= 1;
+            }
+        }
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int n = n0 + ty + 16 * i, k = k0 + tx + 16 * j;
-            if (n < a.N && k < a.K) put(a.dw, ((size_t)g * a.N + n) * a.K + k, a.f32, a.accumulate, acc[i][j]);
+    __syncthreads();
+    if (PAIR) {
+        cluster_sync();                                               // nothing of the pair is issued any more
+        // commits arrive in both CTAs: the last of them, of all products, is there before the second one's shared memory goes
+        if (rank == 1 && warp == 1) mbar_wait(smem_u32(&sh.drain), 0, 1 << 20, nullptr);
+        if (sh.gave_up) {
+            // Where nobody gave up, the products have waited for every copy of both CTAs.  Else the newest copy of each stage
+            // may still be on its way, of either CTA: neither is more than the stages ahead of the other.  A stage that not
+            // both asked for does not complete, and its wait runs out long after its copies have landed.
+            if (rank == 0 && warp == 0) {
+                const int n = max(sh.issued[0], sh.issued[1]), i = n - 1 - lane;
+                if (lane < min(n, P::kStages)) mbar_wait(smem_u32(&sh.full[i % P::kStages]), i / P::kStages & 1, 1 << 20, nullptr);
+            }
+            __syncthreads();
+            cluster_sync();
         }
-    if (a.db && k0 == 0 && threadIdx.x < kTile && n0 + (int)threadIdx.x < a.N)
-        put(a.db, (size_t)g * a.N + n0 + threadIdx.x, a.f32, a.accumulate, db);
+    }
+    if (warp == 3) {
+        if (PAIR) tmem_dealloc_pair(tmem, 512);
+        else tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int KIND, bool DUAL, int BN, bool PAIR>
+cudaError_t launch_plan(const ProductArgs &a, const Maps &maps, int ctas, cudaStream_t st)
+{
+    using P = Plan<KIND, DUAL, BN, PAIR>;
+    auto k = product_kernel<KIND, DUAL, BN, PAIR>;
+    static_assert(P::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = set_shared(k, P::kSmem, ready);
+    if (e != cudaSuccess) return e;
+    return launch_dependent_clusters(k, ctas, PAIR ? 2 : 1, kThreads, P::kSmem, st, a, maps);
+}
+
+bool map_2d(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows, uint32_t box_rows)
+{
+    return make_map_2d(m, p, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, cols, rows, kStep, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+}
+
+// ------------------------------------------------------------------ column sums
+
+// db_g (+)= sum over the group's rows of dy: a cluster of C CTAs has 256 columns of one group, each a part of its rows; a warp
+// reads 8 columns a lane of every 8th row.  The parts meet in the first CTA in a fixed order.
+struct BiasArgs {
+    const uint16_t *dy;
+    const int32_t *offsets;
+    void *db;
+    int *status;
+    int R, N, G, f32, accumulate, parts;
+};
+
+__global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__ BiasArgs a)
+{
+    __shared__ float part[8][256 + 8];
+    __shared__ float total[8][256];                        // of each CTA of the cluster, in the first
+    pdl_trigger();
+    if (a.parts > 1) cluster_arrive();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = a.parts > 1 ? (int)cluster_ctarank() : 0;
+    const int blocks = (a.N + 255) / 256, cluster = blockIdx.x / a.parts, g = cluster / blocks, n0 = (cluster - g * blocks) * 256;
+    bool bad = false;
+    int lo = 0, hi = a.R;
+    if (a.offsets) {
+        int b = 0;
+        for (int i = threadIdx.x; i < a.G; i += 256) {
+            const int o = a.offsets[i], next = i + 1 < a.G ? a.offsets[i + 1] : a.R;
+            b |= o < 0 || o > a.R || next < o;
+        }
+        bad = __syncthreads_or(b);
+        lo = a.offsets[g];
+        hi = g + 1 < a.G ? a.offsets[g + 1] : a.R;
+    }
+    const int col = n0 + 8 * lane;
+    float acc[8] = {};
+    if (!bad && col < a.N) {
+        const int stride = 8 * a.parts;
+        for (int r = lo + rank * 8 + warp; r < hi; r += 4 * stride) {
+            uint4 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (r + i * stride < hi) v[i] = *reinterpret_cast<const uint4 *>(a.dy + (size_t)(r + i * stride) * a.N + col);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    acc[2 * e] += bf16_lo(w[e]);
+                    acc[2 * e + 1] += bf16_hi(w[e]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) part[warp][8 * lane + e] = acc[e];
+    __syncthreads();
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
+    if (a.parts > 1) {
+        cluster_wait();                                    // the first CTA is there
+        st_cluster_u32(mapa_u32(smem_u32(&total[rank][threadIdx.x]), 0), __float_as_uint(s));
+        cluster_sync();
+        if (rank) return;
+        s = 0.f;
+        for (int i = 0; i < a.parts; ++i) s += total[i][threadIdx.x];
+    }
+    const int c = n0 + threadIdx.x;
+    if (bad || c >= a.N) return;
+    const size_t at = (size_t)g * a.N + c;
+    if (a.f32) {
+        float *p = static_cast<float *>(a.db) + at;
+        *p = a.accumulate ? *p + s : s;
+    } else {
+        static_cast<uint16_t *>(a.db)[at] = float_to_bf16_bits(s);
+    }
+}
+
+template <int KIND, bool DUAL>
+cudaError_t launch_rows_product(const GemmArgs &g, cudaStream_t st)
+{
+    ProductArgs a{};
+    a.offsets = g.offsets;
+    for (int i = 0; i < 2; ++i) {
+        a.bias[i] = g.bias[i];
+        a.pre[i] = g.pre[i];
+    }
+    a.residual = g.residual;
+    a.y = g.y;
+    a.status = g.status;
+    a.R = g.R;
+    a.N = g.N;
+    a.K = g.K;
+    a.G = g.G;
+    a.pairs = g.pairs;
+    a.act = g.act;
+    a.y_f32 = g.y_f32;
+    a.wait_limit = g.wait_limit;
+    const int sms = device_sm_count();
+    auto row_tiles = [&](int rows) -> long long {          // at most: every group's last one may be partial
+        return a.offsets ? a.R / rows + (a.G < a.R ? a.G : a.R) : (a.R + rows - 1) / rows;
+    };
+    auto tiles = [&](int out_n) { return row_tiles(128) * ((a.N + out_n - 1) / out_n); };
+    const long long pairs = (a.R / 256) * (long long)((a.N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256));
+    const bool pair = a.R / a.G >= 256 && pairs >= sms / 2;
+    int bn = 256;
+    if (!pair) {
+        if (tiles(DUAL ? 64 : 128) <= sms) bn = 128;
+        if (!DUAL && tiles(64) <= sms) bn = 64;
+    }
+    Maps maps{};
+    bool ok = true;
+    for (int i = 0; i < g.pairs; ++i) {
+        ok = ok && map_2d(&maps.a32[i], g.a[i], a.K, a.R, 32);
+        maps.a[i] = maps.a32[i];
+        if (a.R > 96) ok = ok && map_2d(&maps.a[i], g.a[i], a.K, a.R, 128);
+    }
+    for (int i = 0; i < (DUAL ? 2 : g.pairs); ++i) {
+        if (KIND == kNN) {
+            const uint64_t dims[3] = {(uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.G}, strides[2] = {(uint64_t)a.N * 2, (uint64_t)a.N * a.K * 2};
+            const uint32_t box[3] = {64, 64, 1};
+            ok = ok && make_map_3d(&maps.w[i], g.w[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+        } else {
+            ok = ok && map_2d(&maps.w[i], g.w[i], a.K, (uint64_t)a.G * a.N, pair ? 128 : DUAL ? bn / 2 : bn);
+        }
+    }
+    if (!ok) return cudaErrorInvalidValue;
+    if (pair) return launch_plan<KIND, DUAL, 256, true>(a, maps, sms / 2 * 2, st);
+    const long long n = tiles(DUAL ? bn / 2 : bn);
+    const int ctas = (int)(n < sms ? n : sms);
+    if (bn == 256) return launch_plan<KIND, DUAL, 256, false>(a, maps, ctas, st);
+    if (bn == 128) return launch_plan<KIND, DUAL, 128, false>(a, maps, ctas, st);
+    if constexpr (!DUAL) return launch_plan<KIND, DUAL, 64, false>(a, maps, ctas, st);
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t launch_gemm(const GemmArgs &a, cudaStream_t st)
+cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t st)
 {
-    const long long mt = a.offsets ? a.R / kTile + (a.G < a.R ? a.G : a.R) : (a.R + kTile - 1) / kTile;
-    const long long tiles = mt * ((a.N + kTile - 1) / kTile);
-    return launch_dependent(gemm_kernel, (unsigned)tiles, kThreads, 0, st, a);
+    if (g.glu) return launch_rows_product<kNT, true>(g, st);
+    return g.w_kn ? launch_rows_product<kNN, false>(g, st) : launch_rows_product<kNT, false>(g, st);
 }
 
-cudaError_t launch_wgrad(const WgradArgs &a, cudaStream_t st)
+cudaError_t launch_wgrad(const WgradArgs &g, cudaStream_t st)
 {
-    const long long tiles = (long long)a.G * ((a.N + kTile - 1) / kTile) * ((a.K + kTile - 1) / kTile);
-    return launch_dependent(wgrad_kernel, (unsigned)tiles, kThreads, 0, st, a);
+    ProductArgs a{};
+    a.offsets = g.offsets;
+    a.y = g.dw;
+    a.status = g.status;
+    a.R = g.R;
+    a.M = g.N;
+    a.N = g.K;
+    a.G = g.G;
+    a.y_f32 = g.f32;
+    a.accumulate = g.accumulate;
+    a.wait_limit = g.wait_limit;
+    const int sms = device_sm_count();
+    auto tiles = [&](int rows, int cols) { return (long long)a.G * ((a.M + rows - 1) / rows) * ((a.N + cols - 1) / cols); };
+    const bool pair = a.R / a.G >= 256 && tiles(256, 256) >= sms / 2;
+    int bn = 256;
+    if (!pair) {
+        if (tiles(128, 128) <= sms) bn = 128;
+        if (tiles(128, 64) <= sms) bn = 64;
+    }
+    Maps maps{};
+    if (!map_2d(&maps.a[0], g.dy, a.M, a.R, 64) || !map_2d(&maps.w[0], g.x, a.N, a.R, 64)) return cudaErrorInvalidValue;
+    const long long n = tiles(128, bn);
+    const int ctas = (int)(n < sms ? n : sms);
+    const cudaError_t e = pair        ? launch_plan<kTN, false, 256, true>(a, maps, sms / 2 * 2, st)
+                          : bn == 256 ? launch_plan<kTN, false, 256, false>(a, maps, ctas, st)
+                          : bn == 128 ? launch_plan<kTN, false, 128, false>(a, maps, ctas, st)
+                                      : launch_plan<kTN, false, 64, false>(a, maps, ctas, st);
+    if (e != cudaSuccess || !g.db) return e;
+    const long long blocks = (long long)g.G * ((g.N + 255) / 256);
+    const int parts = blocks * 8 <= 2 * sms && g.R / g.G >= 256 ? 8 : 1;
+    const BiasArgs b{g.dy, g.offsets, g.db, g.status, g.R, g.N, g.G, g.f32, g.accumulate, parts};
+    return launch_dependent_clusters(column_sum_kernel, (unsigned)(blocks * parts), parts, 256, 0, st, b);
 }
 
 }  // namespace qmoe

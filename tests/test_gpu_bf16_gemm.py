@@ -36,6 +36,8 @@ SIZES = [
     ([64], 512, 256), ([129], 136, 328), ([301], 1000, 2184), ([700], 520, 136), ([1500], 768, 192),
     ([0, 3, 0, 130, 1, 0], 200, 136), ([1, 1, 1, 1], 512, 2048), ([40, 0, 0, 257], 72, 64), ([0, 0, 5], 8, 1032),
     ([128, 128, 64], 256, 320), ([300, 500, 1, 700], 512, 264),
+    # pairs of CTAs: row tiles of 256, whole and partial
+    ([2660], 2056, 136), ([2560], 2048, 320), ([300, 1, 0, 1300, 257, 900], 1912, 72), ([20000], 264, 72),
 ]
 
 
@@ -93,7 +95,8 @@ def test_epilogue(ws, counts, N, K, name):
 
 
 @pytest.mark.parametrize("transposed", [0, 1])
-@pytest.mark.parametrize("counts,N,K", [([1], 512, 264), ([150], 264, 72), ([60, 0, 200, 1], 128, 136), ([600], 768, 512)])
+@pytest.mark.parametrize("counts,N,K", [([1], 512, 264), ([150], 264, 72), ([60, 0, 200, 1], 128, 136), ([600], 768, 512),
+                                        ([2700], 2048, 72), ([900, 1900], 2048, 136)])
 def test_two_pairs(ws, counts, N, K, transposed):
     """The sum of two products, rounded once."""
     a, w, offsets, R, want, s = case(counts, N, K, bool(transposed), pairs=2, seed=5)
@@ -104,7 +107,8 @@ def test_two_pairs(ws, counts, N, K, transposed):
 
 @pytest.mark.parametrize("name,biased", [("silu", False), ("gelu", True), ("none", True), ("relu", False)])
 @pytest.mark.parametrize("counts,I,K", [([1], 512, 2048), ([4], 264, 136), ([200], 136, 72), ([0, 3, 0, 130, 1, 0], 200, 136),
-                                        ([1] * 9, 512, 512), ([300, 280], 264, 520)])
+                                        ([1] * 9, 512, 512), ([300, 280], 264, 520),
+                                        ([2570], 1032, 72), ([1000, 0, 5, 1600], 1040, 136)])
 def test_gated_pair(ws, counts, I, K, name, biased):
     offsets, R = offsets_of(counts)
     G = len(counts)
@@ -135,7 +139,9 @@ def test_gated_pair(ws, counts, I, K, name, biased):
 
 
 WSIZES = [([1], 8, 8), ([1], 264, 72), ([15], 64, 64), ([64], 128, 256), ([100], 136, 328), ([700], 520, 264), ([0, 3, 0, 130, 1, 0], 200, 136),
-          ([17, 16, 1, 64, 65, 128], 256, 512), ([300, 0, 500], 72, 1032), ([2] * 40, 64, 136), ([2000], 384, 256)]
+          ([17, 16, 1, 64, 65, 128], 256, 512), ([300, 0, 500], 72, 1032), ([2] * 40, 64, 136), ([2000], 384, 256),
+          # pairs of CTAs
+          ([300], 2048, 2560), ([320], 2056, 2632), ([256, 0, 777, 1, 600], 1000, 1288), ([15 * 64 + 9, 300, 15 * 64], 1288, 1544)]
 
 
 @pytest.mark.parametrize("counts,N,K", WSIZES)
@@ -178,10 +184,11 @@ def test_weight_gradient_without_rows(ws):
     assert bool((y == MARK).all())
 
 
-@pytest.mark.parametrize("counts", [[3, 4], [100, 300], [0, 600]])
-def test_rows_of_no_group(ws, counts):
+@pytest.mark.parametrize("counts,N,K", [([3, 4], 136, 72), ([100, 300], 136, 72), ([0, 600], 136, 72), ([1000, 1700], 2056, 72),
+                                        ([300, 700], 2056, 1288)])
+def test_rows_of_no_group(ws, counts, N, K):
     """Rows before the first group: not written, and what they hold (NaN) reaches nothing."""
-    N, K, first = 136, 72, 5
+    first = 5
     offsets, R = offsets_of(counts, first=first)
     a, w = bf16(R, K, seed=1), bf16(2, N, K, seed=2, size=K ** -0.5)
     a[:first] = float("nan")
@@ -199,11 +206,11 @@ def test_rows_of_no_group(ws, counts):
 
 
 @pytest.mark.parametrize("transposed", [0, 1])
-@pytest.mark.parametrize("counts", [[1, 2, 1], [70, 30, 90], [260, 300, 10]])
+@pytest.mark.parametrize("counts,N,K", [([1, 2, 1], 136, 72), ([70, 30, 90], 136, 72), ([260, 300, 10], 136, 72),
+                                        ([1290, 1300, 300], 2056, 72), ([700, 300, 99], 1288, 1288)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf")])
-def test_non_finite_values_stay_apart(ws, counts, transposed, bad):
+def test_non_finite_values_stay_apart(ws, counts, N, K, transposed, bad):
     """A group whose rows and matrix hold no finite value next to groups that do: tiles, panels and steps end inside one."""
-    N, K = 136, 72
     offsets, R = offsets_of(counts)
     a, w = bf16(R, K, seed=1), bf16(3, *((K, N) if transposed else (N, K)), seed=2, size=K ** -0.5)
     rows = list(groups(counts))
@@ -228,10 +235,9 @@ def test_non_finite_values_stay_apart(ws, counts, transposed, bad):
 
 
 @pytest.mark.parametrize("bad_offsets", [[0, 9, 4], [0, 4, 99], [-1, 3, 4], [1 << 30, 2, 3]])
-@pytest.mark.parametrize("R", [6, 700])
-def test_malformed_offsets_are_reported(bad_offsets, R):
+@pytest.mark.parametrize("R,N,K", [(6, 72, 64), (700, 72, 64), (2600, 2048, 1536)])
+def test_malformed_offsets_are_reported(bad_offsets, R, N, K):
     w = torch.zeros(512, dtype=torch.uint8, device="cuda")
-    N, K = 72, 64
     bad_offsets = [o if o != 9 else R - 1 for o in bad_offsets] if R > 10 else bad_offsets
     bad_offsets = [o if o != 99 else R + 1 for o in bad_offsets]
     offsets = torch.tensor(bad_offsets, dtype=torch.int32, device="cuda")
