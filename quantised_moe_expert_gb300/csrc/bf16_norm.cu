@@ -11,10 +11,13 @@
 //   e = scale f(gate) D,  dx = rx (e w' - x^ mean(e w' x^))       (dx = e without post_norm)
 //   dpre_weight = sum_t dy s^,  dpost_weight = sum_t e x^
 //
-// A thread keeps 8 consecutive elements of a row in registers from the one read to the write; sums over the row go through
-// shuffles and shared memory.  Backward, a block walks over every gridDim-th row with the sums over rows of its threads'
-// columns in registers, writes them as one row of the workspace, and a second launch adds those up in a fixed order.
+// Bound: bytes.  A thread keeps CH segments of 8 elements of a row in registers from the one read to the write; sums over
+// the row go through shuffles and shared memory.  Backward, a block walks over every gridDim-th row: the next row's
+// elements are on their way under this one's sums, which meet in two rounds (everything that needs only the inputs, then what
+// needs D); the sums over rows of a thread's columns stay in registers, are written as one row of the workspace, and a
+// second launch adds those up in a fixed order.
 #include "bf16.cuh"
+#include "f32x2.cuh"
 #include "tc_ptx.cuh"
 
 namespace qmoe {
@@ -23,200 +26,337 @@ namespace {
 using tc::pdl_trigger;
 using tc::pdl_wait;
 
-constexpr int kMaxThreads = kNormMaxN / 8;
+__device__ __forceinline__ uint4 load8(const uint16_t *p, size_t seg) { return reinterpret_cast<const uint4 *>(p)[seg]; }
+__device__ __forceinline__ uint4 load8_once(const uint16_t *p, size_t seg) { return __ldcs(reinterpret_cast<const uint4 *>(p) + seg); }
+__device__ __forceinline__ uint4 zero4() { return make_uint4(0, 0, 0, 0); }
 
-__device__ __forceinline__ void unpack(uint4 u, float (&v)[8])
+// offset + weight, or ones, of a segment.
+__device__ __forceinline__ void weights(const uint16_t *w, uint4 raw, F2 offset, F2 (&v)[4])
 {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if (!w) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = f2(1.f, 1.f);
+        return;
+    }
+    unpack8(raw, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = add2(v[i], offset);
+}
+__device__ __forceinline__ float sum2(F2 v)
+{
+    const float2 p = unf2(v);
+    return p.x + p.y;
+}
+// f of a segment's gate values.
+__device__ __forceinline__ void gate_values(int act, uint4 raw, F2 (&f)[4])
+{
+    unpack8(raw, f);
+    if (act == MOE_ACT_NONE) return;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(w[i]);
-        v[2 * i + 1] = bf16_hi(w[i]);
+        const float2 g = unf2(f[i]);
+        const float s0 = sigmoid(g.x), s1 = sigmoid(g.y);
+        f[i] = act == MOE_ACT_SILU ? f2(g.x * s0, g.y * s1) : f2(s0, s1);
     }
 }
-__device__ __forceinline__ uint4 pack(const float (&v)[8])
-{
-    return make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-}
-__device__ __forceinline__ uint4 load8(const uint16_t *p, size_t seg) { return reinterpret_cast<const uint4 *>(p)[seg]; }
 
-// Sum of v over the block (blockDim a multiple of 32); buf: 32 floats that no thread still reads.
-__device__ __forceinline__ float block_sum(float v, float *buf)
+// Sums of N values over the TPR threads of a row; buf: a float4 a warp that no thread still reads.  Every thread of the
+// block takes part.  Four values share their first two exchanges (each lane goes on with one of them): 6 shuffles in place of 20.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float4 *buf)
 {
+    static_assert(N <= 4, "a float4 a warp");
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, w0 = w / (TPR / 32) * (TPR / 32);
+    if (N > 1) {
+        const float v2 = N > 2 ? v[N > 2 ? 2 : 0] : 0.f, v3 = N > 3 ? v[N > 3 ? 3 : 0] : 0.f;
+        const bool odd = lane & 1, high = lane & 2;
+        float p = odd ? v[1] : v[0], q = odd ? v3 : v2;                          // values 0 and 2, or 1 and 3
+        p += __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[1], 1);
+        if (N > 2) q += __shfl_xor_sync(0xFFFFFFFFu, odd ? v2 : v3, 1);
+        float r = N > 2 && high ? q : p;
+        r += __shfl_xor_sync(0xFFFFFFFFu, N > 2 ? (high ? p : q) : p, 2);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    const int warps = blockDim.x >> 5;
-    if (warps == 1) return v;
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
+        for (int o = 4; o < 32; o <<= 1) r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
+        if (TPR == 32) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, r, i);
+            return;
+        }
+        if (lane < 4) reinterpret_cast<float *>(buf + w)[lane] = r;
+    } else {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) v[0] += __shfl_xor_sync(0xFFFFFFFFu, v[0], o);
+        if (TPR == 32) return;
+        if (lane == 0) buf[w].x = v[0];
+    }
     __syncthreads();
-    float s = 0.f;
-    for (int i = 0; i < warps; ++i) s += buf[i];
-    return s;
-}
-
-// offset + weight of this thread's elements, or ones.
-__device__ __forceinline__ void weights(const uint16_t *w, float offset, int seg, bool on, float (&v)[8])
-{
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 1.0f;
-    if (!w || !on) return;
-    unpack(load8(w, seg), v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += offset;
-}
-
-__global__ void __launch_bounds__(kMaxThreads) gated_norm_kernel(const __grid_constant__ GatedNormArgs a)
-{
-    __shared__ float buf[2][32];
-    pdl_trigger();
-    pdl_wait();
-    const int nseg = a.n / 8, seg = threadIdx.x, t = blockIdx.x;
-    const bool on = seg < nseg;
-    const size_t at = (size_t)t * nseg + seg;
-    float x[8] = {}, r[8] = {}, g[8], w[8];
-    if (on) unpack(load8(a.x, at), x);
-    if (on && a.residual) unpack(load8(a.residual, at), r);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) g[e] = a.scale;
-    if (on && a.gate_shape != MOE_GATE_NONE) {
-        if (a.gate_shape == MOE_GATE_ROW) {
-            const float f = act_value(a.act, bf16_bits_to_float(a.gate[t]));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = f * a.scale;
+    F2 lo = f2(0.f, 0.f), hi = lo;
+    float one = 0.f;
+#pragma unroll 8
+    for (int j = 0; j < TPR / 32; ++j) {
+        if (N == 1) {
+            one += buf[w0 + j].x;
+        } else if (N == 2) {
+            const float2 p = *reinterpret_cast<const float2 *>(buf + w0 + j);
+            lo = add2(lo, f2(p.x, p.y));
         } else {
-            unpack(load8(a.gate, a.gate_shape == MOE_GATE_FULL ? at : seg), g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = act_value(a.act, g[e]) * a.scale;
+            const float4 p = buf[w0 + j];
+            lo = add2(lo, f2(p.x, p.y));
+            hi = add2(hi, f2(p.z, p.w));
         }
     }
-    if (a.post_norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-        const float rx = rsqrtf(block_sum(ss, buf[0]) / (float)a.n + a.eps);
-        weights(a.post_weight, a.weight_offset, seg, on, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * rx * w[e];
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = fmaf(g[e], x[e], r[e]);
-    const uint4 s = pack(r);
-    if (on && a.sum) reinterpret_cast<uint4 *>(a.sum)[at] = s;
-    if (!a.y) return;
-    unpack(s, r);
-    float ss = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(r[e], r[e], ss);
-    const float rs = rsqrtf(block_sum(on ? ss : 0.f, buf[1]) / (float)a.n + a.eps);
-    weights(a.pre_weight, a.weight_offset, seg, on, w);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) r[e] = r[e] * rs * w[e];
-    if (on) reinterpret_cast<uint4 *>(a.y)[at] = pack(r);
+    const float2 l = unf2(lo), h = unf2(hi);
+    v[0] = N == 1 ? one : l.x;
+    if (N > 1) v[N > 1 ? 1 : 0] = l.y;
+    if (N > 2) v[N > 2 ? 2 : 0] = h.x;
+    if (N > 3) v[N > 3 ? 3 : 0] = h.y;
 }
 
-__global__ void __launch_bounds__(kMaxThreads) gated_norm_grad_kernel(const __grid_constant__ GatedNormArgs a)
+constexpr int block_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+template <int TPR, int CH>
+__global__ void __launch_bounds__(block_of(TPR)) gated_norm_kernel(const __grid_constant__ GatedNormArgs a)
 {
-    __shared__ float buf[5][32];
+    constexpr int kRows = block_of(TPR) / TPR;
+    __shared__ float4 buf[2][block_of(TPR) / 32];
+    pdl_trigger();
+    pdl_wait();
+    const int nseg = a.n / 8, tr = threadIdx.x % TPR, t = blockIdx.x * kRows + threadIdx.x / TPR;
+    const bool live = t < a.T;
+    const size_t row = (size_t)t * nseg;
+    uint4 rx[CH], rr[CH], rg[CH], w0[CH], w1[CH];
+    const float row_gate = live && a.gate_shape == MOE_GATE_ROW ? bf16_bits_to_float(a.gate[t]) : 0.f;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int seg = c * TPR + tr;
+        const bool on = live && seg < nseg;
+        rx[c] = on ? load8_once(a.x, row + seg) : zero4();
+        rr[c] = on && a.residual ? load8_once(a.residual, row + seg) : zero4();
+        rg[c] = on && a.gate_shape == MOE_GATE_FULL      ? load8_once(a.gate, row + seg)
+                : on && a.gate_shape == MOE_GATE_CHANNEL ? load8(a.gate, seg)
+                                                         : zero4();
+        w0[c] = on && a.post_weight ? load8(a.post_weight, seg) : zero4();
+        w1[c] = on && a.y && a.pre_weight ? load8(a.pre_weight, seg) : zero4();
+    }
+    F2 x[CH][4];
+#pragma unroll
+    for (int c = 0; c < CH; ++c) unpack8(rx[c], x[c]);
+    float rstd = 1.f;
+    if (a.post_norm) {
+        F2 ss = f2(0.f, 0.f);
+#pragma unroll
+        for (int c = 0; c < CH; ++c)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ss = fma2(x[c][i], x[c][i], ss);
+        float v[1] = {sum2(ss)};
+        row_sums<TPR>(v, buf[0]);
+        rstd = rsqrtf(v[0] / (float)a.n + a.eps);
+    }
+    float each = a.scale * rstd;
+    if (a.gate_shape == MOE_GATE_ROW) each *= act_value(a.act, row_gate);
+    const F2 each2 = f2(each, each), off2 = f2(a.weight_offset, a.weight_offset);
+    F2 ss = f2(0.f, 0.f);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int seg = c * TPR + tr;
+        F2 r[4], w[4], g[4];
+        unpack8(rr[c], r);
+        weights(a.post_weight, w0[c], off2, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[c][i] = mul2(mul2(x[c][i], each2), w[i]);
+        if (a.gate_shape >= MOE_GATE_CHANNEL) {
+            gate_values(a.act, rg[c], g);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[c][i] = fma2(g[i], x[c][i], r[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[c][i] = add2(x[c][i], r[i]);
+        }
+        const uint4 s = pack8(x[c]);
+        if (live && seg < nseg && a.sum) reinterpret_cast<uint4 *>(a.sum)[row + seg] = s;
+        unpack8(s, x[c]);
+        if (seg < nseg) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ss = fma2(x[c][i], x[c][i], ss);
+        }
+    }
+    if (!a.y) return;
+    float v[1] = {sum2(ss)};
+    row_sums<TPR>(v, buf[1]);
+    rstd = rsqrtf(v[0] / (float)a.n + a.eps);
+    const F2 r2 = f2(rstd, rstd);
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+        const int seg = c * TPR + tr;
+        F2 w[4];
+        weights(a.pre_weight, w1[c], off2, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[c][i] = mul2(mul2(x[c][i], r2), w[i]);
+        if (live && seg < nseg) reinterpret_cast<uint4 *>(a.y)[row + seg] = pack8(x[c]);
+    }
+}
+
+// A row's inputs as they were read.
+struct RawRow {
+    uint4 x, s, dy, ds, gate;
+    float row_gate;
+};
+__device__ __forceinline__ RawRow load_row(const GatedNormArgs &a, int t, int nseg, int seg, bool on)
+{
+    RawRow r{zero4(), zero4(), zero4(), zero4(), zero4(), 0.f};
+    if (t >= a.T) return r;
+    if (a.gate_shape == MOE_GATE_ROW) r.row_gate = bf16_bits_to_float(a.gate[t]);
+    if (!on) return r;
+    const size_t at = (size_t)t * nseg + seg;
+    r.x = load8_once(a.x, at);
+    r.s = load8_once(a.sum, at);
+    if (a.dy) r.dy = load8_once(a.dy, at);
+    if (a.dsum) r.ds = load8_once(a.dsum, at);
+    if (a.gate_shape == MOE_GATE_FULL) r.gate = load8_once(a.gate, at);
+    if (a.gate_shape == MOE_GATE_CHANNEL) r.gate = load8(a.gate, seg);
+    return r;
+}
+__device__ __forceinline__ uint32_t word(const uint4 &u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
+__device__ __forceinline__ F2 pair_of(const uint4 &u, int i) { return f2(bf16_lo(word(u, i)), bf16_hi(word(u, i))); }
+__device__ __forceinline__ F2 weight_of(const uint16_t *w, const uint4 &raw, int i, F2 offset)
+{
+    return w ? add2(pair_of(raw, i), offset) : f2(1.f, 1.f);
+}
+__device__ __forceinline__ uint32_t pack_pair(F2 v)
+{
+    const float2 p = unf2(v);
+    return pack_bf16(p.x, p.y);
+}
+template <int ACT>
+__device__ __forceinline__ void gate_pair(F2 raw, F2 &f, F2 &slope)
+{
+    f = raw;
+    slope = f2(1.f, 1.f);
+    if (ACT == MOE_ACT_NONE) return;
+    const float2 g = unf2(raw);
+    const F2 s = f2(sigmoid(g.x), sigmoid(g.y)), minus = f2(-1.f, -1.f);
+    if (ACT == MOE_ACT_SILU) {
+        f = mul2(raw, s);
+        slope = fma2(f, fma2(s, minus, f2(1.f, 1.f)), s);       // s + g s (1 - s)
+    } else {
+        f = s;
+        slope = fma2(mul2(s, minus), s, s);
+    }
+}
+
+// AHEAD: the next row's elements are asked for before this row's are used (where registers last: rows are kept as they were
+// read and widened in each round, and the sums over rows lie in shared memory, each thread's own).
+template <int TPR, int BLOCKS, bool AHEAD, bool BY_ELEMENT, int ACT>
+__global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __grid_constant__ GatedNormArgs a)
+{
+    extern __shared__ float4 sums[];                           // [post, pre, gate][half of a segment][thread]
+    __shared__ float4 buf[2][2][TPR / 32];                     // [row's parity][round]
     pdl_trigger();
     pdl_wait();
     const int nseg = a.n / 8, seg = threadIdx.x;
     const bool on = seg < nseg;
-    float post[8], pre[8], gate[8], slope[8];
-    weights(a.post_weight, a.weight_offset, seg, on, post);
-    weights(a.pre_weight, a.weight_offset, seg, on, pre);
+    const bool want_post = a.dpost_weight != nullptr, want_pre = a.dpre_weight != nullptr;
+    const bool want_gate = BY_ELEMENT && a.dgate && a.gate_shape == MOE_GATE_CHANNEL;
+    const bool full = BY_ELEMENT && a.dgate && a.gate_shape == MOE_GATE_FULL;
+    const F2 off2 = f2(a.weight_offset, a.weight_offset), scale2 = f2(a.scale, a.scale);
+    const float inv_n = 1.0f / (float)a.n;
+    const uint4 post = on && a.post_weight ? load8(a.post_weight, seg) : zero4(), pre = on && a.pre_weight ? load8(a.pre_weight, seg) : zero4();
+    float4 *const mine = sums + threadIdx.x;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) gate[e] = 1.f, slope[e] = 0.f;
-    if (on && a.gate_shape == MOE_GATE_CHANNEL) {
-        unpack(load8(a.gate, seg), gate);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 f = act_slope(a.act, gate[e]);
-            gate[e] = f.x;
-            slope[e] = f.y;
-        }
-    }
-    float sum_pre[8] = {}, sum_post[8] = {}, sum_gate[8] = {};
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x) {
+    for (int i = 0; i < 6; ++i) mine[i * TPR] = make_float4(0.f, 0.f, 0.f, 0.f);
+    RawRow next;
+    if (AHEAD) next = load_row(a, blockIdx.x, nseg, seg, on);
+    int parity = 0;
+    for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 1) {
+        const RawRow raw = AHEAD ? next : load_row(a, t, nseg, seg, on);
+        if (AHEAD) next = load_row(a, t + gridDim.x, nseg, seg, on);
         const size_t at = (size_t)t * nseg + seg;
-        float x[8] = {}, s[8] = {}, dy[8] = {}, d[8] = {};
-        if (on) unpack(load8(a.x, at), x);
-        if (on) unpack(load8(a.sum, at), s);
-        if (on && a.dy) unpack(load8(a.dy, at), dy);
-        if (on && a.dsum) unpack(load8(a.dsum, at), d);
-        if (a.gate_shape == MOE_GATE_FULL && on) {
-            unpack(load8(a.gate, at), gate);
+        float v[3];
+        {
+            F2 ss = f2(0.f, 0.f), m = ss, xx = ss;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float2 f = act_slope(a.act, gate[e]);
-                gate[e] = f.x;
-                slope[e] = f.y;
+            for (int i = 0; i < 4; ++i) {
+                const F2 s = pair_of(raw.s, i), x = pair_of(raw.x, i);
+                ss = fma2(s, s, ss);
+                m = fma2(mul2(pair_of(raw.dy, i), weight_of(a.pre_weight, pre, i, off2)), s, m);
+                xx = fma2(x, x, xx);
+            }
+            v[0] = sum2(ss);
+            v[1] = sum2(m);
+            v[2] = sum2(xx);
+        }
+        row_sums<TPR>(v, buf[parity][0]);
+        const float rx = a.post_norm ? rsqrtf(v[2] * inv_n + a.eps) : 1.0f;
+        const float rs = a.dy ? rsqrtf(v[0] * inv_n + a.eps) : 0.0f, ms = -v[1] * inv_n * rs * rs * rs;
+        float2 row_f = make_float2(1.f, 0.f);
+        if (!BY_ELEMENT && a.gate_shape == MOE_GATE_ROW) row_f = act_slope(a.act, raw.row_gate);
+        const F2 rs2 = f2(rs, rs), ms2 = f2(ms, ms);            // -rs^3 mean(dy w s): what s is multiplied by
+        const F2 rx2 = f2(rx, rx), row2 = f2(row_f.x, row_f.x);
+        F2 e[4], m = f2(0.f, 0.f), db = m;
+        uint32_t wd[4], wg[4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            F2 add[3][2];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int i = 2 * h + j;
+                const F2 s = pair_of(raw.s, i), dr = mul2(pair_of(raw.dy, i), rs2);
+                F2 d = pair_of(raw.ds, i);
+                if (a.dy) d = fma2(s, ms2, fma2(dr, weight_of(a.pre_weight, pre, i, off2), d));
+                add[1][j] = mul2(dr, s);
+                wd[i] = pack_pair(d);
+                const F2 x = mul2(pair_of(raw.x, i), rx2), b = mul2(x, weight_of(a.post_weight, post, i, off2)), ds = mul2(d, scale2);
+                if (BY_ELEMENT) {
+                    F2 f, slope;
+                    gate_pair<ACT>(pair_of(raw.gate, i), f, slope);
+                    add[2][j] = mul2(mul2(ds, b), slope);
+                    wg[i] = pack_pair(add[2][j]);
+                    e[i] = mul2(ds, f);
+                } else {
+                    db = fma2(ds, b, db);
+                    e[i] = mul2(ds, row2);
+                    add[2][j] = f2(0.f, 0.f);
+                    wg[i] = 0;
+                }
+                add[0][j] = mul2(e[i], x);
+                m = fma2(e[i], b, m);
+            }
+#pragma unroll
+            for (int k = 0; k < 3; ++k) {
+                if (k == 0 ? !want_post : k == 1 ? !want_pre : !want_gate) continue;
+                float4 *const p = mine + (2 * k + h) * TPR;
+                const float4 o = *p;
+                const float2 lo = unf2(add2(f2(o.x, o.y), add[k][0])), hi = unf2(add2(f2(o.z, o.w), add[k][1]));
+                *p = make_float4(lo.x, lo.y, hi.x, hi.y);
             }
         }
-        float row_slope = 0.f;
-        if (a.gate_shape == MOE_GATE_ROW) {
-            const float2 f = act_slope(a.act, bf16_bits_to_float(a.gate[t]));
-            row_slope = f.y;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) gate[e] = f.x;
+        if (on && a.dresidual) reinterpret_cast<uint4 *>(a.dresidual)[at] = make_uint4(wd[0], wd[1], wd[2], wd[3]);
+        if (on && full) reinterpret_cast<uint4 *>(a.dgate)[at] = make_uint4(wg[0], wg[1], wg[2], wg[3]);
+        float mean = 0.f;
+        if (BY_ELEMENT) {
+            float u[1] = {sum2(m)};
+            if (a.post_norm) row_sums<TPR>(u, buf[parity][1]);
+            mean = -u[0] * inv_n;
+        } else if (a.post_norm || a.gate_shape == MOE_GATE_ROW) {
+            float u[2] = {sum2(m), sum2(db)};
+            row_sums<TPR>(u, buf[parity][1]);
+            if (a.gate_shape == MOE_GATE_ROW && a.dgate && threadIdx.x == 0) static_cast<float *>(a.dgate)[t] = u[1] * row_f.y;
+            mean = -u[0] * inv_n;
         }
-        if (a.dy) {
-            float ss = 0.f, m = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ss = fmaf(s[e], s[e], ss);
-                m = fmaf(dy[e] * pre[e], s[e], m);
-            }
-            const float rs = rsqrtf(block_sum(ss, buf[0]) / (float)a.n + a.eps);
-            m = block_sum(m, buf[1]) / (float)a.n * rs * rs;            // mean(dy w s^) rs
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                sum_pre[e] = fmaf(dy[e], s[e] * rs, sum_pre[e]);
-                d[e] += rs * dy[e] * pre[e] - s[e] * rs * m;
-            }
-        }
-        if (on && a.dresidual) reinterpret_cast<uint4 *>(a.dresidual)[at] = pack(d);
-        float rx = 1.f;
         if (a.post_norm) {
-            float ss = 0.f;
+            const F2 mean2 = f2(mean * rx, mean * rx);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-            rx = rsqrtf(block_sum(ss, buf[2]) / (float)a.n + a.eps);
+            for (int i = 0; i < 4; ++i) e[i] = mul2(fma2(pair_of(raw.x, i), mean2, mul2(e[i], weight_of(a.post_weight, post, i, off2))), rx2);
         }
-        float dg[8], row = 0.f, m = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] *= rx;
-            const float ds = a.scale * d[e], db = ds * x[e] * post[e];
-            row += db;
-            dg[e] = db * slope[e];
-            sum_gate[e] += dg[e];
-            d[e] = ds * gate[e];
-            sum_post[e] = fmaf(d[e], x[e], sum_post[e]);
-            d[e] *= post[e];
-            m = fmaf(d[e], x[e], m);
-        }
-        if (a.dgate && a.gate_shape == MOE_GATE_FULL && on) reinterpret_cast<uint4 *>(a.dgate)[at] = pack(dg);
-        if (a.dgate && a.gate_shape == MOE_GATE_ROW) {
-            row = block_sum(row, buf[3]);
-            if (threadIdx.x == 0) static_cast<float *>(a.dgate)[t] = row * row_slope;
-        }
-        if (a.post_norm) {
-            m = block_sum(m, buf[4]) / (float)a.n;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = rx * (d[e] - x[e] * m);
-        }
-        if (on) reinterpret_cast<uint4 *>(a.dx)[at] = pack(d);
-        __syncthreads();                               // the sums' buffers are the next row's
+        if (on) reinterpret_cast<uint4 *>(a.dx)[at] = make_uint4(pack_pair(e[0]), pack_pair(e[1]), pack_pair(e[2]), pack_pair(e[3]));
     }
-    float *const out = a.partial + (size_t)blockIdx.x * 3 * a.n + 8 * seg;
     if (!on) return;
+    float *const out = a.partial + (size_t)blockIdx.x * 3 * a.n + 8 * seg;
 #pragma unroll
-    for (int e = 0; e < 8; e += 4) {
-        if (a.dpost_weight) *reinterpret_cast<float4 *>(out + e) = make_float4(sum_post[e], sum_post[e + 1], sum_post[e + 2], sum_post[e + 3]);
-        if (a.dpre_weight) *reinterpret_cast<float4 *>(out + a.n + e) = make_float4(sum_pre[e], sum_pre[e + 1], sum_pre[e + 2], sum_pre[e + 3]);
-        if (a.dgate && a.gate_shape == MOE_GATE_CHANNEL)
-            *reinterpret_cast<float4 *>(out + 2 * a.n + e) = make_float4(sum_gate[e], sum_gate[e + 1], sum_gate[e + 2], sum_gate[e + 3]);
-    }
+    for (int k = 0; k < 3; ++k)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (k == 0 ? want_post : k == 1 ? want_pre : want_gate) *reinterpret_cast<float4 *>(out + k * a.n + 4 * h) = mine[(2 * k + h) * TPR];
 }
 
 // Adds up the blocks' sums: a block has 32 columns of one of the three gradients, a warp every 32nd block.
@@ -230,8 +370,11 @@ __global__ void __launch_bounds__(1024) gated_norm_sum_kernel(const __grid_const
                        : a.gate_shape == MOE_GATE_CHANNEL ? static_cast<float *>(a.dgate) : nullptr;
     if (!out) return;
     float v = 0.f;
-    if (col < a.n)
-        for (int b = warp; b < blocks; b += 32) v += a.partial[(size_t)b * 3 * a.n + (size_t)which * a.n + col];
+    if (col < a.n) {
+        const float *p = a.partial + (size_t)which * a.n + col;
+#pragma unroll 4
+        for (int b = warp; b < blocks; b += 32) v += p[(size_t)b * 3 * a.n];
+    }
     part[warp][lane] = v;
     __syncthreads();
     if (warp) return;
@@ -241,12 +384,44 @@ __global__ void __launch_bounds__(1024) gated_norm_sum_kernel(const __grid_const
     if (col < a.n) out[col] = v;
 }
 
-int threads_of(int n) { return (n / 8 + 31) / 32 * 32; }
-// Blocks of the backward pass: 1024 threads an SM of 152.
+// Threads of a block of the backward pass, and blocks an SM.
+constexpr int kGradPlans[][2] = {{32, 16}, {64, 8}, {128, 4}, {256, 2}, {512, 1}, {640, 1}, {768, 1}, {1024, 1}};
+int grad_plan(int n)
+{
+    int i = 0;
+    while (kGradPlans[i][0] * 8 < n) ++i;
+    return i;
+}
+// Blocks of the backward pass, the same on any device: all that fit on 152 SMs.
 int grad_blocks(int T, int n)
 {
-    const int most = 152 * (1024 / threads_of(n) < 8 ? 1024 / threads_of(n) : 8);
+    const int most = 152 * kGradPlans[grad_plan(n)][1];
     return T < most ? T : most;
+}
+template <int TH, int BL, bool AHEAD, bool BY_ELEMENT, int ACT>
+cudaError_t launch_plan(const GatedNormArgs &a, int blocks, cudaStream_t st)
+{
+    constexpr int kSmem = 6 * 16 * TH;
+    auto k = gated_norm_grad_kernel<TH, BL, AHEAD, BY_ELEMENT, ACT>;
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = set_shared(k, kSmem, ready);
+    return e != cudaSuccess ? e : launch_dependent(k, blocks, TH, kSmem, st, a);
+}
+template <int I, bool AHEAD>
+cudaError_t launch_backward(const GatedNormArgs &a, int blocks, cudaStream_t st)
+{
+    constexpr int kThreads = kGradPlans[I][0], kBlocks = kGradPlans[I][1];
+    if (a.gate_shape < MOE_GATE_CHANNEL) return launch_plan<kThreads, kBlocks, AHEAD, false, MOE_ACT_NONE>(a, blocks, st);
+    if (a.act == MOE_ACT_SILU) return launch_plan<kThreads, kBlocks, AHEAD, true, MOE_ACT_SILU>(a, blocks, st);
+    if (a.act == MOE_ACT_SIGMOID) return launch_plan<kThreads, kBlocks, AHEAD, true, MOE_ACT_SIGMOID>(a, blocks, st);
+    return launch_plan<kThreads, kBlocks, AHEAD, true, MOE_ACT_NONE>(a, blocks, st);
+}
+
+template <int TPR, int CH>
+cudaError_t launch_forward(const GatedNormArgs &a, cudaStream_t st)
+{
+    const int rows = block_of(TPR) / TPR;
+    return launch_dependent(gated_norm_kernel<TPR, CH>, (unsigned)((a.T + rows - 1) / rows), block_of(TPR), 0, st, a);
 }
 
 }  // namespace
@@ -255,13 +430,29 @@ size_t gated_norm_partials(int T, int n) { return (size_t)grad_blocks(T, n) * 3 
 
 cudaError_t launch_gated_norm(const GatedNormArgs &a, cudaStream_t st)
 {
-    return launch_dependent(gated_norm_kernel, (unsigned)a.T, threads_of(a.n), 0, st, a);
+    const int nseg = a.n / 8;
+    if (nseg <= 32) return launch_forward<32, 1>(a, st);
+    if (nseg <= 128) return launch_forward<128, 1>(a, st);
+    if (nseg <= 256 && a.T >= 512) return launch_forward<128, 2>(a, st);
+    if (nseg <= 256) return launch_forward<256, 1>(a, st);
+    if (nseg <= 512) return launch_forward<256, 2>(a, st);
+    return launch_forward<512, 2>(a, st);
 }
 
 cudaError_t launch_gated_norm_grad(const GatedNormArgs &a, cudaStream_t st)
 {
     const int blocks = grad_blocks(a.T, a.n);
-    const cudaError_t e = launch_dependent(gated_norm_grad_kernel, blocks, threads_of(a.n), 0, st, a);
+    cudaError_t e = cudaErrorInvalidValue;
+    switch (grad_plan(a.n)) {
+    case 0: e = launch_backward<0, true>(a, blocks, st); break;
+    case 1: e = launch_backward<1, true>(a, blocks, st); break;
+    case 2: e = launch_backward<2, true>(a, blocks, st); break;
+    case 3: e = launch_backward<3, true>(a, blocks, st); break;
+    case 4: e = launch_backward<4, true>(a, blocks, st); break;
+    case 5: e = launch_backward<5, true>(a, blocks, st); break;
+    case 6: e = launch_backward<6, true>(a, blocks, st); break;
+    case 7: e = launch_backward<7, false>(a, blocks, st); break;
+    }
     if (e != cudaSuccess || !(a.dpost_weight || a.dpre_weight || (a.dgate && a.gate_shape == MOE_GATE_CHANNEL))) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((a.n + 31) / 32, 3);
