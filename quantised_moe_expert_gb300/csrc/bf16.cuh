@@ -71,6 +71,7 @@ struct GemmArgs {
     long long wait_limit;
 };
 cudaError_t launch_gemm(const GemmArgs &a, cudaStream_t st);
+cudaError_t launch_gemm_vec(const GemmArgs &a, cudaStream_t st);      // few rows, w [G, N, K] (bf16_vec.cu)
 
 // dw_g (+)= dy_g^T x_g, db_g (+)= column sums of dy_g.
 struct WgradArgs {

@@ -44,6 +44,7 @@ struct Plan {
 
 struct Maps {
     CUtensorMap a[2], a32[2], w[2];                  // first operand(s) in whole and in 32-row boxes, second operand(s)
+    CUtensorMap y, pre[2];                           // outputs, in boxes of 32 rows x 64 bytes
 };
 
 // What a launch computes.
@@ -133,13 +134,18 @@ __device__ __forceinline__ void build_table(const ProductArgs &a, Shared &sh, in
     }
 }
 
-// Tile `tile`: column tiles of a row tile follow each other.
+// Tile `tile`: kBand row tiles of a column follow each other, then those of the next column, so that what the SMs work on at a
+// time shares rows and columns.
+// (Weight gradients of several groups by rows of tiles: the groups share nothing.)
+constexpr int kBand = 8;
 template <int KIND, int ROWS, int OUT_N>
 __device__ __forceinline__ Tile tile_at(const ProductArgs &a, const Shared &sh, int tile, int n_tiles)
 {
-    const int mt = tile / n_tiles;
+    const int most = KIND == kTN && a.offsets ? 1 : kBand;
+    const int band = tile / (most * n_tiles), in = tile - band * most * n_tiles, high = min(most, sh.row_tiles - band * most);
+    const int nt = in / high, mt = band * most + in - nt * high;
     Tile t;
-    t.col0 = (tile - mt * n_tiles) * OUT_N;
+    t.col0 = nt * OUT_N;
     t.first = t.terms = 0;
     if (KIND == kTN) {
         const int per = (a.M + ROWS - 1) / ROWS;
@@ -206,15 +212,22 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 
 // ------------------------------------------------------------------ epilogue
 
-// 32 rows of 64 bytes, a lane a row in 16-byte chunks, to rows `pitch` bytes apart from `dst` on, the first `rows` rows and
-// `chunks` chunks of each, through `stage`: 4 lanes write a row's bytes together.  Row r's chunk k lies at k ^ r / 2 of the
-// row, so that no bank is met twice in a phase.  ADD: fp32 values added to what is there.
-template <bool ADD>
-__device__ __forceinline__ void store_staged(uint8_t *dst, size_t pitch, const uint32_t *w, int rows, int chunks, int lane, uint8_t *stage)
+// 32 rows of 64 bytes, a lane a row in 16-byte chunks, into `stage`: row r's chunk k lies at k ^ r / 2 of the row (the 64-byte
+// swizzle), so that no bank is met twice in a phase.  The copy engine has read what it was last given from there.
+__device__ __forceinline__ void stage_rows(const uint32_t *w, int lane, uint8_t *stage)
 {
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         *reinterpret_cast<uint4 *>(stage + lane * 64 + ((k ^ (lane >> 1)) & 3) * 16) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+}
+// The first `rows` rows and `chunks` chunks of each to rows `pitch` bytes apart from `dst` on: 4 lanes write a row's bytes
+// together.  ADD: fp32 values added to what is there.
+template <bool ADD>
+__device__ __forceinline__ void store_staged(uint8_t *dst, size_t pitch, const uint32_t *w, int rows, int chunks, int lane, uint8_t *stage)
+{
+    stage_rows(w, lane, stage);
     __syncwarp();
     const int k = lane & 3;
 #pragma unroll
@@ -235,11 +248,32 @@ __device__ __forceinline__ void store_staged(uint8_t *dst, size_t pitch, const u
     }
     __syncwarp();
 }
+// The same through the copy engine, which leaves out what lies past the map's last row and column.  A lane of its own row
+// touches 32 lines in every store, and through shared memory and back 64 wavefronts of the load/store unit are needed for 32
+// columns; this way 16 (weight gradients of 64 experts, one step a tile: 5,000 cycles a tile with plain stores).
+template <int KIND>
+__device__ __forceinline__ void store_box(const CUtensorMap *map, int col, int row, int g, const uint32_t *w, int lane, uint8_t *stage)
+{
+    stage_rows(w, lane, stage);
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (KIND == kTN)
+            asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                         "r"(col), "r"(row), "r"(g), "r"(smem_u32(stage))
+                         : "memory");
+        else
+            tma_store_2d(map, col, row, smem_u32(stage));
+        bulk_commit();
+    }
+}
 // The other way: the lane's row of up to 64 bytes.
 __device__ __forceinline__ void load_staged(uint32_t *w, const uint8_t *src, size_t pitch, int rows, int chunks, int lane, uint8_t *stage)
 {
     const int k = lane & 3;
     uint4 v[4];
+    if (lane == 0) bulk_wait_read<0>();
+    __syncwarp();
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = i * 8 + lane / 4;
@@ -263,15 +297,8 @@ __device__ __forceinline__ void load_staged(uint32_t *w, const uint8_t *src, siz
     __syncwarp();
 }
 
-template <int N>
-__device__ __forceinline__ void pack_row(const float (&v)[N], uint32_t (&w)[N / 2])
-{
-#pragma unroll
-    for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
-}
-
-// Adds the bias of 32 columns from `col` on (of which `cols` exist) to a row.
-__device__ __forceinline__ void add_bias(float (&v)[32], const uint16_t *bias, int cols)
+// Adds the bias of 32 columns (of which `cols` exist) to a row.
+__device__ __forceinline__ void add_bias(float *v, const uint16_t *bias, int cols)
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -285,102 +312,108 @@ __device__ __forceinline__ void add_bias(float (&v)[32], const uint16_t *bias, i
         }
     }
 }
-__device__ __forceinline__ void apply(int act, float (&v)[32])
+template <int N>
+__device__ __forceinline__ void apply(int act, float (&v)[N])
 {
     switch (act) {
     case MOE_ACT_SILU:
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = act_value(MOE_ACT_SILU, v[i]);
+        for (int i = 0; i < N; ++i) v[i] = act_value(MOE_ACT_SILU, v[i]);
         break;
     case MOE_ACT_GELU:
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = act_value(MOE_ACT_GELU, v[i]);
+        for (int i = 0; i < N; ++i) v[i] = act_value(MOE_ACT_GELU, v[i]);
         break;
     case MOE_ACT_RELU:
 #pragma unroll
-        for (int i = 0; i < 32; ++i) v[i] = act_value(MOE_ACT_RELU, v[i]);
+        for (int i = 0; i < N; ++i) v[i] = act_value(MOE_ACT_RELU, v[i]);
         break;
     default: break;
     }
 }
+template <int N>
+__device__ __forceinline__ void load_columns(uint32_t d, float (&v)[N])
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 16) {
+        uint32_t r[16];
+        tmem_ld16(d + c, r);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[c + i] = __uint_as_float(r[i]);
+    }
+}
 
-// The warp's 32 rows x COLS columns of a tile from the accumulators (second: those of the up products) to the outputs, 32
-// columns at a time; release() once the accumulators are read.  row: the first row's index in the outputs, of which
-// `rows` exist; cols: columns from col0 on that exist; empty: a sum without terms.
+// The warp's 32 rows x COLS columns of a tile from the accumulators (second: those of the up products) to the outputs;
+// release() once the accumulators are in registers.  row: the first row's index (TN: in its matrix), of which `rows` exist;
+// whole: no row of another group follows within the 32; empty: a sum without terms.
 template <int KIND, bool DUAL, int COLS, class Release>
-__device__ __forceinline__ void finish(const ProductArgs &a, uint32_t d, uint32_t second, int g, size_t row, int rows, int col0, bool empty,
-                                       int lane, uint8_t *stage, Release release)
+__device__ __forceinline__ void finish(const ProductArgs &a, const Maps &maps, uint32_t d, uint32_t second, int g, int row, int rows, bool whole,
+                                       int col0, bool empty, int lane, uint8_t *stage, Release release)
 {
     const size_t n = a.N;
-#pragma unroll 1
-    for (int c = 0; c < COLS; c += 32) {
-        float v[32], u[32];
-        {
-            uint32_t r0[16], r1[16], s0[16], s1[16];
-            tmem_ld16(d + c, r0);
-            tmem_ld16(d + c + 16, r1);
-            if (DUAL) {
-                tmem_ld16(second + c, s0);
-                tmem_ld16(second + c + 16, s1);
+    float v[COLS], u[DUAL ? COLS : 1];
+    load_columns(d, v);
+    if constexpr (DUAL) load_columns(second, u);
+    tmem_ld_wait();
+    release();
+    if (KIND == kTN && empty) {
+#pragma unroll
+        for (int i = 0; i < COLS; ++i) v[i] = 0.f;
+    }
+    const size_t first = KIND == kTN ? (size_t)g * a.M + row : (size_t)row;
+    // 32 bf16 columns from c on of these rows
+    auto put16 = [&](const CUtensorMap *map, uint16_t *out, const float *from, int c, int cols) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w[i] = pack_bf16(from[2 * i], from[2 * i + 1]);
+        if (whole) store_box<KIND>(map, col0 + c, row, g, w, lane, stage);
+        else store_staged<false>(reinterpret_cast<uint8_t *>(out + first * n + col0 + c), n * 2, w, rows, cols / 8, lane, stage);
+    };
+    if (KIND != kTN) {
+#pragma unroll
+        for (int c = 0; c < COLS; c += 32) {
+            const int cols = a.N - col0 - c;
+            if (cols <= 0) break;
+            if (a.bias[0]) add_bias(v + c, a.bias[0] + g * n + col0 + c, cols);
+            if (a.pre[0]) put16(&maps.pre[0], a.pre[0], v + c, c, cols);
+            if constexpr (DUAL) {
+                if (a.bias[1]) add_bias(u + c, a.bias[1] + g * n + col0 + c, cols);
+                if (a.pre[1]) put16(&maps.pre[1], a.pre[1], u + c, c, cols);
             }
-            tmem_ld_wait();
+        }
+        apply(a.act, v);
+        if constexpr (DUAL) {
+#pragma unroll
+            for (int i = 0; i < COLS; ++i) v[i] *= u[i];
+        }
+    }
+#pragma unroll
+    for (int c = 0; c < COLS; c += 32) {
+        const int cols = a.N - col0 - c;
+        if (cols <= 0) break;
+        if (KIND != kTN && !DUAL && a.residual) {
+            uint32_t w[16];
+            load_staged(w, reinterpret_cast<const uint8_t *>(a.residual + first * n + col0 + c), n * 2, rows, cols / 8, lane, stage);
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                v[i] = __uint_as_float(r0[i]);
-                v[16 + i] = __uint_as_float(r1[i]);
-                if (DUAL) {
-                    u[i] = __uint_as_float(s0[i]);
-                    u[16 + i] = __uint_as_float(s1[i]);
-                }
+                v[c + 2 * i] += bf16_lo(w[i]);
+                v[c + 2 * i + 1] += bf16_hi(w[i]);
             }
         }
-        if (c + 32 >= COLS) release();
-        const int col = col0 + c, cols = a.N - col;
-        if (cols <= 0) continue;
-        const size_t at = row * n + col;
-        uint32_t w[16];
-        if (KIND == kTN) {
-            if (empty) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0.f;
-            }
-        } else {
-            if (a.bias[0]) add_bias(v, a.bias[0] + g * n + col, cols);
-            if (DUAL && a.bias[1]) add_bias(u, a.bias[1] + g * n + col, cols);
-            if (a.pre[0]) {
-                pack_row(v, w);
-                store_staged<false>(reinterpret_cast<uint8_t *>(a.pre[0] + at), n * 2, w, rows, cols / 8, lane, stage);
-            }
-            if (DUAL && a.pre[1]) {
-                pack_row(u, w);
-                store_staged<false>(reinterpret_cast<uint8_t *>(a.pre[1] + at), n * 2, w, rows, cols / 8, lane, stage);
-            }
-            apply(a.act, v);
-            if (DUAL) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] *= u[i];
-            }
-            if (!DUAL && a.residual) {
-                load_staged(w, reinterpret_cast<const uint8_t *>(a.residual + at), n * 2, rows, cols / 8, lane, stage);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    v[2 * i] += bf16_lo(w[i]);
-                    v[2 * i + 1] += bf16_hi(w[i]);
-                }
-            }
+        if (DUAL || !a.y_f32) {
+            put16(&maps.y, static_cast<uint16_t *>(a.y), v + c, c, cols);
+            continue;
         }
-        if (!DUAL && a.y_f32) {
-            uint8_t *y = reinterpret_cast<uint8_t *>(static_cast<float *>(a.y) + at);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+        for (int h = 0; h < 2 * 16; h += 16) {
+            if (h >= cols) break;
+            uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[16 * h + i]);
-                if (KIND == kTN && a.accumulate) store_staged<true>(y + 64 * h, n * 4, w, rows, cols / 4 - 4 * h, lane, stage);
-                else store_staged<false>(y + 64 * h, n * 4, w, rows, cols / 4 - 4 * h, lane, stage);
-            }
-        } else {
-            pack_row(v, w);
-            store_staged<false>(reinterpret_cast<uint8_t *>(static_cast<uint16_t *>(a.y) + at), n * 2, w, rows, cols / 8, lane, stage);
+            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[c + h + i]);
+            uint8_t *y = reinterpret_cast<uint8_t *>(static_cast<float *>(a.y) + first * n + col0 + c + h);
+            if (KIND == kTN && a.accumulate) store_staged<true>(y, n * 4, w, rows, (cols - h) / 4, lane, stage);
+            else if (whole) store_box<KIND>(&maps.y, col0 + c + h, row, g, w, lane, stage);
+            else store_staged<false>(y, n * 4, w, rows, (cols - h) / 4, lane, stage);
         }
     }
 }
@@ -553,7 +586,6 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
         int st = 0, acc = 0;
         uint32_t ph = 0, aph = 0, cph = 0;                              // cph: a bit a stage
         bool ok = true;
-        constexpr uint32_t kId = idesc_bf16<KIND>(P::kRows, BN);
         for (int tile = first_tile; ok && tile < total; tile += stride) {
             const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
             const int steps = steps_of(t);
@@ -561,6 +593,8 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
             ok = wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1);
             tc_fence_after();
             const uint32_t d = tmem + acc * BN;
+            // columns past the last are not multiplied (whole instructions of 16)
+            const uint32_t id = idesc_bf16<KIND>(P::kRows, PAIR || DUAL ? BN : min(BN, (a.N - t.col0 + 15) & ~15));
             for (int ks = 0; ok && ks < steps; ++ks) {
                 ok = wait(smem_u32(&sh.full[st]), ph);
                 if (PAIR && ok && clear && ks == steps - 1) {
@@ -577,7 +611,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                 const int kk = (left + 15) / 16;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * (KIND == kTN ? 128 : 2), bd + j * (KIND == kNT ? 2 : 128), kId, ks > 0 || j > 0,
+                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * (KIND == kTN ? 128 : 2), bd + j * (KIND == kNT ? 2 : 128), id, ks > 0 || j > 0,
                                            leader & (uint32_t)(j < kk));
                 if (leader) {
                     if (PAIR) mma_commit_pair(smem_u32(&sh.empty[st]));
@@ -627,11 +661,17 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                 break;
             }
             tph ^= 1u << st;
-            const int lo = t.terms % kStep, n = ((lo + 15) & ~15) - lo;               // rows up to the end of an instruction
-            uint8_t *const base = smem + st * P::kStageBytes;
-            for (int i = lane; i < (2 + P::kHeld / 64) * n * 8; i += 32) {
-                const int block = i / (n * 8), rest = i - block * n * 8;
-                *reinterpret_cast<uint4 *>(base + block * kBlockBytes + (lo + rest / 8) * 128 + rest % 8 * 16) = make_uint4(0, 0, 0, 0);
+            // rows up to the end of an instruction, 8 lanes a row
+            const int lo = t.terms % kStep, end = (lo + 15) & ~15;
+            uint8_t *const base = smem + st * P::kStageBytes + lane % 8 * 16;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = lo + lane / 8 + 4 * i;
+                if (r < end) {
+#pragma unroll
+                    for (int block = 0; block < 2 + P::kHeld / 64; ++block)
+                        *reinterpret_cast<uint4 *>(base + block * kBlockBytes + r * 128) = make_uint4(0, 0, 0, 0);
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -666,8 +706,9 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                 }
             };
             if (r0 < t.rows && col0 < a.N)
-                finish<KIND, DUAL, kCols>(a, d, d + BN / 2, t.g, (size_t)(KIND == kTN ? (size_t)t.g * a.M : 0) + t.row0 + r0, t.rows - r0, col0,
-                                          KIND == kTN && t.terms == 0, lane, smem + P::kOutAt + (warp - 4) * (P::kOutBytes / 8), release);
+                finish<KIND, DUAL, kCols>(a, maps, d, d + BN / 2, t.g, t.row0 + r0, t.rows - r0,
+                                          KIND == kTN || t.rows - r0 >= 32 || t.row0 + t.rows == a.R, col0, KIND == kTN && t.terms == 0, lane,
+                                          smem + P::kOutAt + (warp - 4) * (P::kOutBytes / 8), release);
             else
                 release();
             if (++acc == 2) {
@@ -675,6 +716,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                 aph ^= 1;
             }
         }
+        if (lane == 0) bulk_wait<0>();                                // what was written through the copy engine is there
     }
     __syncthreads();
     if (PAIR) {
@@ -709,6 +751,17 @@ cudaError_t launch_plan(const ProductArgs &a, const Maps &maps, int ctas, cudaSt
     const cudaError_t e = set_shared(k, P::kSmem, ready);
     if (e != cudaSuccess) return e;
     return launch_dependent_clusters(k, ctas, PAIR ? 2 : 1, kThreads, P::kSmem, st, a, maps);
+}
+
+// Rows of outputs in boxes of 32 x 64 bytes: [rows, cols], or with G > 0 [G, rows, cols].
+bool map_out(CUtensorMap *m, void *p, bool f32, uint64_t cols, uint64_t rows, uint64_t G)
+{
+    const CUtensorMapDataType type = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint32_t size = f32 ? 4 : 2;
+    if (!G) return make_map_2d(m, p, type, size, cols, rows, 64 / size, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    const uint64_t dims[3] = {cols, rows, G}, strides[2] = {cols * size, cols * rows * size};
+    const uint32_t box[3] = {64 / size, 32, 1};
+    return make_map_3d(m, p, type, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
 }
 
 bool map_2d(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows, uint32_t box_rows)
@@ -844,6 +897,9 @@ cudaError_t launch_rows_product(const GemmArgs &g, cudaStream_t st)
             ok = ok && map_2d(&maps.w[i], g.w[i], a.K, (uint64_t)a.G * a.N, pair ? 128 : DUAL ? bn / 2 : bn);
         }
     }
+    ok = ok && map_out(&maps.y, g.y, g.y_f32, a.N, a.R, 0);
+    for (int i = 0; i < 2; ++i)
+        if (g.pre[i]) ok = ok && map_out(&maps.pre[i], g.pre[i], false, a.N, a.R, 0);
     if (!ok) return cudaErrorInvalidValue;
     if (pair) return launch_plan<KIND, DUAL, 256, true>(a, maps, sms / 2 * 2, st);
     const long long n = tiles(DUAL ? bn / 2 : bn);
@@ -858,6 +914,13 @@ cudaError_t launch_rows_product(const GemmArgs &g, cudaStream_t st)
 
 cudaError_t launch_gemm(const GemmArgs &g, cudaStream_t st)
 {
+    // Few rows without tiles (bf16_vec.cu): up to 8 of one group; of groups, up to a number of outputs that grows with K, since a
+    // tile's steps follow each other.  us, tiles / without: 1 to 8 x 4096 x 2048 9.9 / 4.9 to 5.1, x 8192 x 4096 17.1 / 13.2 to 14.3,
+    // x 2048 x 512 4.0 / 2.6 to 2.9; 9 and 16 x 4096 x 2048 9.9 / 7.9, 8.3, x 8192 x 4096 17.0 / 22.1, 23.8.  Experts (257, hidden 2048,
+    // inter 512), 1, 2, 4, 8 and 16 tokens: the gated pair 11.8 / 8.0, 14.9 / 13.8, 25.7 / 25.1, 42.9 / 42.1, 69.6 / 71.9 (73,728
+    // outputs at 8 tokens), the down products 6.8 / 5.4, 9.4 / 9.6 (18,432 and 36,864).
+    const long long outputs = (long long)g.R * g.N * (g.glu ? 2 : 1), most = g.K < 512 ? 20480 : g.K < 2048 ? 40ll * g.K : 81920;
+    if (!g.w_kn && (g.offsets ? outputs <= most : g.R <= 8)) return launch_gemm_vec(g, st);
     if (g.glu) return launch_rows_product<kNT, true>(g, st);
     return g.w_kn ? launch_rows_product<kNN, false>(g, st) : launch_rows_product<kNT, false>(g, st);
 }
@@ -884,7 +947,7 @@ cudaError_t launch_wgrad(const WgradArgs &g, cudaStream_t st)
         if (tiles(128, 64) <= sms) bn = 64;
     }
     Maps maps{};
-    if (!map_2d(&maps.a[0], g.dy, a.M, a.R, 64) || !map_2d(&maps.w[0], g.x, a.N, a.R, 64)) return cudaErrorInvalidValue;
+    if (!map_2d(&maps.a[0], g.dy, a.M, a.R, 64) || !map_2d(&maps.w[0], g.x, a.N, a.R, 64) || !map_out(&maps.y, g.dw, g.f32, a.N, a.M, a.G)) return cudaErrorInvalidValue;
     const long long n = tiles(128, bn);
     const int ctas = (int)(n < sms ? n : sms);
     const cudaError_t e = pair        ? launch_plan<kTN, false, 256, true>(a, maps, sms / 2 * 2, st)
