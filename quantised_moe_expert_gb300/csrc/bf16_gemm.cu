@@ -30,16 +30,19 @@ constexpr int kStep = 64;                          // terms of a step: 128 bytes
 constexpr int kBlockBytes = 64 * 128;              // an MN-major block: 64 terms x 64 columns
 enum Kind { kNT, kNN, kTN };
 
-template <int KIND, bool DUAL, int BN, bool PAIR>
+template <int KIND, bool DUAL, int BN, bool PAIR, int SPLIT>
 struct Plan {
     static constexpr int kOutN = DUAL ? BN / 2 : BN;                 // output columns of a tile
     static constexpr int kRows = PAIR ? 256 : 128;                   // output rows of a tile
     static constexpr int kHeld = PAIR ? BN / 2 : BN;                 // columns of the second operand in this CTA
     static constexpr int kABytes = 128 * 128, kBBytes = kHeld * 128, kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = PAIR ? 6 : BN == 256 ? 4 : BN == 128 ? 6 : 8;
-    static constexpr int kStaged = 64;                               // bytes of a row that an epilogue warp stages at a time
-    static constexpr int kOutBytes = 8 * 32 * kStaged;
-    static constexpr int kOutAt = kStages * kStageBytes, kSmem = kOutAt + kOutBytes + 1024;
+    static constexpr int kStages = PAIR ? 6 : BN == 256 ? 4 : BN == 128 ? (SPLIT > 1 ? 4 : 5) : 7;
+    // an epilogue warp's 64-byte pieces of 32 rows: two, where the table of groups leaves room
+    static constexpr int kBufs = KIND != kTN && (PAIR || BN == 256) ? 1 : 2, kOutBytes = SPLIT > 1 ? 0 : 8 * 2048 * kBufs;
+    static constexpr int kMats = DUAL ? 2 : 1;
+    static constexpr int kPartBytes = SPLIT > 1 ? kMats * kOutN * 128 * 4 : 0;   // all CTAs' sums of them
+    static constexpr int kOutAt = kStages * kStageBytes, kPartAt = kOutAt + kOutBytes, kSmem = kPartAt + kPartBytes + 1024;
+    static_assert(SPLIT == 1 || (kMats * kOutN <= 128 && !PAIR), "shared memory of the sums");
 };
 
 struct Maps {
@@ -59,6 +62,7 @@ struct ProductArgs {
     long long wait_limit;
 };
 
+template <int KIND>
 struct Shared {
     uint64_t full[8], empty[8], tail[8], cleared[8], acc_full[2], acc_empty[2], drain;
     uint32_t tmem;
@@ -66,7 +70,7 @@ struct Shared {
     int bad, groups, row_tiles;                      // malformed offsets; groups with rows; their row tiles
     int gave_up, issued[2];                          // a pair's: whether any of its waits ran out; copies of each CTA
     int2 warp_sum[kThreads / 32];
-    int2 group[kMaxGroups + 1];                      // NT, NN: those groups: row tiles before it, start << 10 | group; TN: offsets
+    int2 group[KIND == kTN ? 1 : kMaxGroups + 1];    // those groups: row tiles before it, start << 10 | group
 };
 
 constexpr int kGroupBits = 10;
@@ -77,9 +81,9 @@ struct Tile {
     int first, terms;                                // TN: first row of the sum, rows of it
 };
 
-// The groups with rows and the tiles before each (NT, NN), or the groups' first rows (TN).  Every thread takes part.
+// The groups with rows and the tiles before each (NT, NN); a check of the offsets alone (TN).  Every thread takes part.
 template <int KIND, int ROWS>
-__device__ __forceinline__ void build_table(const ProductArgs &a, Shared &sh, int warp, int lane)
+__device__ __forceinline__ void build_table(const ProductArgs &a, Shared<KIND> &sh, int warp, int lane)
 {
     constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
     const int g0 = threadIdx.x * kPer;
@@ -90,12 +94,10 @@ __device__ __forceinline__ void build_table(const ProductArgs &a, Shared &sh, in
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
         if (o[i] < 0 || o[i] > a.R || o[i + 1] < o[i]) sh.bad = 1;
-        if (KIND == kTN && g0 + i <= a.G) sh.group[g0 + i].x = o[i];
         n.x += (max(o[i + 1] - o[i], 0) + ROWS - 1) / ROWS;
         n.y += o[i + 1] > o[i];
     }
     if (KIND == kTN) {
-        if (threadIdx.x == 0) sh.group[a.G].x = a.R;
         __syncthreads();
         if (threadIdx.x == 0 && sh.bad) {
             sh.row_tiles = 0;
@@ -139,7 +141,7 @@ __device__ __forceinline__ void build_table(const ProductArgs &a, Shared &sh, in
 // (Weight gradients of several groups by rows of tiles: the groups share nothing.)
 constexpr int kBand = 8;
 template <int KIND, int ROWS, int OUT_N>
-__device__ __forceinline__ Tile tile_at(const ProductArgs &a, const Shared &sh, int tile, int n_tiles)
+__device__ __forceinline__ Tile tile_at(const ProductArgs &a, const Shared<KIND> &sh, int tile, int n_tiles)
 {
     const int most = KIND == kTN && a.offsets ? 1 : kBand;
     const int band = tile / (most * n_tiles), in = tile - band * most * n_tiles, high = min(most, sh.row_tiles - band * most);
@@ -152,8 +154,8 @@ __device__ __forceinline__ Tile tile_at(const ProductArgs &a, const Shared &sh, 
         t.g = mt / per;
         t.row0 = (mt - t.g * per) * ROWS;
         t.rows = min(a.M - t.row0, ROWS);
-        t.first = a.offsets ? sh.group[t.g].x : 0;
-        t.terms = (a.offsets ? sh.group[t.g + 1].x : a.R) - t.first;
+        t.first = a.offsets ? a.offsets[t.g] : 0;
+        t.terms = (a.offsets && t.g + 1 < a.G ? a.offsets[t.g + 1] : a.R) - t.first;
         return t;
     }
     if (!a.offsets) {
@@ -214,9 +216,14 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap
 
 // 32 rows of 64 bytes, a lane a row in 16-byte chunks, into `stage`: row r's chunk k lies at k ^ r / 2 of the row (the 64-byte
 // swizzle), so that no bank is met twice in a phase.  The copy engine has read what it was last given from there.
+struct Stage {
+    uint8_t *base;
+    int cur;                                         // byte of the buffer that is next
+};
+template <int LEFT>
 __device__ __forceinline__ void stage_rows(const uint32_t *w, int lane, uint8_t *stage)
 {
-    if (lane == 0) bulk_wait_read<0>();
+    if (lane == 0) bulk_wait_read<LEFT>();
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < 4; ++k)
@@ -225,9 +232,10 @@ __device__ __forceinline__ void stage_rows(const uint32_t *w, int lane, uint8_t 
 // The first `rows` rows and `chunks` chunks of each to rows `pitch` bytes apart from `dst` on: 4 lanes write a row's bytes
 // together.  ADD: fp32 values added to what is there.
 template <bool ADD>
-__device__ __forceinline__ void store_staged(uint8_t *dst, size_t pitch, const uint32_t *w, int rows, int chunks, int lane, uint8_t *stage)
+__device__ __forceinline__ void store_staged(uint8_t *dst, size_t pitch, const uint32_t *w, int rows, int chunks, int lane, const Stage &buf)
 {
-    stage_rows(w, lane, stage);
+    uint8_t *const stage = buf.base + buf.cur;
+    stage_rows<0>(w, lane, stage);
     __syncwarp();
     const int k = lane & 3;
 #pragma unroll
@@ -251,10 +259,12 @@ __device__ __forceinline__ void store_staged(uint8_t *dst, size_t pitch, const u
 // The same through the copy engine, which leaves out what lies past the map's last row and column.  A lane of its own row
 // touches 32 lines in every store, and through shared memory and back 64 wavefronts of the load/store unit are needed for 32
 // columns; this way 16 (weight gradients of 64 experts, one step a tile: 5,000 cycles a tile with plain stores).
-template <int KIND>
-__device__ __forceinline__ void store_box(const CUtensorMap *map, int col, int row, int g, const uint32_t *w, int lane, uint8_t *stage)
+template <int KIND, int BUFS>
+__device__ __forceinline__ void store_box(const CUtensorMap *map, int col, int row, int g, const uint32_t *w, int lane, Stage &buf)
 {
-    stage_rows(w, lane, stage);
+    uint8_t *const stage = buf.base + buf.cur;
+    stage_rows<BUFS - 1>(w, lane, stage);
+    if (BUFS > 1) buf.cur ^= 2048;
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
@@ -268,8 +278,9 @@ __device__ __forceinline__ void store_box(const CUtensorMap *map, int col, int r
     }
 }
 // The other way: the lane's row of up to 64 bytes.
-__device__ __forceinline__ void load_staged(uint32_t *w, const uint8_t *src, size_t pitch, int rows, int chunks, int lane, uint8_t *stage)
+__device__ __forceinline__ void load_staged(uint32_t *w, const uint8_t *src, size_t pitch, int rows, int chunks, int lane, const Stage &buf)
 {
+    uint8_t *const stage = buf.base + buf.cur;
     const int k = lane & 3;
     uint4 v[4];
     if (lane == 0) bulk_wait_read<0>();
@@ -346,9 +357,9 @@ __device__ __forceinline__ void load_columns(uint32_t d, float (&v)[N])
 // The warp's 32 rows x COLS columns of a tile from the accumulators (second: those of the up products) to the outputs;
 // release() once the accumulators are in registers.  row: the first row's index (TN: in its matrix), of which `rows` exist;
 // whole: no row of another group follows within the 32; empty: a sum without terms.
-template <int KIND, bool DUAL, int COLS, class Release>
+template <int KIND, bool DUAL, int COLS, int BUFS, class Release>
 __device__ __forceinline__ void finish(const ProductArgs &a, const Maps &maps, uint32_t d, uint32_t second, int g, int row, int rows, bool whole,
-                                       int col0, bool empty, int lane, uint8_t *stage, Release release)
+                                       int col0, bool empty, int lane, Stage &stage, Release release)
 {
     const size_t n = a.N;
     float v[COLS], u[DUAL ? COLS : 1];
@@ -366,7 +377,7 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const Maps &maps, u
         uint32_t w[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) w[i] = pack_bf16(from[2 * i], from[2 * i + 1]);
-        if (whole) store_box<KIND>(map, col0 + c, row, g, w, lane, stage);
+        if (whole) store_box<KIND, BUFS>(map, col0 + c, row, g, w, lane, stage);
         else store_staged<false>(reinterpret_cast<uint8_t *>(out + first * n + col0 + c), n * 2, w, rows, cols / 8, lane, stage);
     };
     if (KIND != kTN) {
@@ -404,38 +415,113 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const Maps &maps, u
             put16(&maps.y, static_cast<uint16_t *>(a.y), v + c, c, cols);
             continue;
         }
+        if constexpr (!DUAL) {
 #pragma unroll
-        for (int h = 0; h < 2 * 16; h += 16) {
-            if (h >= cols) break;
-            uint32_t w[16];
+            for (int h = 0; h < 32; h += 16) {
+                if (h >= cols) break;
+                uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[c + h + i]);
-            uint8_t *y = reinterpret_cast<uint8_t *>(static_cast<float *>(a.y) + first * n + col0 + c + h);
-            if (KIND == kTN && a.accumulate) store_staged<true>(y, n * 4, w, rows, (cols - h) / 4, lane, stage);
-            else if (whole) store_box<KIND>(&maps.y, col0 + c + h, row, g, w, lane, stage);
-            else store_staged<false>(y, n * 4, w, rows, (cols - h) / 4, lane, stage);
+                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[c + h + i]);
+                uint8_t *y = reinterpret_cast<uint8_t *>(static_cast<float *>(a.y) + first * n + col0 + c + h);
+                if (KIND == kTN && a.accumulate) store_staged<true>(y, n * 4, w, rows, (cols - h) / 4, lane, stage);
+                else if (whole) store_box<KIND, BUFS>(&maps.y, col0 + c + h, row, g, w, lane, stage);
+                else store_staged<false>(y, n * 4, w, rows, (cols - h) / 4, lane, stage);
+            }
+        }
+    }
+}
+
+// A split tile's columns that this CTA finishes, from all CTAs' sums: part[(source, matrix, column / 4)][row] of four columns.
+template <int KIND, bool DUAL, int COLS, int SPLIT>
+__device__ __forceinline__ void finish_split(const ProductArgs &a, const float4 *part, const Tile &t, int col0)
+{
+    constexpr int kMats = DUAL ? 2 : 1, kSegs = COLS / 8;
+    const size_t n = a.N, first = KIND == kTN ? (size_t)t.g * a.M + t.row0 : (size_t)t.row0;
+    for (int i = threadIdx.x; i < t.rows * kSegs; i += kThreads) {
+        const int r = i / kSegs, seg = i - r * kSegs, col = col0 + 8 * seg;
+        if (col >= a.N) continue;
+        float v[kMats][8];
+#pragma unroll
+        for (int m = 0; m < kMats; ++m) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[m][e] = 0.f;
+#pragma unroll
+            for (int s = 0; s < SPLIT; ++s)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float4 p = part[((s * kMats + m) * (COLS / 4) + 2 * seg + h) * 128 + r];
+                    v[m][4 * h] += p.x;
+                    v[m][4 * h + 1] += p.y;
+                    v[m][4 * h + 2] += p.z;
+                    v[m][4 * h + 3] += p.w;
+                }
+        }
+        const size_t at = (first + r) * n + col;
+        auto add16 = [&](float (&x)[8], const uint16_t *p) {
+            const uint4 b = *reinterpret_cast<const uint4 *>(p);
+            const uint32_t w[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[2 * k] += bf16_lo(w[k]);
+                x[2 * k + 1] += bf16_hi(w[k]);
+            }
+        };
+        auto put16 = [&](uint16_t *p, const float (&x)[8]) {
+            *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+        };
+        if (KIND != kTN) {
+#pragma unroll
+            for (int m = 0; m < kMats; ++m) {
+                if (a.bias[m]) add16(v[m], a.bias[m] + t.g * n + col);
+                if (a.pre[m]) put16(a.pre[m] + at, v[m]);
+            }
+            apply(a.act, v[0]);
+            if (DUAL) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[0][e] *= v[kMats - 1][e];
+            }
+            if (!DUAL && a.residual) add16(v[0], a.residual + at);
+        }
+        if (DUAL || !a.y_f32) {
+            put16(static_cast<uint16_t *>(a.y) + at, v[0]);
+            continue;
+        }
+        float4 *y = reinterpret_cast<float4 *>(static_cast<float *>(a.y) + at);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float4 o = make_float4(v[0][4 * h], v[0][4 * h + 1], v[0][4 * h + 2], v[0][4 * h + 3]);
+            if (KIND == kTN && a.accumulate) {
+                const float4 p = y[h];
+                o = make_float4(o.x + p.x, o.y + p.y, o.z + p.z, o.w + p.w);
+            }
+            y[h] = o;
         }
     }
 }
 
 // ------------------------------------------------------------------ the kernel
 //
+// SPLIT: few tiles, where the steps one after the other are the time: a cluster of SPLIT CTAs shares out a tile's steps;
+// each CTA finishes its part of the tile's columns from all CTAs' sums, which meet in its shared memory, in their order.
+//
 // PAIR: two SMs share a tile of 256 x 256 (cta_group::2): each holds its own 128 rows of the first operand and half of the
 // second's columns, so that a step brings an SM 32 KB in place of 48 KB for the same products.  The first CTA issues the
 // products of both; a stage's copies complete on its barrier, and its commits arrive in both.  A step whose end has to
 // be cleared completes on each CTA's own barrier first, and counts once both have cleared their part.
 
-template <int KIND, bool DUAL, int BN, bool PAIR>
+template <int KIND, bool DUAL, int BN, bool PAIR, int SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
 product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Maps maps)
 {
-    using P = Plan<KIND, DUAL, BN, PAIR>;
+    using P = Plan<KIND, DUAL, BN, PAIR, SPLIT>;
+    constexpr int kCluster = PAIR ? 2 : SPLIT;
+    [[maybe_unused]] constexpr int kPartCols = P::kOutN / SPLIT;     // columns that this CTA of a split tile finishes
     extern __shared__ uint8_t smem_raw[];
-    __shared__ Shared sh;
+    __shared__ Shared<KIND> sh;
     uint8_t *smem = align_smem_1024(smem_raw);
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int rank = PAIR ? (int)cluster_ctarank() : 0;
-    const int first_tile = PAIR ? blockIdx.x >> 1 : blockIdx.x, stride = PAIR ? gridDim.x >> 1 : gridDim.x;
+    const int rank = PAIR ? (int)cluster_ctarank() : 0, part = SPLIT > 1 ? (int)cluster_ctarank() : 0;
+    const int first_tile = blockIdx.x / kCluster, stride = gridDim.x / kCluster;
     const int n_tiles = (a.N + P::kOutN - 1) / P::kOutN, k_steps = (a.K + kStep - 1) / kStep;
 
     pdl_trigger();
@@ -469,12 +555,12 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
         }
     }
     __syncthreads();
-    if (PAIR) cluster_arrive();
+    if (kCluster > 1) cluster_arrive();
     pdl_wait();
     if (a.offsets) build_table<KIND, P::kRows>(a, sh, warp, lane);
     tc_fence_before();
     __syncthreads();
-    if (PAIR) cluster_wait();                                         // the barriers of both CTAs are there
+    if (kCluster > 1) cluster_wait();                                 // the barriers of all its CTAs are there
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, sh.tmem, 0);
     const int total = __shfl_sync(0xFFFFFFFFu, sh.row_tiles * n_tiles, 0);
@@ -491,8 +577,14 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
         return __all_sync(0xFFFFFFFFu, PAIR ? mbar_wait_cluster(bar, parity, a.wait_limit, abort) : mbar_wait(bar, parity, a.wait_limit, abort));
     };
     auto steps_of = [&](const Tile &t) { return KIND == kTN ? (t.terms + kStep - 1) / kStep : a.pairs * k_steps; };
-    // the last step of a sum that ends inside it, before the last of all rows (past which the copies bring zeros)
-    auto to_clear = [&](const Tile &t) { return KIND == kTN && t.terms % kStep != 0 && t.first + t.terms < a.R; };
+    // this CTA's steps of a tile
+    auto first_step = [&](int steps) { return SPLIT > 1 ? steps * part / SPLIT : 0; };
+    auto last_step = [&](int steps) { return SPLIT > 1 ? steps * (part + 1) / SPLIT : steps; };
+    // whether it has the last step of a sum that ends inside it, before the last of all rows (past which the copies bring zeros)
+    auto to_clear = [&](const Tile &t) {
+        return KIND == kTN && t.terms % kStep != 0 && t.first + t.terms < a.R &&
+               (SPLIT == 1 || (last_step(steps_of(t)) == steps_of(t) && first_step(steps_of(t)) < steps_of(t)));
+    };
 
     // A role's warp walks its loop as a whole and only the issuing instructions are one lane's (scaled_gemm.cu).
     // registers: 384 x 168 at launch, redistributed by warpgroup to 104 and 2 x 200 (the same total)
@@ -510,7 +602,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
             // the second operand's columns of this CTA, and how many blocks of 64 of them exist
             const int c0 = t.col0 + rank * P::kHeld, blocks = min(P::kHeld / 64, PAIR ? P::kHeld / 64 : (a.N - c0 + 63) / 64);
             const bool clear = to_clear(t);
-            for (int ks = 0; ks < steps; ++ks) {
+            for (int ks = first_step(steps); ks < last_step(steps); ++ks) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.empty[st]), ph ^ 1, a.wait_limit, abort));
                 if (!ok) {
                     if (leader) fail();
@@ -595,7 +687,8 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
             const uint32_t d = tmem + acc * BN;
             // columns past the last are not multiplied (whole instructions of 16)
             const uint32_t id = idesc_bf16<KIND>(P::kRows, PAIR || DUAL ? BN : min(BN, (a.N - t.col0 + 15) & ~15));
-            for (int ks = 0; ok && ks < steps; ++ks) {
+            const int ks0 = first_step(steps), ks1 = last_step(steps);
+            for (int ks = ks0; ok && ks < ks1; ++ks) {
                 ok = wait(smem_u32(&sh.full[st]), ph);
                 if (PAIR && ok && clear && ks == steps - 1) {
                     ok = wait(smem_u32(&sh.cleared[st]), cph >> st & 1);
@@ -611,7 +704,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                 const int kk = (left + 15) / 16;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * (KIND == kTN ? 128 : 2), bd + j * (KIND == kNT ? 2 : 128), id, ks > 0 || j > 0,
+                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * (KIND == kTN ? 128 : 2), bd + j * (KIND == kNT ? 2 : 128), id, ks > ks0 || j > 0,
                                            leader & (uint32_t)(j < kk));
                 if (leader) {
                     if (PAIR) mma_commit_pair(smem_u32(&sh.empty[st]));
@@ -650,7 +743,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
         uint32_t tph = 0;                                               // a bit a stage
         for (int tile = first_tile; tile < total; tile += stride) {
             const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
-            it += steps_of(t);
+            it += last_step(steps_of(t)) - first_step(steps_of(t));
             if (!to_clear(t)) continue;
             const int st = (it - 1) % P::kStages;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.tail[st]), tph >> st & 1, a.wait_limit, abort))) {
@@ -685,6 +778,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
         // ---- accumulators to outputs: two warps share a quarter of the rows, each with half of the output columns
         constexpr int kCols = P::kOutN / 2;
         const int quad = warp & 3, half = (warp - 4) >> 2;
+        Stage stage{smem + P::kOutAt + (warp - 4) * (P::kOutBytes / 8), 0};
         int acc = 0;
         uint32_t aph = 0;
         for (int tile = first_tile; tile < total; tile += stride) {
@@ -705,20 +799,45 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                     else mbar_arrive(empty);
                 }
             };
-            if (r0 < t.rows && col0 < a.N)
-                finish<KIND, DUAL, kCols>(a, maps, d, d + BN / 2, t.g, t.row0 + r0, t.rows - r0,
-                                          KIND == kTN || t.rows - r0 >= 32 || t.row0 + t.rows == a.R, col0, KIND == kTN && t.terms == 0, lane,
-                                          smem + P::kOutAt + (warp - 4) * (P::kOutBytes / 8), release);
-            else
+            if constexpr (SPLIT > 1) {
+                const bool empty = first_step(steps_of(t)) == last_step(steps_of(t));
+                const uint32_t parts = smem_u32(smem + P::kPartAt) + (quad * 32 + lane) * 16;
+#pragma unroll
+                for (int m = 0; m < P::kMats; ++m) {
+                    float v[kCols];
+                    load_columns(d + m * (BN / 2), v);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < kCols / 4; ++i) {
+                        const int c = half * kCols + 4 * i, to = c / kPartCols, at = c % kPartCols / 4;
+                        const uint32_t p = mapa_u32(parts + ((part * P::kMats + m) * (kPartCols / 4) + at) * 128 * 16, to);
+                        if (empty) st_cluster_v4(p, 0, 0, 0, 0);
+                        else st_cluster_v4(p, __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+                    }
+                }
+                break;                                                // a cluster has one tile at most
+            } else if (r0 < t.rows && col0 < a.N) {
+                finish<KIND, DUAL, kCols, P::kBufs>(a, maps, d, d + BN / 2, t.g, t.row0 + r0, t.rows - r0,
+                                                    KIND == kTN || t.rows - r0 >= 32 || t.row0 + t.rows == a.R, col0, KIND == kTN && t.terms == 0,
+                                                    lane, stage, release);
+            } else {
                 release();
+            }
             if (++acc == 2) {
                 acc = 0;
                 aph ^= 1;
             }
         }
-        if (lane == 0) bulk_wait<0>();                                // what was written through the copy engine is there
+        if (SPLIT == 1 && lane == 0) bulk_wait<0>();                  // what was written through the copy engine is there
     }
     __syncthreads();
+    if constexpr (SPLIT > 1) {
+        cluster_sync();                                               // all CTAs' sums are there
+        if (first_tile < total && !*abort) {
+            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, first_tile, n_tiles);
+            finish_split<KIND, DUAL, kPartCols, SPLIT>(a, reinterpret_cast<const float4 *>(smem + P::kPartAt), t, t.col0 + part * kPartCols);
+        }
+    }
     if (PAIR) {
         cluster_sync();                                               // nothing of the pair is issued any more
         // commits arrive in both CTAs: the last of them, of all products, is there before the second one's shared memory goes
@@ -741,16 +860,57 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
     }
 }
 
-template <int KIND, bool DUAL, int BN, bool PAIR>
+template <int KIND, bool DUAL, int BN, bool PAIR, int SPLIT = 1>
 cudaError_t launch_plan(const ProductArgs &a, const Maps &maps, int ctas, cudaStream_t st)
 {
-    using P = Plan<KIND, DUAL, BN, PAIR>;
-    auto k = product_kernel<KIND, DUAL, BN, PAIR>;
-    static_assert(P::kSmem + sizeof(Shared) <= 227 * 1024, "shared memory");
+    using P = Plan<KIND, DUAL, BN, PAIR, SPLIT>;
+    auto k = product_kernel<KIND, DUAL, BN, PAIR, SPLIT>;
+    static_assert(P::kSmem + sizeof(Shared<KIND>) <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = set_shared(k, P::kSmem, ready);
     if (e != cudaSuccess) return e;
-    return launch_dependent_clusters(k, ctas, PAIR ? 2 : 1, kThreads, P::kSmem, st, a, maps);
+    return launch_dependent_clusters(k, ctas, PAIR ? 2 : SPLIT, kThreads, P::kSmem, st, a, maps);
+}
+// How few tiles of about `steps` steps run: on one CTA each or shared out to S, of 64 columns or (long sums, not DUAL) of 128.
+// us, 1 / 2 / 4 / 8 CTAs a tile: 16 rows x 1024 (16 tiles), K = 512 4.4 / 4.6 / 4.4 / -, 1024 6.2 / 5.4 / 4.9 / -, 2048 9.5 / 7.2 / 5.6 / -, 4096 16.4 /
+// 10.8 / 7.5 / -; 128 rows x 512 (8 tiles), K = 512 4.6 / 5.2 / 4.6 / 4.6, 1024 6.4 / 6.1 / 5.1 / 4.9, 4096 16.4 / 11.3 / 7.7 / 6.1.  Clusters
+// of 8 beyond 64 CTAs do not all find room at once (16 x 1024 x 1024 8.7).  128 columns exchange twice the sums: 301 x 1000 x 1024 6.3 with
+// 64 columns on two CTAs, 7.6 with 128 on four; gradients of 1024 x 512 from 2048 rows 8.7 and 9.2, from 8192 rows 18.4 and 14.8.
+struct Split {
+    int bn, ways;
+};
+template <class Tiles>
+Split split_of(Tiles tiles, bool wide, int steps, int sms)
+{
+    Split best{64, 1};
+    int least = steps;                                     // of a CTA
+    for (int bn = 64; bn <= (wide && steps >= 64 ? 128 : 64); bn *= 2)
+        for (int s = 2; s <= 8; s *= 2) {
+            const long long n = tiles(bn) * s;
+            if (n > (s == 8 ? 64 : s == 4 ? 128 : sms) || steps < (s == 2 ? 10 : s == 4 ? 9 : 16)) continue;
+            if ((steps + s - 1) / s < least) {
+                least = (steps + s - 1) / s;
+                best = Split{bn, s};
+            }
+        }
+    return best;
+}
+template <int KIND, bool DUAL>
+cudaError_t launch_narrow(const ProductArgs &a, const Maps &maps, long long tiles, Split how, int sms, cudaStream_t st)
+{
+    constexpr int kBn = DUAL ? 128 : 64;
+    const int ctas = (int)tiles * how.ways;
+    if (!DUAL && how.bn == 128) {
+        if constexpr (!DUAL) {
+            if (how.ways == 2) return launch_plan<KIND, false, 128, false, 2>(a, maps, ctas, st);
+            if (how.ways == 4) return launch_plan<KIND, false, 128, false, 4>(a, maps, ctas, st);
+            return launch_plan<KIND, false, 128, false, 8>(a, maps, ctas, st);
+        }
+    }
+    if (how.ways == 2) return launch_plan<KIND, DUAL, kBn, false, 2>(a, maps, ctas, st);
+    if (how.ways == 4) return launch_plan<KIND, DUAL, kBn, false, 4>(a, maps, ctas, st);
+    if (how.ways == 8) return launch_plan<KIND, DUAL, kBn, false, 8>(a, maps, ctas, st);
+    return launch_plan<KIND, DUAL, kBn, false>(a, maps, (int)(tiles < sms ? tiles : sms), st);
 }
 
 // Rows of outputs in boxes of 32 x 64 bytes: [rows, cols], or with G > 0 [G, rows, cols].
@@ -781,6 +941,7 @@ struct BiasArgs {
     int R, N, G, f32, accumulate, parts;
 };
 
+constexpr int kRowsAhead = 16;
 __global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__ BiasArgs a)
 {
     __shared__ float part[8][256 + 8];
@@ -806,15 +967,15 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__
     float acc[8] = {};
     if (!bad && col < a.N) {
         const int stride = 8 * a.parts;
-        for (int r = lo + rank * 8 + warp; r < hi; r += 4 * stride) {
-            uint4 v[4];
+        for (int r = lo + rank * 8 + warp; r < hi; r += kRowsAhead * stride) {
+            uint4 v[kRowsAhead];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kRowsAhead; ++i) {
                 v[i] = make_uint4(0, 0, 0, 0);
                 if (r + i * stride < hi) v[i] = *reinterpret_cast<const uint4 *>(a.dy + (size_t)(r + i * stride) * a.N + col);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kRowsAhead; ++i) {
                 const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -877,9 +1038,13 @@ cudaError_t launch_rows_product(const GemmArgs &g, cudaStream_t st)
     const long long pairs = (a.R / 256) * (long long)((a.N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256));
     const bool pair = a.R / a.G >= 256 && pairs >= sms / 2;
     int bn = 256;
+    Split how{64, 1};
     if (!pair) {
-        if (tiles(DUAL ? 64 : 128) <= sms) bn = 128;
-        if (!DUAL && tiles(64) <= sms) bn = 64;
+        if (tiles(DUAL ? 64 : 128) <= sms) {
+            bn = 128;
+            how = split_of(tiles, !DUAL, a.pairs * ((a.K + kStep - 1) / kStep), sms);
+        }
+        if (!DUAL && (how.ways > 1 || tiles(64) <= sms)) bn = how.bn;
     }
     Maps maps{};
     bool ok = true;
@@ -904,10 +1069,10 @@ cudaError_t launch_rows_product(const GemmArgs &g, cudaStream_t st)
     if (pair) return launch_plan<KIND, DUAL, 256, true>(a, maps, sms / 2 * 2, st);
     const long long n = tiles(DUAL ? bn / 2 : bn);
     const int ctas = (int)(n < sms ? n : sms);
-    if (bn == 256) return launch_plan<KIND, DUAL, 256, false>(a, maps, ctas, st);
-    if (bn == 128) return launch_plan<KIND, DUAL, 128, false>(a, maps, ctas, st);
-    if constexpr (!DUAL) return launch_plan<KIND, DUAL, 64, false>(a, maps, ctas, st);
-    return cudaErrorInvalidValue;
+    if (how.ways > 1 || bn == (DUAL ? 128 : 64)) return launch_narrow<KIND, DUAL>(a, maps, n, how, sms, st);
+    if constexpr (!DUAL)
+        if (bn == 128) return launch_plan<KIND, DUAL, 128, false>(a, maps, ctas, st);
+    return launch_plan<KIND, DUAL, 256, false>(a, maps, ctas, st);
 }
 
 }  // namespace
@@ -942,23 +1107,30 @@ cudaError_t launch_wgrad(const WgradArgs &g, cudaStream_t st)
     auto tiles = [&](int rows, int cols) { return (long long)a.G * ((a.M + rows - 1) / rows) * ((a.N + cols - 1) / cols); };
     const bool pair = a.R / a.G >= 256 && tiles(256, 256) >= sms / 2;
     int bn = 256;
+    Split how{64, 1};
     if (!pair) {
-        if (tiles(128, 128) <= sms) bn = 128;
-        if (tiles(128, 64) <= sms) bn = 64;
+        if (tiles(128, 128) <= sms) {
+            bn = 128;
+            how = split_of([&](int cols) { return tiles(128, cols); }, true, (a.R / a.G + kStep - 1) / kStep, sms);
+        }
+        if (how.ways > 1 || tiles(128, 64) <= sms) bn = how.bn;
     }
     Maps maps{};
     if (!map_2d(&maps.a[0], g.dy, a.M, a.R, 64) || !map_2d(&maps.w[0], g.x, a.N, a.R, 64) || !map_out(&maps.y, g.dw, g.f32, a.N, a.M, a.G)) return cudaErrorInvalidValue;
     const long long n = tiles(128, bn);
     const int ctas = (int)(n < sms ? n : sms);
-    const cudaError_t e = pair        ? launch_plan<kTN, false, 256, true>(a, maps, sms / 2 * 2, st)
-                          : bn == 256 ? launch_plan<kTN, false, 256, false>(a, maps, ctas, st)
-                          : bn == 128 ? launch_plan<kTN, false, 128, false>(a, maps, ctas, st)
-                                      : launch_plan<kTN, false, 64, false>(a, maps, ctas, st);
-    if (e != cudaSuccess || !g.db) return e;
-    const long long blocks = (long long)g.G * ((g.N + 255) / 256);
-    const int parts = blocks * 8 <= 2 * sms && g.R / g.G >= 256 ? 8 : 1;
-    const BiasArgs b{g.dy, g.offsets, g.db, g.status, g.R, g.N, g.G, g.f32, g.accumulate, parts};
-    return launch_dependent_clusters(column_sum_kernel, (unsigned)(blocks * parts), parts, 256, 0, st, b);
+    if (g.db) {
+        // first, so that the products find dy in L2
+        const long long blocks = (long long)g.G * ((g.N + 255) / 256);
+        const int parts = blocks * 8 <= 2 * sms && g.R / g.G >= 256 ? 8 : 1;
+        const BiasArgs b{g.dy, g.offsets, g.db, g.status, g.R, g.N, g.G, g.f32, g.accumulate, parts};
+        const cudaError_t e = launch_dependent_clusters(column_sum_kernel, (unsigned)(blocks * parts), parts, 256, 0, st, b);
+        if (e != cudaSuccess) return e;
+    }
+    if (pair) return launch_plan<kTN, false, 256, true>(a, maps, sms / 2 * 2, st);
+    if (how.ways > 1 || bn == 64) return launch_narrow<kTN, false>(a, maps, n, how, sms, st);
+    if (bn == 128) return launch_plan<kTN, false, 128, false>(a, maps, ctas, st);
+    return launch_plan<kTN, false, 256, false>(a, maps, ctas, st);
 }
 
 }  // namespace qmoe
