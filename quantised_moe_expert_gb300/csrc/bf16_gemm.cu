@@ -28,6 +28,7 @@ constexpr int kThreads = 384;
 constexpr int kMaxGroups = 1024;
 constexpr int kStep = 64;                          // terms of a step: 128 bytes of a K-major row
 constexpr int kBlockBytes = 64 * 128;              // an MN-major block: 64 terms x 64 columns
+constexpr int kSliceBytes = 16 * 128;              // one of 16 terms
 enum Kind { kNT, kNN, kTN };
 
 template <int KIND, bool DUAL, int BN, bool PAIR, int SPLIT>
@@ -37,8 +38,9 @@ struct Plan {
     static constexpr int kHeld = PAIR ? BN / 2 : BN;                 // columns of the second operand in this CTA
     static constexpr int kABytes = 128 * 128, kBBytes = kHeld * 128, kStageBytes = kABytes + kBBytes;
     static constexpr int kStages = PAIR ? 6 : BN == 256 ? 4 : BN == 128 ? (SPLIT > 1 ? 4 : 5) : 7;
-    // an epilogue warp's 64-byte pieces of 32 rows: two, where the table of groups leaves room
-    static constexpr int kBufs = KIND != kTN && (PAIR || BN == 256) ? 1 : 2, kOutBytes = SPLIT > 1 ? 0 : 8 * 2048 * kBufs;
+    // an epilogue warp's 32 rows at a time: 128 bytes of each where the table of groups leaves room and a warp has them
+    static constexpr int kRowBytes = (KIND != kTN && (PAIR || BN == 256)) || kOutN == 64 ? 64 : 128;
+    static constexpr int kOutBytes = SPLIT > 1 ? 0 : 8 * 32 * kRowBytes;
     static constexpr int kMats = DUAL ? 2 : 1;
     static constexpr int kPartBytes = SPLIT > 1 ? kMats * kOutN * 128 * 4 : 0;   // all CTAs' sums of them
     static constexpr int kOutAt = kStages * kStageBytes, kPartAt = kOutAt + kOutBytes, kSmem = kPartAt + kPartBytes + 1024;
@@ -47,7 +49,8 @@ struct Plan {
 
 struct Maps {
     CUtensorMap a[2], a32[2], w[2];                  // first operand(s) in whole and in 32-row boxes, second operand(s)
-    CUtensorMap y, pre[2];                           // outputs, in boxes of 32 rows x 64 bytes
+    CUtensorMap a16, w16;                            // TN: both operands in boxes of 16 terms
+    CUtensorMap y, pre[2];                           // outputs, in an epilogue warp's boxes of 32 rows
 };
 
 // What a launch computes.
@@ -59,6 +62,7 @@ struct ProductArgs {
     int *status;
     int R, M, N, K, G;                               // rows; TN: output rows of a matrix; output columns; terms (NT, NN)
     int pairs, act, y_f32, accumulate;
+    int blocks_a, blocks_w;                          // MN-major operands whose maps bring all of a tile's blocks in one copy
     long long wait_limit;
 };
 
@@ -182,9 +186,9 @@ __device__ __forceinline__ Tile tile_at(const ProductArgs &a, const Shared<KIND>
 
 // An MN-major operand in the 128-byte swizzle: blocks of 64 columns (rows of 128 bytes, one term a row), 8 terms 1024 bytes
 // apart (stride byte offset), the next 64 columns a block further (leading byte offset).
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr)
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t block = kBlockBytes)
 {
-    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(kBlockBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(block >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) |
            (2ull << 61);
 }
 // kind::f16 with bf16 operands: D f32 [4,6) = 1, A and B bf16 [7,10), [10,13) = 1, A and B MN-major [15], [16].
@@ -203,45 +207,65 @@ __device__ __forceinline__ void mma_bf16(uint32_t d, uint64_t adesc, uint64_t bd
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(issue), "n"(CG)
         : "memory");
 }
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar)
+// A copy of up to four dimensions; PAIR: completes on a barrier of either CTA of the pair (a cluster address).
+template <bool PAIR>
+__device__ __forceinline__ void load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w, uint32_t bar)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, %3, %4, %5}], "
+            "[%6];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+            : "memory");
+}
+// BLOCKS blocks of 64 columns from column `col` on x TERMS terms from `row` on of matrix g: one copy where the map has the blocks as a
+// dimension, else the first `some` of them one by one.
+template <bool PAIR, int BLOCKS, int TERMS>
+__device__ __forceinline__ void load_blocks(uint32_t dst, const CUtensorMap *map, bool at_once, int some, int col, int row, int g, uint32_t bar)
+{
+    if (at_once) {
+        load_4d<PAIR>(dst, map, 0, row, col / 64, g, bar);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < BLOCKS; ++i)
+        if (i < some) load_4d<PAIR>(dst + i * TERMS * 128, map, col + 64 * i, row, 0, g, bar);
 }
 
 // ------------------------------------------------------------------ epilogue
 
-// 32 rows of 64 bytes, a lane a row in 16-byte chunks, into `stage`: row r's chunk k lies at k ^ r / 2 of the row (the 64-byte
-// swizzle), so that no bank is met twice in a phase.  The copy engine has read what it was last given from there.
-struct Stage {
-    uint8_t *base;
-    int cur;                                         // byte of the buffer that is next
-};
-template <int LEFT>
+// 32 rows of B bytes (64 or 128), a lane a row in 16-byte chunks, into `stage`: row r's chunk k lies at k ^ r / 2 or k ^ r of the
+// row (the 64- and 128-byte swizzles), so that no bank is met twice in a phase.  The copy engine has read what it was last
+// given from there.
+template <int B>
+__device__ __forceinline__ int chunk_at(int r, int k) { return r * B + ((k ^ (B == 64 ? r >> 1 : r)) & (B / 16 - 1)) * 16; }
+template <int B>
 __device__ __forceinline__ void stage_rows(const uint32_t *w, int lane, uint8_t *stage)
 {
-    if (lane == 0) bulk_wait_read<LEFT>();
+    if (lane == 0) bulk_wait_read<0>();
     __syncwarp();
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        *reinterpret_cast<uint4 *>(stage + lane * 64 + ((k ^ (lane >> 1)) & 3) * 16) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    for (int k = 0; k < B / 16; ++k)
+        *reinterpret_cast<uint4 *>(stage + chunk_at<B>(lane, k)) = make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
 }
-// The first `rows` rows and `chunks` chunks of each to rows `pitch` bytes apart from `dst` on: 4 lanes write a row's bytes
+// The first `rows` rows and `chunks` chunks of each to rows `pitch` bytes apart from `dst` on: 4 or 8 lanes write a row's bytes
 // together.  ADD: fp32 values added to what is there.
-template <bool ADD>
-__device__ __forceinline__ void store_staged(uint8_t *dst, size_t pitch, const uint32_t *w, int rows, int chunks, int lane, const Stage &buf)
+template <int B, bool ADD>
+__device__ __forceinline__ void store_staged(uint8_t *dst, size_t pitch, const uint32_t *w, int rows, int chunks, int lane, uint8_t *stage)
 {
-    uint8_t *const stage = buf.base + buf.cur;
-    stage_rows<0>(w, lane, stage);
+    constexpr int kLanes = B / 16;
+    stage_rows<B>(w, lane, stage);
     __syncwarp();
-    const int k = lane & 3;
+    const int k = lane % kLanes;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + lane / 4;
-        uint4 v = *reinterpret_cast<const uint4 *>(stage + r * 64 + ((k ^ (r >> 1)) & 3) * 16);
+    for (int i = 0; i < kLanes; ++i) {
+        const int r = (i * 32 + lane) / kLanes;
+        uint4 v = *reinterpret_cast<const uint4 *>(stage + chunk_at<B>(r, k));
         if (r < rows && k < chunks) {
             uint4 *p = reinterpret_cast<uint4 *>(dst + r * pitch + 16 * k);
             if (ADD) {
@@ -259,12 +283,10 @@ __device__ __forceinline__ void store_staged(uint8_t *dst, size_t pitch, const u
 // The same through the copy engine, which leaves out what lies past the map's last row and column.  A lane of its own row
 // touches 32 lines in every store, and through shared memory and back 64 wavefronts of the load/store unit are needed for 32
 // columns; this way 16 (weight gradients of 64 experts, one step a tile: 5,000 cycles a tile with plain stores).
-template <int KIND, int BUFS>
-__device__ __forceinline__ void store_box(const CUtensorMap *map, int col, int row, int g, const uint32_t *w, int lane, Stage &buf)
+template <int KIND, int B>
+__device__ __forceinline__ void store_box(const CUtensorMap *map, int col, int row, int g, const uint32_t *w, int lane, uint8_t *stage)
 {
-    uint8_t *const stage = buf.base + buf.cur;
-    stage_rows<BUFS - 1>(w, lane, stage);
-    if (BUFS > 1) buf.cur ^= 2048;
+    stage_rows<B>(w, lane, stage);
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
@@ -277,29 +299,27 @@ __device__ __forceinline__ void store_box(const CUtensorMap *map, int col, int r
         bulk_commit();
     }
 }
-// The other way: the lane's row of up to 64 bytes.
-__device__ __forceinline__ void load_staged(uint32_t *w, const uint8_t *src, size_t pitch, int rows, int chunks, int lane, const Stage &buf)
+// The other way: the lane's row of up to B bytes.
+template <int B>
+__device__ __forceinline__ void load_staged(uint32_t *w, const uint8_t *src, size_t pitch, int rows, int chunks, int lane, uint8_t *stage)
 {
-    uint8_t *const stage = buf.base + buf.cur;
-    const int k = lane & 3;
-    uint4 v[4];
+    constexpr int kLanes = B / 16;
+    const int k = lane % kLanes;
+    uint4 v[kLanes];
     if (lane == 0) bulk_wait_read<0>();
     __syncwarp();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + lane / 4;
+    for (int i = 0; i < kLanes; ++i) {
+        const int r = (i * 32 + lane) / kLanes;
         v[i] = make_uint4(0, 0, 0, 0);
         if (r < rows && k < chunks) v[i] = *reinterpret_cast<const uint4 *>(src + r * pitch + 16 * k);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int r = i * 8 + lane / 4;
-        *reinterpret_cast<uint4 *>(stage + r * 64 + ((k ^ (r >> 1)) & 3) * 16) = v[i];
-    }
+    for (int i = 0; i < kLanes; ++i) *reinterpret_cast<uint4 *>(stage + chunk_at<B>((i * 32 + lane) / kLanes, k)) = v[i];
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(stage + lane * 64 + ((j ^ (lane >> 1)) & 3) * 16);
+    for (int j = 0; j < kLanes; ++j) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(stage + chunk_at<B>(lane, j));
         w[4 * j] = u.x;
         w[4 * j + 1] = u.y;
         w[4 * j + 2] = u.z;
@@ -308,11 +328,12 @@ __device__ __forceinline__ void load_staged(uint32_t *w, const uint8_t *src, siz
     __syncwarp();
 }
 
-// Adds the bias of 32 columns (of which `cols` exist) to a row.
+// Adds the bias of N columns (of which `cols` exist) to a row.
+template <int N>
 __device__ __forceinline__ void add_bias(float *v, const uint16_t *bias, int cols)
 {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < N / 8; ++i) {
         if (8 * i >= cols) break;
         const uint4 b = reinterpret_cast<const uint4 *>(bias)[i];
         const uint32_t u[4] = {b.x, b.y, b.z, b.w};
@@ -357,9 +378,9 @@ __device__ __forceinline__ void load_columns(uint32_t d, float (&v)[N])
 // The warp's 32 rows x COLS columns of a tile from the accumulators (second: those of the up products) to the outputs;
 // release() once the accumulators are in registers.  row: the first row's index (TN: in its matrix), of which `rows` exist;
 // whole: no row of another group follows within the 32; empty: a sum without terms.
-template <int KIND, bool DUAL, int COLS, int BUFS, class Release>
+template <int KIND, bool DUAL, int COLS, int B, class Release>
 __device__ __forceinline__ void finish(const ProductArgs &a, const Maps &maps, uint32_t d, uint32_t second, int g, int row, int rows, bool whole,
-                                       int col0, bool empty, int lane, Stage &stage, Release release)
+                                       int col0, bool empty, int lane, uint8_t *stage, Release release)
 {
     const size_t n = a.N;
     float v[COLS], u[DUAL ? COLS : 1];
@@ -372,23 +393,23 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const Maps &maps, u
         for (int i = 0; i < COLS; ++i) v[i] = 0.f;
     }
     const size_t first = KIND == kTN ? (size_t)g * a.M + row : (size_t)row;
-    // 32 bf16 columns from c on of these rows
+    constexpr int kC = B / 2, kF = B / 4;                            // bf16 and fp32 columns of B bytes
     auto put16 = [&](const CUtensorMap *map, uint16_t *out, const float *from, int c, int cols) {
-        uint32_t w[16];
+        uint32_t w[kC / 2];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w[i] = pack_bf16(from[2 * i], from[2 * i + 1]);
-        if (whole) store_box<KIND, BUFS>(map, col0 + c, row, g, w, lane, stage);
-        else store_staged<false>(reinterpret_cast<uint8_t *>(out + first * n + col0 + c), n * 2, w, rows, cols / 8, lane, stage);
+        for (int i = 0; i < kC / 2; ++i) w[i] = pack_bf16(from[2 * i], from[2 * i + 1]);
+        if (whole) store_box<KIND, B>(map, col0 + c, row, g, w, lane, stage);
+        else store_staged<B, false>(reinterpret_cast<uint8_t *>(out + first * n + col0 + c), n * 2, w, rows, cols / 8, lane, stage);
     };
     if (KIND != kTN) {
 #pragma unroll
-        for (int c = 0; c < COLS; c += 32) {
+        for (int c = 0; c < COLS; c += kC) {
             const int cols = a.N - col0 - c;
             if (cols <= 0) break;
-            if (a.bias[0]) add_bias(v + c, a.bias[0] + g * n + col0 + c, cols);
+            if (a.bias[0]) add_bias<kC>(v + c, a.bias[0] + g * n + col0 + c, cols);
             if (a.pre[0]) put16(&maps.pre[0], a.pre[0], v + c, c, cols);
             if constexpr (DUAL) {
-                if (a.bias[1]) add_bias(u + c, a.bias[1] + g * n + col0 + c, cols);
+                if (a.bias[1]) add_bias<kC>(u + c, a.bias[1] + g * n + col0 + c, cols);
                 if (a.pre[1]) put16(&maps.pre[1], a.pre[1], u + c, c, cols);
             }
         }
@@ -399,14 +420,14 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const Maps &maps, u
         }
     }
 #pragma unroll
-    for (int c = 0; c < COLS; c += 32) {
+    for (int c = 0; c < COLS; c += kC) {
         const int cols = a.N - col0 - c;
         if (cols <= 0) break;
         if (KIND != kTN && !DUAL && a.residual) {
-            uint32_t w[16];
-            load_staged(w, reinterpret_cast<const uint8_t *>(a.residual + first * n + col0 + c), n * 2, rows, cols / 8, lane, stage);
+            uint32_t w[kC / 2];
+            load_staged<B>(w, reinterpret_cast<const uint8_t *>(a.residual + first * n + col0 + c), n * 2, rows, cols / 8, lane, stage);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < kC / 2; ++i) {
                 v[c + 2 * i] += bf16_lo(w[i]);
                 v[c + 2 * i + 1] += bf16_hi(w[i]);
             }
@@ -417,15 +438,15 @@ __device__ __forceinline__ void finish(const ProductArgs &a, const Maps &maps, u
         }
         if constexpr (!DUAL) {
 #pragma unroll
-            for (int h = 0; h < 32; h += 16) {
+            for (int h = 0; h < kC; h += kF) {
                 if (h >= cols) break;
-                uint32_t w[16];
+                uint32_t w[kF];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[c + h + i]);
+                for (int i = 0; i < kF; ++i) w[i] = __float_as_uint(v[c + h + i]);
                 uint8_t *y = reinterpret_cast<uint8_t *>(static_cast<float *>(a.y) + first * n + col0 + c + h);
-                if (KIND == kTN && a.accumulate) store_staged<true>(y, n * 4, w, rows, (cols - h) / 4, lane, stage);
-                else if (whole) store_box<KIND, BUFS>(&maps.y, col0 + c + h, row, g, w, lane, stage);
-                else store_staged<false>(y, n * 4, w, rows, (cols - h) / 4, lane, stage);
+                if (KIND == kTN && a.accumulate) store_staged<B, true>(y, n * 4, w, rows, (cols - h) / 4, lane, stage);
+                else if (whole) store_box<KIND, B>(&maps.y, col0 + c + h, row, g, w, lane, stage);
+                else store_staged<B, false>(y, n * 4, w, rows, (cols - h) / 4, lane, stage);
             }
         }
     }
@@ -600,7 +621,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
             const int steps = steps_of(t), row = t.row0 + rank * 128, mine = t.rows - rank * 128;
             const int boxes = mine > 96 || PAIR ? 4 : (mine + 31) / 32;
             // the second operand's columns of this CTA, and how many blocks of 64 of them exist
-            const int c0 = t.col0 + rank * P::kHeld, blocks = min(P::kHeld / 64, PAIR ? P::kHeld / 64 : (a.N - c0 + 63) / 64);
+            const int c0 = t.col0 + rank * P::kHeld, blocks = PAIR || a.blocks_w ? P::kHeld / 64 : min(P::kHeld / 64, (a.N - c0 + 63) / 64);
             const bool clear = to_clear(t);
             for (int ks = first_step(steps); ks < last_step(steps); ++ks) {
                 ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.empty[st]), ph ^ 1, a.wait_limit, abort));
@@ -613,17 +634,19 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                 if (leader) {
                     const uint32_t local = smem_u32(tail ? &sh.tail[st] : &sh.full[st]), bar = PAIR ? mapa_u32(local, tail ? rank : 0) : local;
                     if (KIND == kTN) {
-                        const int r = t.first + ks * kStep;
-                        if (PAIR) {
-                            if (tail) mbar_arrive_expect_tx(local, P::kStageBytes);
-                            else if (rank == 0) mbar_arrive_expect_tx(local, 2 * P::kStageBytes);
-                            for (int i = 0; i < 2; ++i) tma_load_2d_pair(base + i * kBlockBytes, &maps.a[0], row + 64 * i, r, bar);
-                            for (int i = 0; i < P::kHeld / 64; ++i) tma_load_2d_pair(b + i * kBlockBytes, &maps.w[0], c0 + 64 * i, r, bar);
+                        const int r = t.first + ks * kStep, ablocks = a.blocks_a || PAIR || mine > 64 ? 2 : 1;
+                        // the end of a sum in slices of 16 terms: only those that have some
+                        const int slices = (min(t.first + t.terms - r, kStep) + 15) / 16, bytes = (ablocks + blocks) * slices * kSliceBytes;
+                        if (!PAIR || tail) mbar_arrive_expect_tx(local, bytes);
+                        else if (rank == 0) mbar_arrive_expect_tx(local, 2 * bytes);
+                        if (t.first + t.terms - r >= kStep) {
+                            load_blocks<PAIR, 2, kStep>(base, &maps.a[0], a.blocks_a, ablocks, row, r, 0, bar);
+                            load_blocks<PAIR, P::kHeld / 64, kStep>(b, &maps.w[0], a.blocks_w, blocks, c0, r, 0, bar);
                         } else {
-                            const int ablocks = mine > 64 ? 2 : 1;
-                            mbar_arrive_expect_tx(bar, (ablocks + blocks) * kBlockBytes);
-                            for (int i = 0; i < ablocks; ++i) tma_load_2d(base + i * kBlockBytes, &maps.a[0], row + 64 * i, r, bar);
-                            for (int i = 0; i < blocks; ++i) tma_load_2d(b + i * kBlockBytes, &maps.w[0], c0 + 64 * i, r, bar);
+                            for (int j = 0; j < slices; ++j) {
+                                load_blocks<PAIR, 2, 16>(base + j * 2 * kSliceBytes, &maps.a16, a.blocks_a, ablocks, row, r + 16 * j, 0, bar);
+                                load_blocks<PAIR, P::kHeld / 64, 16>(b + j * (P::kHeld / 64) * kSliceBytes, &maps.w16, a.blocks_w, blocks, c0, r + 16 * j, 0, bar);
+                            }
                         }
                     } else {
                         const int pair = ks >= k_steps, k = (pair ? ks - k_steps : ks) * kStep;
@@ -631,14 +654,14 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                         if (PAIR) {
                             if (rank == 0) mbar_arrive_expect_tx(local, 2 * P::kStageBytes);
                             if (KIND == kNN)
-                                for (int i = 0; i < P::kHeld / 64; ++i) tma_load_3d_pair(b + i * kBlockBytes, &maps.w[pair], c0 + 64 * i, k, t.g, bar);
+                                load_blocks<true, P::kHeld / 64, kStep>(b, &maps.w[pair], a.blocks_w, blocks, c0, k, t.g, bar);
                             else
                                 tma_load_2d_pair(b, &maps.w[DUAL ? rank : pair], k, t.g * a.N + (DUAL ? t.col0 : c0), bar);
                             tma_load_2d_pair(base, &maps.a[pair], k, row, bar);
                         } else {
                             mbar_arrive_expect_tx(bar, boxes * 32 * 128 + bbytes);
                             if (KIND == kNN) {
-                                for (int i = 0; i < blocks; ++i) tma_load_3d(b + i * kBlockBytes, &maps.w[pair], c0 + 64 * i, k, t.g, bar);
+                                load_blocks<false, P::kHeld / 64, kStep>(b, &maps.w[pair], a.blocks_w, blocks, c0, k, t.g, bar);
                             } else {
                                 tma_load_2d(b, &maps.w[DUAL ? 0 : pair], k, t.g * a.N + c0, bar);
                                 if (DUAL) tma_load_2d(b + P::kBBytes / 2, &maps.w[1], k, t.g * a.N + c0, bar);
@@ -697,14 +720,21 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t base = smem0 + st * P::kStageBytes;
-                const uint64_t ad = KIND == kTN ? desc_mn(base) : desc_sw128(base);
-                const uint64_t bd = KIND == kNT ? desc_sw128(base + P::kABytes) : desc_mn(base + P::kABytes);
+                uint64_t ad = KIND == kTN ? desc_mn(base) : desc_sw128(base);
+                uint64_t bd = KIND == kNT ? desc_sw128(base + P::kABytes) : desc_mn(base + P::kABytes);
+                uint32_t da = KIND == kTN ? kSliceBytes >> 4 : 2, db = KIND == kNT ? 2 : kSliceBytes >> 4;   // from instruction to instruction
                 // instructions of 16 terms: 32 bytes along K-major rows, 16 rows of MN-major blocks
                 const int left = KIND == kTN ? t.terms - ks * kStep : a.K - (ks >= k_steps ? ks - k_steps : ks) * kStep;
                 const int kk = (left + 15) / 16;
+                if (KIND == kTN && left < kStep) {                    // in slices, a block of 16 terms behind the other
+                    ad = desc_mn(base, kSliceBytes);
+                    bd = desc_mn(base + P::kABytes, kSliceBytes);
+                    da = 2 * kSliceBytes >> 4;
+                    db = (P::kHeld / 64) * kSliceBytes >> 4;
+                }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * (KIND == kTN ? 128 : 2), bd + j * (KIND == kNT ? 2 : 128), id, ks > ks0 || j > 0,
+                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * da, bd + j * db, id, ks > ks0 || j > 0,
                                            leader & (uint32_t)(j < kk));
                 if (leader) {
                     if (PAIR) mma_commit_pair(smem_u32(&sh.empty[st]));
@@ -754,16 +784,19 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                 break;
             }
             tph ^= 1u << st;
-            // rows up to the end of an instruction, 8 lanes a row
-            const int lo = t.terms % kStep, end = (lo + 15) & ~15;
+            // terms up to the end of the last slice, 8 lanes a row
+            const int lo = t.terms % kStep, slice = lo / 16;
             uint8_t *const base = smem + st * P::kStageBytes + lane % 8 * 16;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = lo + lane / 8 + 4 * i;
-                if (r < end) {
+                const int r = lo % 16 + lane / 8 + 4 * i;
+                if (r < 16 && lo % 16) {
 #pragma unroll
-                    for (int block = 0; block < 2 + P::kHeld / 64; ++block)
-                        *reinterpret_cast<uint4 *>(base + block * kBlockBytes + r * 128) = make_uint4(0, 0, 0, 0);
+                    for (int block = 0; block < 2; ++block)
+                        *reinterpret_cast<uint4 *>(base + (slice * 2 + block) * kSliceBytes + r * 128) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int block = 0; block < P::kHeld / 64; ++block)
+                        *reinterpret_cast<uint4 *>(base + P::kABytes + (slice * (P::kHeld / 64) + block) * kSliceBytes + r * 128) = make_uint4(0, 0, 0, 0);
                 }
             }
             fence_proxy_async_smem();
@@ -778,27 +811,18 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
         // ---- accumulators to outputs: two warps share a quarter of the rows, each with half of the output columns
         constexpr int kCols = P::kOutN / 2;
         const int quad = warp & 3, half = (warp - 4) >> 2;
-        Stage stage{smem + P::kOutAt + (warp - 4) * (P::kOutBytes / 8), 0};
-        int acc = 0;
-        uint32_t aph = 0;
-        for (int tile = first_tile; tile < total; tile += stride) {
+        uint8_t *const stage = smem + P::kOutAt + (warp - 4) * (P::kOutBytes / 8);
+        int i = 0;
+        for (int tile = first_tile; tile < total; tile += stride, ++i) {
+            const int acc = i & 1;
             const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
             const int r0 = rank * 128 + quad * 32, col0 = t.col0 + half * kCols;
-            const uint32_t d = tmem + acc * BN + half * kCols + ((uint32_t)(quad * 32) << 16);
-            if (!wait(smem_u32(&sh.acc_full[acc]), aph)) {
+            if (!wait(smem_u32(&sh.acc_full[acc]), i >> 1 & 1)) {
                 if (lane == 0) fail();
                 break;
             }
             tc_fence_after();
-            const uint32_t empty = smem_u32(&sh.acc_empty[acc]);
-            auto release = [&]() {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (PAIR) mbar_arrive_cluster(mapa_u32(empty, 0));
-                    else mbar_arrive(empty);
-                }
-            };
+            const uint32_t d = tmem + acc * BN + half * kCols + ((uint32_t)(quad * 32) << 16);
             if constexpr (SPLIT > 1) {
                 const bool empty = first_step(steps_of(t)) == last_step(steps_of(t));
                 const uint32_t parts = smem_u32(smem + P::kPartAt) + (quad * 32 + lane) * 16;
@@ -808,24 +832,30 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                     load_columns(d + m * (BN / 2), v);
                     tmem_ld_wait();
 #pragma unroll
-                    for (int i = 0; i < kCols / 4; ++i) {
-                        const int c = half * kCols + 4 * i, to = c / kPartCols, at = c % kPartCols / 4;
+                    for (int j = 0; j < kCols / 4; ++j) {
+                        const int c = half * kCols + 4 * j, to = c / kPartCols, at = c % kPartCols / 4;
                         const uint32_t p = mapa_u32(parts + ((part * P::kMats + m) * (kPartCols / 4) + at) * 128 * 16, to);
                         if (empty) st_cluster_v4(p, 0, 0, 0, 0);
-                        else st_cluster_v4(p, __float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]), __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3]));
+                        else st_cluster_v4(p, __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
                     }
                 }
                 break;                                                // a cluster has one tile at most
-            } else if (r0 < t.rows && col0 < a.N) {
-                finish<KIND, DUAL, kCols, P::kBufs>(a, maps, d, d + BN / 2, t.g, t.row0 + r0, t.rows - r0,
-                                                    KIND == kTN || t.rows - r0 >= 32 || t.row0 + t.rows == a.R, col0, KIND == kTN && t.terms == 0,
-                                                    lane, stage, release);
             } else {
-                release();
-            }
-            if (++acc == 2) {
-                acc = 0;
-                aph ^= 1;
+                const uint32_t empty = smem_u32(&sh.acc_empty[acc]);
+                auto release = [&]() {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR) mbar_arrive_cluster(mapa_u32(empty, 0));
+                        else mbar_arrive(empty);
+                    }
+                };
+                if (r0 < t.rows && col0 < a.N)
+                    finish<KIND, DUAL, kCols, P::kRowBytes>(a, maps, d, d + BN / 2, t.g, t.row0 + r0, t.rows - r0,
+                                                            KIND == kTN || t.rows - r0 >= 32 || t.row0 + t.rows == a.R, col0,
+                                                            KIND == kTN && t.terms == 0, lane, stage, release);
+                else
+                    release();
             }
         }
         if (SPLIT == 1 && lane == 0) bulk_wait<0>();                  // what was written through the copy engine is there
@@ -860,10 +890,28 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
     }
 }
 
+// Rows of outputs in boxes of 32 rows x `bytes`: [rows, cols], or with G > 0 [G, rows, cols].
+bool map_out(CUtensorMap *m, void *p, bool f32, uint64_t cols, uint64_t rows, uint64_t G, uint32_t bytes)
+{
+    const CUtensorMapSwizzle swz = bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    const CUtensorMapDataType type = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint32_t size = f32 ? 4 : 2;
+    if (!G) return make_map_2d(m, p, type, size, cols, rows, bytes / size, 32, swz);
+    const uint64_t dims[3] = {cols, rows, G}, strides[2] = {cols * size, cols * rows * size};
+    const uint32_t box[3] = {bytes / size, 32, 1};
+    return make_map_3d(m, p, type, dims, strides, box, swz);
+}
+
 template <int KIND, bool DUAL, int BN, bool PAIR, int SPLIT = 1>
-cudaError_t launch_plan(const ProductArgs &a, const Maps &maps, int ctas, cudaStream_t st)
+cudaError_t launch_plan(const ProductArgs &a, Maps &maps, int ctas, cudaStream_t st)
 {
     using P = Plan<KIND, DUAL, BN, PAIR, SPLIT>;
+    if (SPLIT == 1) {
+        bool ok = map_out(&maps.y, a.y, a.y_f32, a.N, KIND == kTN ? a.M : a.R, KIND == kTN ? a.G : 0, P::kRowBytes);
+        for (int i = 0; i < 2; ++i)
+            if (a.pre[i]) ok = ok && map_out(&maps.pre[i], a.pre[i], false, a.N, a.R, 0, P::kRowBytes);
+        if (!ok) return cudaErrorInvalidValue;
+    }
     auto k = product_kernel<KIND, DUAL, BN, PAIR, SPLIT>;
     static_assert(P::kSmem + sizeof(Shared<KIND>) <= 227 * 1024, "shared memory");
     static std::atomic<uint64_t> ready{0};
@@ -896,7 +944,7 @@ Split split_of(Tiles tiles, bool wide, int steps, int sms)
     return best;
 }
 template <int KIND, bool DUAL>
-cudaError_t launch_narrow(const ProductArgs &a, const Maps &maps, long long tiles, Split how, int sms, cudaStream_t st)
+cudaError_t launch_narrow(const ProductArgs &a, Maps &maps, long long tiles, Split how, int sms, cudaStream_t st)
 {
     constexpr int kBn = DUAL ? 128 : 64;
     const int ctas = (int)tiles * how.ways;
@@ -913,15 +961,24 @@ cudaError_t launch_narrow(const ProductArgs &a, const Maps &maps, long long tile
     return launch_plan<KIND, DUAL, kBn, false>(a, maps, (int)(tiles < sms ? tiles : sms), st);
 }
 
-// Rows of outputs in boxes of 32 x 64 bytes: [rows, cols], or with G > 0 [G, rows, cols].
-bool map_out(CUtensorMap *m, void *p, bool f32, uint64_t cols, uint64_t rows, uint64_t G)
+// An MN-major operand, G matrices [terms, cols], in boxes of `box_terms` x 64 columns, or, where the columns are whole blocks of 64,
+// of `blocks` of those at once: a copy costs its issue about 100 cycles (gradients of 257 groups of 143 rows, 2048 x 512, three steps of
+// six copies a tile: of 3,940 cycles a tile the copies' warp had 2,350 of its own).
+bool map_mn(CUtensorMap *m, const void *p, uint64_t cols, uint64_t terms, uint64_t G, uint32_t box_terms, uint32_t blocks, int *at_once)
 {
-    const CUtensorMapDataType type = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    const uint32_t size = f32 ? 4 : 2;
-    if (!G) return make_map_2d(m, p, type, size, cols, rows, 64 / size, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-    const uint64_t dims[3] = {cols, rows, G}, strides[2] = {cols * size, cols * rows * size};
-    const uint32_t box[3] = {64 / size, 32, 1};
-    return make_map_3d(m, p, type, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_64B);
+    auto fn = tensor_map_encoder();
+    if (!fn) return false;
+    *at_once = cols % 64 == 0;
+    cuuint64_t dims[4] = {cols, terms, 1, G}, strides[3] = {cols * 2, cols * terms * 2, cols * terms * 2};
+    cuuint32_t box[4] = {64, box_terms, 1, 1}, each[4] = {1, 1, 1, 1};
+    if (*at_once) {
+        dims[0] = 64;
+        dims[2] = cols / 64;
+        strides[1] = 128;
+        box[2] = blocks;
+    }
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box, each, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool map_2d(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows, uint32_t box_rows)
@@ -931,8 +988,9 @@ bool map_2d(CUtensorMap *m, const void *p, uint64_t cols, uint64_t rows, uint32_
 
 // ------------------------------------------------------------------ column sums
 
-// db_g (+)= sum over the group's rows of dy: a cluster of C CTAs has 256 columns of one group, each a part of its rows; a warp
-// reads 8 columns a lane of every 8th row.  The parts meet in the first CTA in a fixed order.
+// db_g (+)= sum over the group's rows of dy: a cluster of `parts` CTAs has 256 columns of one group, each a part of its rows; a
+// warp reads 8 columns a lane of every kSumWarps-th row.  The parts meet in the first CTA in a fixed order.  Many warps, since
+// the compiler keeps few of a thread's loads on their way (4096 x 4096 with 8 warps 34 us).
 struct BiasArgs {
     const uint16_t *dy;
     const int32_t *offsets;
@@ -940,11 +998,11 @@ struct BiasArgs {
     int *status;
     int R, N, G, f32, accumulate, parts;
 };
+constexpr int kSumWarps = 32;
 
-constexpr int kRowsAhead = 16;
-__global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__ BiasArgs a)
+__global__ void __launch_bounds__(32 * kSumWarps) column_sum_kernel(const __grid_constant__ BiasArgs a)
 {
-    __shared__ float part[8][256 + 8];
+    __shared__ float part[kSumWarps][256 + 8];
     __shared__ float total[8][256];                        // of each CTA of the cluster, in the first
     pdl_trigger();
     if (a.parts > 1) cluster_arrive();
@@ -955,7 +1013,7 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__
     int lo = 0, hi = a.R;
     if (a.offsets) {
         int b = 0;
-        for (int i = threadIdx.x; i < a.G; i += 256) {
+        for (int i = threadIdx.x; i < a.G; i += 32 * kSumWarps) {
             const int o = a.offsets[i], next = i + 1 < a.G ? a.offsets[i + 1] : a.R;
             b |= o < 0 || o > a.R || next < o;
         }
@@ -966,22 +1024,15 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__
     const int col = n0 + 8 * lane;
     float acc[8] = {};
     if (!bad && col < a.N) {
-        const int stride = 8 * a.parts;
-        for (int r = lo + rank * 8 + warp; r < hi; r += kRowsAhead * stride) {
-            uint4 v[kRowsAhead];
+        const uint16_t *p = a.dy + col;
+#pragma unroll 4
+        for (int r = lo + rank * kSumWarps + warp; r < hi; r += kSumWarps * a.parts) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(p + (size_t)r * a.N);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-            for (int i = 0; i < kRowsAhead; ++i) {
-                v[i] = make_uint4(0, 0, 0, 0);
-                if (r + i * stride < hi) v[i] = *reinterpret_cast<const uint4 *>(a.dy + (size_t)(r + i * stride) * a.N + col);
-            }
-#pragma unroll
-            for (int i = 0; i < kRowsAhead; ++i) {
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    acc[2 * e] += bf16_lo(w[e]);
-                    acc[2 * e + 1] += bf16_hi(w[e]);
-                }
+            for (int e = 0; e < 4; ++e) {
+                acc[2 * e] += bf16_lo(w[e]);
+                acc[2 * e + 1] += bf16_hi(w[e]);
             }
         }
     }
@@ -989,18 +1040,21 @@ __global__ void __launch_bounds__(256) column_sum_kernel(const __grid_constant__
     for (int e = 0; e < 8; ++e) part[warp][8 * lane + e] = acc[e];
     __syncthreads();
     float s = 0.f;
+    if (threadIdx.x < 256) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
+        for (int i = 0; i < kSumWarps; ++i) s += part[i][threadIdx.x];
+    }
     if (a.parts > 1) {
         cluster_wait();                                    // the first CTA is there
-        st_cluster_u32(mapa_u32(smem_u32(&total[rank][threadIdx.x]), 0), __float_as_uint(s));
+        if (threadIdx.x < 256) st_cluster_u32(mapa_u32(smem_u32(&total[rank][threadIdx.x]), 0), __float_as_uint(s));
         cluster_sync();
         if (rank) return;
         s = 0.f;
-        for (int i = 0; i < a.parts; ++i) s += total[i][threadIdx.x];
+        if (threadIdx.x < 256)
+            for (int i = 0; i < a.parts; ++i) s += total[i][threadIdx.x];
     }
     const int c = n0 + threadIdx.x;
-    if (bad || c >= a.N) return;
+    if (bad || threadIdx.x >= 256 || c >= a.N) return;
     const size_t at = (size_t)g * a.N + c;
     if (a.f32) {
         float *p = static_cast<float *>(a.db) + at;
@@ -1055,16 +1109,11 @@ cudaError_t launch_rows_product(const GemmArgs &g, cudaStream_t st)
     }
     for (int i = 0; i < (DUAL ? 2 : g.pairs); ++i) {
         if (KIND == kNN) {
-            const uint64_t dims[3] = {(uint64_t)a.N, (uint64_t)a.K, (uint64_t)a.G}, strides[2] = {(uint64_t)a.N * 2, (uint64_t)a.N * a.K * 2};
-            const uint32_t box[3] = {64, 64, 1};
-            ok = ok && make_map_3d(&maps.w[i], g.w[i], CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_128B);
+            ok = ok && map_mn(&maps.w[i], g.w[i], a.N, a.K, a.G, kStep, pair ? 2 : bn / 64, &a.blocks_w);
         } else {
             ok = ok && map_2d(&maps.w[i], g.w[i], a.K, (uint64_t)a.G * a.N, pair ? 128 : DUAL ? bn / 2 : bn);
         }
     }
-    ok = ok && map_out(&maps.y, g.y, g.y_f32, a.N, a.R, 0);
-    for (int i = 0; i < 2; ++i)
-        if (g.pre[i]) ok = ok && map_out(&maps.pre[i], g.pre[i], false, a.N, a.R, 0);
     if (!ok) return cudaErrorInvalidValue;
     if (pair) return launch_plan<KIND, DUAL, 256, true>(a, maps, sms / 2 * 2, st);
     const long long n = tiles(DUAL ? bn / 2 : bn);
@@ -1116,7 +1165,10 @@ cudaError_t launch_wgrad(const WgradArgs &g, cudaStream_t st)
         if (how.ways > 1 || tiles(128, 64) <= sms) bn = how.bn;
     }
     Maps maps{};
-    if (!map_2d(&maps.a[0], g.dy, a.M, a.R, 64) || !map_2d(&maps.w[0], g.x, a.N, a.R, 64) || !map_out(&maps.y, g.dw, g.f32, a.N, a.M, a.G)) return cudaErrorInvalidValue;
+    const int blocks = pair ? 2 : bn / 64;
+    if (!map_mn(&maps.a[0], g.dy, a.M, a.R, 1, kStep, 2, &a.blocks_a) || !map_mn(&maps.a16, g.dy, a.M, a.R, 1, 16, 2, &a.blocks_a) ||
+        !map_mn(&maps.w[0], g.x, a.N, a.R, 1, kStep, blocks, &a.blocks_w) || !map_mn(&maps.w16, g.x, a.N, a.R, 1, 16, blocks, &a.blocks_w))
+        return cudaErrorInvalidValue;
     const long long n = tiles(128, bn);
     const int ctas = (int)(n < sms ? n : sms);
     if (g.db) {
@@ -1124,7 +1176,7 @@ cudaError_t launch_wgrad(const WgradArgs &g, cudaStream_t st)
         const long long blocks = (long long)g.G * ((g.N + 255) / 256);
         const int parts = blocks * 8 <= 2 * sms && g.R / g.G >= 256 ? 8 : 1;
         const BiasArgs b{g.dy, g.offsets, g.db, g.status, g.R, g.N, g.G, g.f32, g.accumulate, parts};
-        const cudaError_t e = launch_dependent_clusters(column_sum_kernel, (unsigned)(blocks * parts), parts, 256, 0, st, b);
+        const cudaError_t e = launch_dependent_clusters(column_sum_kernel, (unsigned)(blocks * parts), parts, 32 * kSumWarps, 0, st, b);
         if (e != cudaSuccess) return e;
     }
     if (pair) return launch_plan<kTN, false, 256, true>(a, maps, sms / 2 * 2, st);

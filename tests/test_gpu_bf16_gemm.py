@@ -36,6 +36,8 @@ SIZES = [
     ([64], 512, 256), ([129], 136, 328), ([301], 1000, 2184), ([700], 520, 136), ([1500], 768, 192),
     ([0, 3, 0, 130, 1, 0], 200, 136), ([1, 1, 1, 1], 512, 2048), ([40, 0, 0, 257], 72, 64), ([0, 0, 5], 8, 1032),
     ([128, 128, 64], 256, 320), ([300, 500, 1, 700], 512, 264),
+    # widths of whole blocks of 64: a tile that ends inside the blocks of a copy
+    ([50], 64, 64), ([300], 320, 128), ([90, 200], 192, 200), ([20, 700], 576, 192),
     # a tile's steps shared out to 2, 4 and 8 CTAs, of one group and of several
     ([12], 1000, 520), ([140], 520, 1032), ([20], 264, 1096), ([9, 0, 14], 136, 1032), ([30, 90], 1000, 456),
     # pairs of CTAs: row tiles of 256, whole and partial
@@ -144,6 +146,8 @@ def test_gated_pair(ws, counts, I, K, name, biased):
 
 WSIZES = [([1], 8, 8), ([1], 264, 72), ([15], 64, 64), ([64], 128, 256), ([100], 136, 328), ([700], 520, 264), ([0, 3, 0, 130, 1, 0], 200, 136),
           ([17, 16, 1, 64, 65, 128], 256, 512), ([300, 0, 500], 72, 1032), ([2] * 40, 64, 136), ([2000], 384, 256),
+          # widths of whole blocks of 64
+          ([90, 0, 200, 3], 192, 320), ([70], 448, 64), ([20, 700], 200, 576), ([300] * 5, 64, 192),
           # a tile's steps shared out
           ([2000], 64, 72), ([700, 0, 900, 40], 72, 136), ([530], 264, 328), ([1, 515, 510], 200, 264), ([500, 3, 0], 520, 200),
           # pairs of CTAs
