@@ -218,10 +218,22 @@ __device__ __forceinline__ RawRow load_row(const GatedNormArgs &a, int t, int ns
 }
 __device__ __forceinline__ uint32_t word(const uint4 &u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; }
 __device__ __forceinline__ F2 pair_of(const uint4 &u, int i) { return f2(bf16_lo(word(u, i)), bf16_hi(word(u, i))); }
-__device__ __forceinline__ F2 weight_of(const uint16_t *w, const uint4 &raw, int i, F2 offset)
-{
-    return w ? add2(pair_of(raw, i), offset) : f2(1.f, 1.f);
-}
+// A segment of weights with their offset: in fp32 (KEEP, where registers last) or as they were read; ones without weights.
+template <bool KEEP>
+struct Weights {
+    F2 v[KEEP ? 4 : 1], off;
+    uint4 raw;
+    __device__ __forceinline__ Weights(const uint16_t *w, int seg, bool on, float offset)
+    {
+        raw = w && on ? load8(w, seg) : make_uint4(0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u);
+        off = w ? f2(offset, offset) : f2(0.f, 0.f);
+        if (KEEP) {
+#pragma unroll
+            for (int i = 0; i < (KEEP ? 4 : 1); ++i) v[i] = add2(pair_of(raw, i), off);
+        }
+    }
+    __device__ __forceinline__ F2 operator[](int i) const { return KEEP ? v[KEEP ? i : 0] : add2(pair_of(raw, i), off); }
+};
 __device__ __forceinline__ uint32_t pack_pair(F2 v)
 {
     const float2 p = unf2(v);
@@ -258,9 +270,10 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
     const bool want_post = a.dpost_weight != nullptr, want_pre = a.dpre_weight != nullptr;
     const bool want_gate = BY_ELEMENT && a.dgate && a.gate_shape == MOE_GATE_CHANNEL;
     const bool full = BY_ELEMENT && a.dgate && a.gate_shape == MOE_GATE_FULL;
-    const F2 off2 = f2(a.weight_offset, a.weight_offset), scale2 = f2(a.scale, a.scale);
+    const F2 scale2 = f2(a.scale, a.scale);
     const float inv_n = 1.0f / (float)a.n;
-    const uint4 post = on && a.post_weight ? load8(a.post_weight, seg) : zero4(), pre = on && a.pre_weight ? load8(a.pre_weight, seg) : zero4();
+    constexpr bool kKeep = TPR * BLOCKS <= 512;
+    const Weights<kKeep> post(a.post_weight, seg, on, a.weight_offset), pre(a.pre_weight, seg, on, a.weight_offset);
     float4 *const mine = sums + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < 6; ++i) mine[i * TPR] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -278,7 +291,7 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
             for (int i = 0; i < 4; ++i) {
                 const F2 s = pair_of(raw.s, i), x = pair_of(raw.x, i);
                 ss = fma2(s, s, ss);
-                m = fma2(mul2(pair_of(raw.dy, i), weight_of(a.pre_weight, pre, i, off2)), s, m);
+                m = fma2(mul2(pair_of(raw.dy, i), pre[i]), s, m);
                 xx = fma2(x, x, xx);
             }
             v[0] = sum2(ss);
@@ -302,10 +315,10 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
                 const int i = 2 * h + j;
                 const F2 s = pair_of(raw.s, i), dr = mul2(pair_of(raw.dy, i), rs2);
                 F2 d = pair_of(raw.ds, i);
-                if (a.dy) d = fma2(s, ms2, fma2(dr, weight_of(a.pre_weight, pre, i, off2), d));
+                if (a.dy) d = fma2(s, ms2, fma2(dr, pre[i], d));
                 add[1][j] = mul2(dr, s);
                 wd[i] = pack_pair(d);
-                const F2 x = mul2(pair_of(raw.x, i), rx2), b = mul2(x, weight_of(a.post_weight, post, i, off2)), ds = mul2(d, scale2);
+                const F2 x = mul2(pair_of(raw.x, i), rx2), b = mul2(x, post[i]), ds = mul2(d, scale2);
                 if (BY_ELEMENT) {
                     F2 f, slope;
                     gate_pair<ACT>(pair_of(raw.gate, i), f, slope);
@@ -346,7 +359,7 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
         if (a.post_norm) {
             const F2 mean2 = f2(mean * rx, mean * rx);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) e[i] = mul2(fma2(pair_of(raw.x, i), mean2, mul2(e[i], weight_of(a.post_weight, post, i, off2))), rx2);
+            for (int i = 0; i < 4; ++i) e[i] = mul2(fma2(pair_of(raw.x, i), mean2, mul2(e[i], post[i])), rx2);
         }
         if (on) reinterpret_cast<uint4 *>(a.dx)[at] = make_uint4(pack_pair(e[0]), pack_pair(e[1]), pack_pair(e[2]), pack_pair(e[3]));
     }
