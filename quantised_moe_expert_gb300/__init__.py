@@ -667,6 +667,58 @@ class ScaledLayer:
         return cls(host.shape, fmt, router, v, mat(gate, None), mat(up, None), mat(down, h_scale), h_scale)
 
 
+class Experts16:
+    """The experts of a layer in 16 bits, forward and backward: stacks gate, up [G, inter, hidden] and down [G, hidden, inter]
+    (bf16 device tensors), the shared expert's matrices last.
+
+    Routing comes from moe_route and moe_permute (or any that gives the same): inv_perm [T k], offsets of the sorted rows, pick
+    weights p [T, k] and the shared expert's w_shared [T]."""
+
+    def __init__(self, gate, up, down, top_k: int, has_shared: bool, act: int = MOE_ACT_SILU):
+        G, I, H = gate.shape
+        if tuple(up.shape) != (G, I, H) or tuple(down.shape) != (G, H, I):
+            raise MoeError("Experts16", MOE_ERR_INVALID_ARG)
+        self.gate, self.up, self.down = gate, up, down
+        self.n_experts, self.top_k, self.has_shared, self.act = G - int(has_shared), top_k, int(has_shared), act
+
+    def forward(self, x, inv_perm, offsets, p, w_shared, ws, keep: bool = False, stream=None):
+        """y [T, hidden] (bf16), and with keep what backward needs."""
+        (G, I, H), T, k, sh = self.gate.shape, x.shape[0], self.top_k, self.has_shared
+        R = T * (k + sh)
+        new = lambda *n: torch.empty(n, dtype=torch.bfloat16, device=x.device)
+        rows, h, slots, y = new(R, H), new(R, I), new(R, H), new(T, H)
+        g, u = (new(R, I), new(R, I)) if keep else (None, None)
+        moe_dispatch(x, T, H, k, sh, inv_perm, rows, ws, stream)
+        moe_gemm_glu(rows, self.gate, self.up, None, None, self.act, R, I, H, G, offsets, g, u, h, ws, stream)
+        moe_gemm(h, self.down, None, None, 0, R, H, I, G, offsets, None, MOE_ACT_NONE, None, None, slots, ws, stream)
+        moe_weighted_sum(slots, T, H, k, sh, inv_perm, p, w_shared, y, ws, stream)
+        return (y, (rows, g, u, h, slots, inv_perm, offsets, p, w_shared)) if keep else y
+
+    def backward(self, dy, kept, ws, stream=None, dgate=None, dup=None, ddown=None, accumulate: bool = False):
+        """Gradients of x, p, w_shared (None without a shared expert), gate, up and down, from dy [T, hidden] and what
+        forward kept.  dgate, dup, ddown: where to write them (fp32 or bf16, new bf16 tensors by default), or with accumulate
+        where to add them (fp32)."""
+        rows, g, u, h, slots, inv_perm, offsets, p, w_shared = kept
+        (G, I, H), T, k, sh = self.gate.shape, dy.shape[0], self.top_k, self.has_shared
+        R = T * (k + sh)
+        new = lambda *n: torch.empty(n, dtype=torch.bfloat16, device=dy.device)
+        dgate, dup, ddown = (torch.empty_like(m) if d is None else d for d, m in ((dgate, self.gate), (dup, self.up), (ddown, self.down)))
+        dslots, dh, dg, du, dx = new(R, H), new(R, I), new(R, I), new(R, I), new(T, H)
+        dp = torch.empty((T, k), device=dy.device)
+        dw_shared = torch.empty((T,), device=dy.device) if sh else None
+        acc = int(accumulate)
+        moe_weighted_sum_grad(dy, slots, T, H, k, sh, inv_perm, p, w_shared, dslots, dp, dw_shared, ws, stream)
+        moe_gemm_wgrad(dslots, h, R, H, I, G, offsets, acc, ddown, None, ws, stream)
+        moe_gemm(dslots, self.down, None, None, 1, R, I, H, G, offsets, None, MOE_ACT_NONE, None, None, dh, ws, stream)
+        moe_act_grad(self.act, dh, g, u, R, I, dg, du, stream)
+        moe_gemm_wgrad(dg, rows, R, I, H, G, offsets, acc, dgate, None, ws, stream)
+        moe_gemm_wgrad(du, rows, R, I, H, G, offsets, acc, dup, None, ws, stream)
+        # dslots' place serves for the gradient of the rows
+        moe_gemm(dg, self.gate, du, self.up, 1, R, H, I, G, offsets, None, MOE_ACT_NONE, None, None, dslots, ws, stream)
+        moe_weighted_sum(dslots, T, H, k, sh, inv_perm, None, None, dx, ws, stream)
+        return dx, dp, dw_shared, dgate, dup, ddown
+
+
 def calibrate_h_scale(layer: DeviceLayer, x: torch.Tensor, margin: float = 1.0) -> torch.Tensor:
     """The NVFP4 factor of h, the same for every expert (shared expert last), from a batch of tokens: the largest |h| the
     layer computes on x, over all experts, times margin, over 2688."""

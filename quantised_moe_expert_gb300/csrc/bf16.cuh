@@ -116,6 +116,7 @@ struct GatedNormArgs {
     void *dgate;
     float *dpost_weight, *dpre_weight;
     float *partial;                      // workspace: column sums of each block
+    int *status;                         // backward
     int T, n, gate_shape, act, post_norm;
     float scale, weight_offset, eps;
 };

@@ -326,6 +326,7 @@ int moe_gated_norm_grad(const uint16_t *x, const uint16_t *sum, const uint16_t *
     a.dgate = dgate;
     a.dpost_weight = dpost_weight;
     a.dpre_weight = dpre_weight;
+    a.status = static_cast<int *>(ws);
     a.partial = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + MOE_SCALED_WS_BYTES);
     a.T = T;
     a.n = n;

@@ -29,6 +29,10 @@ constexpr int kMaxGroups = 1024;
 constexpr int kStep = 64;                          // terms of a step: 128 bytes of a K-major row
 constexpr int kBlockBytes = 64 * 128;              // an MN-major block: 64 terms x 64 columns
 constexpr int kSliceBytes = 16 * 128;              // one of 16 terms
+// fp32 outputs: steps after which a tile's sums leave tensor memory, to be added up in registers.  The tensor cores' additions do not
+// round to nearest, so that their error grows with the number of terms, not its root (2-norm, 512, 1024, 2048, 4096 and 8192 terms in
+// one go: 4.7e-7, 1.0e-6, 2.1e-6, 2.1e-6, 4.4e-6; fp32 on the other units 1.6e-7 to 9.6e-7).
+constexpr int kSegment = 12;
 enum Kind { kNT, kNN, kTN };
 
 template <int KIND, bool DUAL, int BN, bool PAIR, int SPLIT>
@@ -375,23 +379,27 @@ __device__ __forceinline__ void load_columns(uint32_t d, float (&v)[N])
     }
 }
 
-// The warp's 32 rows x COLS columns of a tile from the accumulators (second: those of the up products) to the outputs;
-// release() once the accumulators are in registers.  row: the first row's index (TN: in its matrix), of which `rows` exist;
-// whole: no row of another group follows within the 32; empty: a sum without terms.
-template <int KIND, bool DUAL, int COLS, int B, class Release>
-__device__ __forceinline__ void finish(const ProductArgs &a, const Maps &maps, uint32_t d, uint32_t second, int g, int row, int rows, bool whole,
-                                       int col0, bool empty, int lane, uint8_t *stage, Release release)
+// Adds N accumulator columns to the sums in registers.
+template <int N>
+__device__ __forceinline__ void add_columns(uint32_t d, float (&v)[N])
+{
+#pragma unroll
+    for (int c = 0; c < N; c += 32) {
+        float w[32];
+        load_columns(d + c, w);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[c + i] += w[i];
+    }
+}
+
+// The warp's 32 rows x COLS columns of a tile (v; u: the up products) to the outputs.  row: the first row's index (TN: in its
+// matrix), of which `rows` exist; whole: no row of another group follows within the 32.
+template <int KIND, bool DUAL, int COLS, int B>
+__device__ __forceinline__ void finish(const ProductArgs &a, const Maps &maps, float (&v)[COLS], float (&u)[DUAL ? COLS : 1], int g, int row, int rows,
+                                       bool whole, int col0, int lane, uint8_t *stage)
 {
     const size_t n = a.N;
-    float v[COLS], u[DUAL ? COLS : 1];
-    load_columns(d, v);
-    if constexpr (DUAL) load_columns(second, u);
-    tmem_ld_wait();
-    release();
-    if (KIND == kTN && empty) {
-#pragma unroll
-        for (int i = 0; i < COLS; ++i) v[i] = 0.f;
-    }
     const size_t first = KIND == kTN ? (size_t)g * a.M + row : (size_t)row;
     constexpr int kC = B / 2, kF = B / 4;                            // bf16 and fp32 columns of B bytes
     auto put16 = [&](const CUtensorMap *map, uint16_t *out, const float *from, int c, int cols) {
@@ -707,11 +715,31 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
             const bool clear = to_clear(t);
             ok = wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1);
             tc_fence_after();
-            const uint32_t d = tmem + acc * BN;
+            uint32_t d = tmem + acc * BN;
             // columns past the last are not multiplied (whole instructions of 16)
             const uint32_t id = idesc_bf16<KIND>(P::kRows, PAIR || DUAL ? BN : min(BN, (a.N - t.col0 + 15) & ~15));
             const int ks0 = first_step(steps), ks1 = last_step(steps);
+            // the accumulators are the epilogue's, and the next ones this warp's
+            auto hand_over = [&]() {
+                if (leader) {
+                    if (PAIR) mma_commit_pair(smem_u32(&sh.acc_full[acc]));
+                    else mma_commit(smem_u32(&sh.acc_full[acc]));
+                }
+                if (++acc == 2) {
+                    acc = 0;
+                    aph ^= 1;
+                }
+            };
+            int fresh = ks0;                                          // the step that starts the sums in the accumulators
             for (int ks = ks0; ok && ks < ks1; ++ks) {
+                if (!DUAL && a.y_f32 && ks - fresh == kSegment) {
+                    hand_over();
+                    ok = wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    d = tmem + acc * BN;
+                    fresh = ks;
+                }
                 ok = wait(smem_u32(&sh.full[st]), ph);
                 if (PAIR && ok && clear && ks == steps - 1) {
                     ok = wait(smem_u32(&sh.cleared[st]), cph >> st & 1);
@@ -734,7 +762,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * da, bd + j * db, id, ks > ks0 || j > 0,
+                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * da, bd + j * db, id, ks > fresh || j > 0,
                                            leader & (uint32_t)(j < kk));
                 if (leader) {
                     if (PAIR) mma_commit_pair(smem_u32(&sh.empty[st]));
@@ -746,14 +774,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                 }
             }
             if (!ok) break;
-            if (leader) {
-                if (PAIR) mma_commit_pair(smem_u32(&sh.acc_full[acc]));
-                else mma_commit(smem_u32(&sh.acc_full[acc]));
-            }
-            if (++acc == 2) {
-                acc = 0;
-                aph ^= 1;
-            }
+            hand_over();
         }
         // the products end before the CTA leaves, whoever gave up
         if (leader) {
@@ -812,50 +833,68 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
         constexpr int kCols = P::kOutN / 2;
         const int quad = warp & 3, half = (warp - 4) >> 2;
         uint8_t *const stage = smem + P::kOutAt + (warp - 4) * (P::kOutBytes / 8);
-        int i = 0;
-        for (int tile = first_tile; tile < total; tile += stride, ++i) {
-            const int acc = i & 1;
+        int acc = 0;
+        uint32_t aph = 0;
+        for (int tile = first_tile; tile < total; tile += stride) {
             const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
             const int r0 = rank * 128 + quad * 32, col0 = t.col0 + half * kCols;
-            if (!wait(smem_u32(&sh.acc_full[acc]), i >> 1 & 1)) {
+            const int steps = last_step(steps_of(t)) - first_step(steps_of(t));
+            const int segments = !DUAL && a.y_f32 ? max(1, (steps + kSegment - 1) / kSegment) : 1;
+            const bool any = r0 < t.rows && (SPLIT > 1 || col0 < a.N);
+            float v[kCols], u[DUAL ? kCols : 1];
+            bool ok = true;
+            for (int seg = 0; seg < segments; ++seg) {
+                ok = wait(smem_u32(&sh.acc_full[acc]), aph);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem + acc * BN + half * kCols + ((uint32_t)(quad * 32) << 16);
+                if (any) {
+                    // to registers before anything is computed from them or stored: free for later products
+                    if (seg) {
+                        add_columns(d, v);
+                    } else {
+                        load_columns(d, v);
+                        if constexpr (DUAL) load_columns(d + BN / 2, u);
+                        tmem_ld_wait();
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    if (PAIR) mbar_arrive_cluster(mapa_u32(smem_u32(&sh.acc_empty[acc]), 0));
+                    else mbar_arrive(smem_u32(&sh.acc_empty[acc]));
+                }
+                if (++acc == 2) {
+                    acc = 0;
+                    aph ^= 1;
+                }
+            }
+            if (!ok) {
                 if (lane == 0) fail();
                 break;
             }
-            tc_fence_after();
-            const uint32_t d = tmem + acc * BN + half * kCols + ((uint32_t)(quad * 32) << 16);
+            if (!any) continue;
+            if (steps == 0) {
+#pragma unroll
+                for (int i = 0; i < kCols; ++i) {
+                    v[i] = 0.f;
+                    if (DUAL) u[DUAL ? i : 0] = 0.f;
+                }
+            }
             if constexpr (SPLIT > 1) {
-                const bool empty = first_step(steps_of(t)) == last_step(steps_of(t));
                 const uint32_t parts = smem_u32(smem + P::kPartAt) + (quad * 32 + lane) * 16;
 #pragma unroll
-                for (int m = 0; m < P::kMats; ++m) {
-                    float v[kCols];
-                    load_columns(d + m * (BN / 2), v);
-                    tmem_ld_wait();
+                for (int m = 0; m < P::kMats; ++m)
 #pragma unroll
                     for (int j = 0; j < kCols / 4; ++j) {
                         const int c = half * kCols + 4 * j, to = c / kPartCols, at = c % kPartCols / 4;
-                        const uint32_t p = mapa_u32(parts + ((part * P::kMats + m) * (kPartCols / 4) + at) * 128 * 16, to);
-                        if (empty) st_cluster_v4(p, 0, 0, 0, 0);
-                        else st_cluster_v4(p, __float_as_uint(v[4 * j]), __float_as_uint(v[4 * j + 1]), __float_as_uint(v[4 * j + 2]), __float_as_uint(v[4 * j + 3]));
+                        const float *const f = m ? u : v;
+                        st_cluster_v4(mapa_u32(parts + ((part * P::kMats + m) * (kPartCols / 4) + at) * 128 * 16, to), __float_as_uint(f[4 * j]),
+                                      __float_as_uint(f[4 * j + 1]), __float_as_uint(f[4 * j + 2]), __float_as_uint(f[4 * j + 3]));
                     }
-                }
-                break;                                                // a cluster has one tile at most
             } else {
-                const uint32_t empty = smem_u32(&sh.acc_empty[acc]);
-                auto release = [&]() {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (PAIR) mbar_arrive_cluster(mapa_u32(empty, 0));
-                        else mbar_arrive(empty);
-                    }
-                };
-                if (r0 < t.rows && col0 < a.N)
-                    finish<KIND, DUAL, kCols, P::kRowBytes>(a, maps, d, d + BN / 2, t.g, t.row0 + r0, t.rows - r0,
-                                                            KIND == kTN || t.rows - r0 >= 32 || t.row0 + t.rows == a.R, col0,
-                                                            KIND == kTN && t.terms == 0, lane, stage, release);
-                else
-                    release();
+                finish<KIND, DUAL, kCols, P::kRowBytes>(a, maps, v, u, t.g, t.row0 + r0, t.rows - r0,
+                                                        KIND == kTN || t.rows - r0 >= 32 || t.row0 + t.rows == a.R, col0, lane, stage);
             }
         }
         if (SPLIT == 1 && lane == 0) bulk_wait<0>();                  // what was written through the copy engine is there

@@ -28,6 +28,8 @@ using tc::pdl_wait;
 
 __device__ __forceinline__ uint4 load8(const uint16_t *p, size_t seg) { return reinterpret_cast<const uint4 *>(p)[seg]; }
 __device__ __forceinline__ uint4 load8_once(const uint16_t *p, size_t seg) { return __ldcs(reinterpret_cast<const uint4 *>(p) + seg); }
+constexpr long long kWaitPolls = 1 << 20;                 // bound of a wait, about a second
+
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0, 0, 0, 0); }
 
 // offset + weight, or ones, of a segment.
@@ -256,17 +258,46 @@ __device__ __forceinline__ void gate_pair(F2 raw, F2 &f, F2 &slope)
     }
 }
 
-// AHEAD: the next row's elements are asked for before this row's are used (where registers last: rows are kept as they were
-// read and widened in each round, and the sums over rows lie in shared memory, each thread's own).
-template <int TPR, int BLOCKS, bool AHEAD, bool BY_ELEMENT, int ACT>
+// A row of the ring: its arrays one behind the other, in the order of RawRow.
+__device__ __forceinline__ uint4 ring8(const uint8_t *row, int which, int nseg, int seg) { return reinterpret_cast<const uint4 *>(row)[which * nseg + seg]; }
+
+// STAGES: rows come through a ring in shared memory, filled by the copy engine that many rows ahead (less one); 0: through
+// registers, the next row's elements on their way under this row's sums, where the ring does not fit or pays nothing.
+// Rows are kept as they were read and widened in each round; the sums over rows lie in shared memory, each thread's own.
+template <int TPR, int BLOCKS, int STAGES, bool BY_ELEMENT, int ACT>
 __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __grid_constant__ GatedNormArgs a)
 {
     extern __shared__ float4 sums[];                           // [post, pre, gate][half of a segment][thread]
     __shared__ float4 buf[2][2][TPR / 32];                     // [row's parity][round]
-    pdl_trigger();
-    pdl_wait();
+    __shared__ uint64_t landed[STAGES ? STAGES : 1];
+    __shared__ int failed;
+    constexpr bool kAhead = STAGES == 0 && TPR < 1024;
     const int nseg = a.n / 8, seg = threadIdx.x;
     const bool on = seg < nseg;
+    pdl_trigger();
+    if (STAGES && threadIdx.x == 0) {
+        for (int i = 0; i < STAGES; ++i) tc::mbar_init(tc::smem_u32(&landed[i]), 1);
+        failed = 0;
+        tc::fence_mbar_init();
+    }
+    if (STAGES) __syncthreads();
+    pdl_wait();
+    uint8_t *const ring = reinterpret_cast<uint8_t *>(sums + 6 * TPR);
+    const uint32_t row_bytes = 2 * a.n;
+    const bool gate_rows = BY_ELEMENT && a.gate_shape == MOE_GATE_FULL;
+    // row t into the ring's place `st` (one thread)
+    auto fetch = [&](int t, int st) {
+        if (t >= a.T) return;
+        const uint32_t bar = tc::smem_u32(&landed[st]), to = tc::smem_u32(ring) + st * 5 * row_bytes;
+        const uint16_t *const src[5] = {a.x, a.sum, a.dy, a.dsum, gate_rows ? a.gate : nullptr};
+        uint32_t arrays = 0;
+        for (int i = 0; i < 5; ++i) arrays += src[i] != nullptr;
+        tc::mbar_arrive_expect_tx(bar, arrays * row_bytes);
+        for (int i = 0; i < 5; ++i)
+            if (src[i]) tc::bulk_load(to + i * row_bytes, src[i] + (size_t)t * a.n, row_bytes, bar);
+    };
+    if (STAGES && threadIdx.x == 0)
+        for (int i = 0; i < STAGES - 1; ++i) fetch(blockIdx.x + i * gridDim.x, i);
     const bool want_post = a.dpost_weight != nullptr, want_pre = a.dpre_weight != nullptr;
     const bool want_gate = BY_ELEMENT && a.dgate && a.gate_shape == MOE_GATE_CHANNEL;
     const bool full = BY_ELEMENT && a.dgate && a.gate_shape == MOE_GATE_FULL;
@@ -277,12 +308,25 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
     float4 *const mine = sums + threadIdx.x;
 #pragma unroll
     for (int i = 0; i < 6; ++i) mine[i * TPR] = make_float4(0.f, 0.f, 0.f, 0.f);
+    const uint4 channel_gate = BY_ELEMENT && !gate_rows && on ? load8(a.gate, seg) : zero4();
     RawRow next;
-    if (AHEAD) next = load_row(a, blockIdx.x, nseg, seg, on);
-    int parity = 0;
-    for (int t = blockIdx.x; t < a.T; t += gridDim.x, parity ^= 1) {
-        const RawRow raw = AHEAD ? next : load_row(a, t, nseg, seg, on);
-        if (AHEAD) next = load_row(a, t + gridDim.x, nseg, seg, on);
+    if (kAhead) next = load_row(a, blockIdx.x, nseg, seg, on);
+    int parity = 0, st = 0, t = blockIdx.x;
+    uint32_t ph = 0;
+    for (; t < a.T; t += gridDim.x, parity ^= 1) {
+        RawRow raw;
+        const uint8_t *const row = ring + st * 5 * row_bytes;
+        if constexpr (STAGES > 0) {
+            // (a wait that runs out is met by all threads behind the next barrier; until then they compute with what is there)
+            if (!tc::mbar_wait(tc::smem_u32(&landed[st]), ph, kWaitPolls, nullptr)) failed = 1;
+            raw.row_gate = a.gate_shape == MOE_GATE_ROW ? bf16_bits_to_float(a.gate[t]) : 0.f;
+            raw.x = on ? ring8(row, 0, nseg, seg) : zero4();
+            raw.s = on ? ring8(row, 1, nseg, seg) : zero4();
+            raw.dy = on && a.dy ? ring8(row, 2, nseg, seg) : zero4();
+        } else {
+            raw = kAhead ? next : load_row(a, t, nseg, seg, on);
+            if (kAhead) next = load_row(a, t + gridDim.x, nseg, seg, on);
+        }
         const size_t at = (size_t)t * nseg + seg;
         float v[3];
         {
@@ -299,6 +343,16 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
             v[2] = sum2(xx);
         }
         row_sums<TPR>(v, buf[parity][0]);
+        if constexpr (STAGES > 0) {
+            // every thread is past the last row: its place is free
+            if (*static_cast<volatile int *>(&failed)) break;
+            if (threadIdx.x == 0) fetch(t + (STAGES - 1) * gridDim.x, st ? st - 1 : STAGES - 1);
+            raw.x = on ? ring8(row, 0, nseg, seg) : zero4();
+            raw.s = on ? ring8(row, 1, nseg, seg) : zero4();
+            raw.dy = on && a.dy ? ring8(row, 2, nseg, seg) : zero4();
+            raw.ds = on && a.dsum ? ring8(row, 3, nseg, seg) : zero4();
+            raw.gate = gate_rows ? (on ? ring8(row, 4, nseg, seg) : zero4()) : channel_gate;
+        }
         const float rx = a.post_norm ? rsqrtf(v[2] * inv_n + a.eps) : 1.0f;
         const float rs = a.dy ? rsqrtf(v[0] * inv_n + a.eps) : 0.0f, ms = -v[1] * inv_n * rs * rs * rs;
         float2 row_f = make_float2(1.f, 0.f);
@@ -357,11 +411,30 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
             mean = -u[0] * inv_n;
         }
         if (a.post_norm) {
+            if (STAGES) raw.x = on ? ring8(row, 0, nseg, seg) : zero4();
             const F2 mean2 = f2(mean * rx, mean * rx);
 #pragma unroll
             for (int i = 0; i < 4; ++i) e[i] = mul2(fma2(pair_of(raw.x, i), mean2, mul2(e[i], post[i])), rx2);
         }
         if (on) reinterpret_cast<uint4 *>(a.dx)[at] = make_uint4(pack_pair(e[0]), pack_pair(e[1]), pack_pair(e[2]), pack_pair(e[3]));
+        if (STAGES && ++st == STAGES) {
+            st = 0;
+            ph ^= 1;
+        }
+    }
+    if (STAGES && failed) {
+        // nothing is left on its way into this block's shared memory: the rows that were asked for, this one first
+        if (threadIdx.x == 0) {
+            record_status(a.status, MOE_ERR_TIMEOUT);
+            for (int i = 0; i < STAGES - 1 && t + i * gridDim.x < a.T; ++i) {
+                tc::mbar_wait(tc::smem_u32(&landed[st]), ph, kWaitPolls, nullptr);
+                if (++st == STAGES) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            }
+        }
+        return;
     }
     if (!on) return;
     float *const out = a.partial + (size_t)blockIdx.x * 3 * a.n + 8 * seg;
@@ -397,8 +470,8 @@ __global__ void __launch_bounds__(1024) gated_norm_sum_kernel(const __grid_const
     if (col < a.n) out[col] = v;
 }
 
-// Threads of a block of the backward pass, and blocks an SM.
-constexpr int kGradPlans[][2] = {{32, 16}, {64, 8}, {128, 4}, {256, 2}, {512, 1}, {640, 1}, {768, 1}, {1024, 1}};
+// Threads of a block of the backward pass, blocks an SM, stages of its ring.
+constexpr int kGradPlans[][3] = {{32, 16, 0}, {64, 8, 0}, {128, 4, 0}, {256, 3, 2}, {512, 1, 4}, {640, 1, 3}, {768, 1, 2}, {1024, 1, 0}};
 int grad_plan(int n)
 {
     int i = 0;
@@ -411,23 +484,23 @@ int grad_blocks(int T, int n)
     const int most = 152 * kGradPlans[grad_plan(n)][1];
     return T < most ? T : most;
 }
-template <int TH, int BL, bool AHEAD, bool BY_ELEMENT, int ACT>
+template <int I, bool BY_ELEMENT, int ACT>
 cudaError_t launch_plan(const GatedNormArgs &a, int blocks, cudaStream_t st)
 {
-    constexpr int kSmem = 6 * 16 * TH;
-    auto k = gated_norm_grad_kernel<TH, BL, AHEAD, BY_ELEMENT, ACT>;
+    constexpr int kThreads = kGradPlans[I][0], kStages = kGradPlans[I][2], kMost = (6 + 5 * kStages) * 16 * kThreads;
+    static_assert(kMost * kGradPlans[I][1] <= 224 * 1024, "shared memory");
+    auto k = gated_norm_grad_kernel<kThreads, kGradPlans[I][1], kStages, BY_ELEMENT, ACT>;
     static std::atomic<uint64_t> ready{0};
-    const cudaError_t e = set_shared(k, kSmem, ready);
-    return e != cudaSuccess ? e : launch_dependent(k, blocks, TH, kSmem, st, a);
+    const cudaError_t e = set_shared(k, kMost, ready);
+    return e != cudaSuccess ? e : launch_dependent(k, blocks, kThreads, 6 * 16 * kThreads + kStages * 10 * a.n, st, a);
 }
-template <int I, bool AHEAD>
+template <int I>
 cudaError_t launch_backward(const GatedNormArgs &a, int blocks, cudaStream_t st)
 {
-    constexpr int kThreads = kGradPlans[I][0], kBlocks = kGradPlans[I][1];
-    if (a.gate_shape < MOE_GATE_CHANNEL) return launch_plan<kThreads, kBlocks, AHEAD, false, MOE_ACT_NONE>(a, blocks, st);
-    if (a.act == MOE_ACT_SILU) return launch_plan<kThreads, kBlocks, AHEAD, true, MOE_ACT_SILU>(a, blocks, st);
-    if (a.act == MOE_ACT_SIGMOID) return launch_plan<kThreads, kBlocks, AHEAD, true, MOE_ACT_SIGMOID>(a, blocks, st);
-    return launch_plan<kThreads, kBlocks, AHEAD, true, MOE_ACT_NONE>(a, blocks, st);
+    if (a.gate_shape < MOE_GATE_CHANNEL) return launch_plan<I, false, MOE_ACT_NONE>(a, blocks, st);
+    if (a.act == MOE_ACT_SILU) return launch_plan<I, true, MOE_ACT_SILU>(a, blocks, st);
+    if (a.act == MOE_ACT_SIGMOID) return launch_plan<I, true, MOE_ACT_SIGMOID>(a, blocks, st);
+    return launch_plan<I, true, MOE_ACT_NONE>(a, blocks, st);
 }
 
 template <int TPR, int CH>
@@ -457,14 +530,14 @@ cudaError_t launch_gated_norm_grad(const GatedNormArgs &a, cudaStream_t st)
     const int blocks = grad_blocks(a.T, a.n);
     cudaError_t e = cudaErrorInvalidValue;
     switch (grad_plan(a.n)) {
-    case 0: e = launch_backward<0, true>(a, blocks, st); break;
-    case 1: e = launch_backward<1, true>(a, blocks, st); break;
-    case 2: e = launch_backward<2, true>(a, blocks, st); break;
-    case 3: e = launch_backward<3, true>(a, blocks, st); break;
-    case 4: e = launch_backward<4, true>(a, blocks, st); break;
-    case 5: e = launch_backward<5, true>(a, blocks, st); break;
-    case 6: e = launch_backward<6, true>(a, blocks, st); break;
-    case 7: e = launch_backward<7, false>(a, blocks, st); break;
+    case 0: e = launch_backward<0>(a, blocks, st); break;
+    case 1: e = launch_backward<1>(a, blocks, st); break;
+    case 2: e = launch_backward<2>(a, blocks, st); break;
+    case 3: e = launch_backward<3>(a, blocks, st); break;
+    case 4: e = launch_backward<4>(a, blocks, st); break;
+    case 5: e = launch_backward<5>(a, blocks, st); break;
+    case 6: e = launch_backward<6>(a, blocks, st); break;
+    case 7: e = launch_backward<7>(a, blocks, st); break;
     }
     if (e != cudaSuccess || !(a.dpost_weight || a.dpre_weight || (a.dgate && a.gate_shape == MOE_GATE_CHANNEL))) return e;
     cudaLaunchConfig_t cfg{};

@@ -277,3 +277,21 @@ def test_same_call_same_bits(ws):
         outs.append((y, dw, db))
     for o in outs[1:]:
         assert all(torch.equal(p, q) for p, q in zip(o, outs[0]))
+
+
+@pytest.mark.parametrize("terms,N,K", [(500, 200, 136), (4096, 1000, 72), (8192, 64, 72), (5000, 2056, 2632), (4100, 264, 1032)])
+def test_fp32_sums(ws, terms, N, K):
+    """Long sums in fp32: the error in the 2-norm stays that of sums of 768 terms.  An addition is truncated by at most 2^-23 of the
+    sum so far, half of that in the mean, and the sums so far are half of the last one in the mean: 768 / 4 times 2^-23 of a sum, if all point
+    one way; the sums of 768 are then rounded as they are added."""
+    dy, x = bf16(terms, N, seed=1), bf16(terms, K, seed=2)
+    want = dy.double().t() @ x.double()
+    dw, y = marked(1, N, K, dtype=torch.float32), marked(N, K, dtype=torch.float32)
+    qm.moe_gemm_wgrad(dy, x, terms, N, K, 1, None, 0, dw, None, ws)
+    outs = [dw[0]]
+    if terms % 8 == 0:
+        qm.moe_gemm(dy.t().contiguous(), x, None, None, 1, N, K, terms, 1, None, None, 0, None, None, y, ws)
+        outs.append(y)
+    most = min(terms, 768) / 4 * 2.0 ** -23 + (terms / 768) ** 0.5 * 2.0 ** -24
+    for got in outs:
+        assert float((got.double() - want).norm() / want.norm()) < most
