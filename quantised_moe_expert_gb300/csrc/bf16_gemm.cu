@@ -41,9 +41,9 @@ struct Plan {
     static constexpr int kRows = PAIR ? 256 : 128;                   // output rows of a tile
     static constexpr int kHeld = PAIR ? BN / 2 : BN;                 // columns of the second operand in this CTA
     static constexpr int kABytes = 128 * 128, kBBytes = kHeld * 128, kStageBytes = kABytes + kBBytes;
-    static constexpr int kStages = PAIR ? 6 : BN == 256 ? 4 : BN == 128 ? (SPLIT > 1 ? 4 : 5) : 7;
+    static constexpr int kStages = PAIR ? 5 : BN == 256 ? 4 : BN == 128 ? (SPLIT > 1 ? 4 : 5) : 7;
     // an epilogue warp's 32 rows at a time: 128 bytes of each where the table of groups leaves room and a warp has them
-    static constexpr int kRowBytes = (KIND != kTN && (PAIR || BN == 256)) || kOutN == 64 ? 64 : 128;
+    static constexpr int kRowBytes = (KIND != kTN && !PAIR && BN == 256) || kOutN == 64 || (DUAL && BN == 256) ? 64 : 128;
     static constexpr int kOutBytes = SPLIT > 1 ? 0 : 8 * 32 * kRowBytes;
     static constexpr int kMats = DUAL ? 2 : 1;
     static constexpr int kPartBytes = SPLIT > 1 ? kMats * kOutN * 128 * 4 : 0;   // all CTAs' sums of them
@@ -842,6 +842,11 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
             const int segments = !DUAL && a.y_f32 ? max(1, (steps + kSegment - 1) / kSegment) : 1;
             const bool any = r0 < t.rows && (SPLIT > 1 || col0 < a.N);
             float v[kCols], u[DUAL ? kCols : 1];
+            if (KIND != kTN && !DUAL && any && a.residual && lane < t.rows - r0) {
+                // on its way to L2 under the products
+                const uint16_t *p = a.residual + (size_t)(t.row0 + r0 + lane) * a.N + col0;
+                for (int c = 0; c < min(kCols, a.N - col0); c += 64) prefetch_l2_line(p + c);
+            }
             bool ok = true;
             for (int seg = 0; seg < segments; ++seg) {
                 ok = wait(smem_u32(&sh.acc_full[acc]), aph);
