@@ -619,72 +619,96 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
     // registers: 384 x 168 at launch, redistributed by warpgroup to 104 and 2 x 200 (the same total)
     if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == 0) {
-        // ---- copies, each CTA its own
+        // ---- copies, each CTA its own.  What a step costs this one warp in instructions delays the copy: the place in the ring is
+        // carried on, whole steps have a loop of their own.
         const bool leader = elect_one();
         int st = 0, issued = 0;
-        uint32_t ph = 0;
+        uint32_t ph = 0, base = smem0;
         bool ok = true;
+        // the next stage, once its last products are done
+        auto acquire = [&]() {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.empty[0]) + 8 * st, ph ^ 1, a.wait_limit, abort));
+            if (!ok && leader) fail();
+            return ok;
+        };
+        auto advance = [&]() {
+            ++issued;
+            base += P::kStageBytes;
+            if (++st == P::kStages) {
+                st = 0;
+                ph ^= 1;
+                base = smem0;
+            }
+        };
+        const uint32_t full0 = PAIR ? mapa_u32(smem_u32(&sh.full[0]), 0) : smem_u32(&sh.full[0]);   // copies complete there
         for (int tile = first_tile; ok && tile < total; tile += stride) {
             const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
-            const int steps = steps_of(t), row = t.row0 + rank * 128, mine = t.rows - rank * 128;
-            const int boxes = mine > 96 || PAIR ? 4 : (mine + 31) / 32;
+            const int steps = steps_of(t), ks0 = first_step(steps), ks1 = last_step(steps), row = t.row0 + rank * 128, mine = t.rows - rank * 128;
             // the second operand's columns of this CTA, and how many blocks of 64 of them exist
             const int c0 = t.col0 + rank * P::kHeld, blocks = PAIR || a.blocks_w ? P::kHeld / 64 : min(P::kHeld / 64, (a.N - c0 + 63) / 64);
-            const bool clear = to_clear(t);
-            for (int ks = first_step(steps); ks < last_step(steps); ++ks) {
-                ok = __all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.empty[st]), ph ^ 1, a.wait_limit, abort));
-                if (!ok) {
-                    if (leader) fail();
-                    break;
+            if constexpr (KIND == kTN) {
+                const int ablocks = a.blocks_a || PAIR || mine > 64 ? 2 : 1, bytes = (ablocks + blocks) * kBlockBytes, whole = min(ks1, t.terms / kStep);
+                int r = t.first + ks0 * kStep;
+#pragma unroll 1
+                for (int ks = ks0; ks < whole; ++ks, r += kStep) {
+                    if (!acquire()) break;
+                    if (leader) {
+                        const uint32_t bar = full0 + 8 * st;
+                        if (!PAIR) mbar_arrive_expect_tx(bar, bytes);
+                        else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[0]) + 8 * st, 2 * P::kStageBytes);
+                        load_blocks<PAIR, 2, kStep>(base, &maps.a[0], a.blocks_a, ablocks, row, r, 0, bar);
+                        load_blocks<PAIR, P::kHeld / 64, kStep>(base + P::kABytes, &maps.w[0], a.blocks_w, blocks, c0, r, 0, bar);
+                    }
+                    advance();
                 }
-                const uint32_t base = smem0 + st * P::kStageBytes, b = base + P::kABytes;
-                const bool tail = clear && ks == steps - 1;
-                if (leader) {
-                    const uint32_t local = smem_u32(tail ? &sh.tail[st] : &sh.full[st]), bar = PAIR ? mapa_u32(local, tail ? rank : 0) : local;
-                    if (KIND == kTN) {
-                        const int r = t.first + ks * kStep, ablocks = a.blocks_a || PAIR || mine > 64 ? 2 : 1;
-                        // the end of a sum in slices of 16 terms: only those that have some
-                        const int slices = (min(t.first + t.terms - r, kStep) + 15) / 16, bytes = (ablocks + blocks) * slices * kSliceBytes;
-                        if (!PAIR || tail) mbar_arrive_expect_tx(local, bytes);
-                        else if (rank == 0) mbar_arrive_expect_tx(local, 2 * bytes);
-                        if (t.first + t.terms - r >= kStep) {
-                            load_blocks<PAIR, 2, kStep>(base, &maps.a[0], a.blocks_a, ablocks, row, r, 0, bar);
-                            load_blocks<PAIR, P::kHeld / 64, kStep>(b, &maps.w[0], a.blocks_w, blocks, c0, r, 0, bar);
-                        } else {
-                            for (int j = 0; j < slices; ++j) {
-                                load_blocks<PAIR, 2, 16>(base + j * 2 * kSliceBytes, &maps.a16, a.blocks_a, ablocks, row, r + 16 * j, 0, bar);
-                                load_blocks<PAIR, P::kHeld / 64, 16>(b + j * (P::kHeld / 64) * kSliceBytes, &maps.w16, a.blocks_w, blocks, c0, r + 16 * j, 0, bar);
-                            }
-                        }
-                    } else {
-                        const int pair = ks >= k_steps, k = (pair ? ks - k_steps : ks) * kStep;
-                        const int bbytes = KIND == kNN ? blocks * kBlockBytes : P::kBBytes;
-                        if (PAIR) {
-                            if (rank == 0) mbar_arrive_expect_tx(local, 2 * P::kStageBytes);
-                            if (KIND == kNN)
-                                load_blocks<true, P::kHeld / 64, kStep>(b, &maps.w[pair], a.blocks_w, blocks, c0, k, t.g, bar);
-                            else
-                                tma_load_2d_pair(b, &maps.w[DUAL ? rank : pair], k, t.g * a.N + (DUAL ? t.col0 : c0), bar);
-                            tma_load_2d_pair(base, &maps.a[pair], k, row, bar);
-                        } else {
-                            mbar_arrive_expect_tx(bar, boxes * 32 * 128 + bbytes);
-                            if (KIND == kNN) {
-                                load_blocks<false, P::kHeld / 64, kStep>(b, &maps.w[pair], a.blocks_w, blocks, c0, k, t.g, bar);
-                            } else {
-                                tma_load_2d(b, &maps.w[DUAL ? 0 : pair], k, t.g * a.N + c0, bar);
-                                if (DUAL) tma_load_2d(b + P::kBBytes / 2, &maps.w[1], k, t.g * a.N + c0, bar);
-                            }
-                            if (boxes == 4)
-                                tma_load_2d(base, &maps.a[pair], k, row, bar);
-                            else
-                                for (int i = 0; i < boxes; ++i) tma_load_2d(base + i * 32 * 128, &maps.a32[pair], k, row + 32 * i, bar);
+                if (ok && ks0 < ks1 && ks1 > whole && acquire()) {
+                    // the end of a sum, in slices of 16 terms: those that have some
+                    if (leader) {
+                        const bool tail = to_clear(t);
+                        const int slices = (t.terms - whole * kStep + 15) / 16, part = (ablocks + blocks) * slices * kSliceBytes;
+                        const uint32_t local = smem_u32(tail ? &sh.tail[st] : &sh.full[st]), bar = PAIR ? mapa_u32(local, tail ? rank : 0) : local;
+                        if (!PAIR || tail) mbar_arrive_expect_tx(local, part);
+                        else if (rank == 0) mbar_arrive_expect_tx(local, 2 * part);
+                        for (int j = 0; j < slices; ++j) {
+                            load_blocks<PAIR, 2, 16>(base + j * 2 * kSliceBytes, &maps.a16, a.blocks_a, ablocks, row, r + 16 * j, 0, bar);
+                            load_blocks<PAIR, P::kHeld / 64, 16>(base + P::kABytes + j * (P::kHeld / 64) * kSliceBytes, &maps.w16, a.blocks_w, blocks, c0,
+                                                                 r + 16 * j, 0, bar);
                         }
                     }
+                    advance();
                 }
-                ++issued;
-                if (++st == P::kStages) {
-                    st = 0;
-                    ph ^= 1;
+            } else {
+                const int boxes = mine > 96 || PAIR ? 4 : (mine + 31) / 32, wrow = t.g * a.N + (PAIR && DUAL ? t.col0 : c0);
+                const int bytes = boxes * 32 * 128 + (KIND == kNN ? blocks * kBlockBytes : P::kBBytes);
+                int pair = ks0 >= k_steps, k = (ks0 - pair * k_steps) * kStep;
+#pragma unroll 1
+                for (int ks = ks0; ks < ks1; ++ks) {
+                    if (!acquire()) break;
+                    if (leader) {
+                        const uint32_t bar = full0 + 8 * st, w = base + P::kABytes;
+                        if (!PAIR) mbar_arrive_expect_tx(bar, bytes);
+                        else if (rank == 0) mbar_arrive_expect_tx(smem_u32(&sh.full[0]) + 8 * st, 2 * P::kStageBytes);
+                        if (KIND == kNN) {
+                            load_blocks<PAIR, P::kHeld / 64, kStep>(w, &maps.w[pair], a.blocks_w, blocks, c0, k, t.g, bar);
+                        } else if (PAIR) {
+                            tma_load_2d_pair(w, &maps.w[DUAL ? rank : pair], k, wrow, bar);
+                        } else {
+                            tma_load_2d(w, &maps.w[DUAL ? 0 : pair], k, wrow, bar);
+                            if (DUAL) tma_load_2d(w + P::kBBytes / 2, &maps.w[1], k, wrow, bar);
+                        }
+                        if (PAIR)
+                            tma_load_2d_pair(base, &maps.a[pair], k, row, bar);
+                        else if (boxes == 4)
+                            tma_load_2d(base, &maps.a[pair], k, row, bar);
+                        else
+                            for (int i = 0; i < boxes; ++i) tma_load_2d(base + i * 32 * 128, &maps.a32[pair], k, row + 32 * i, bar);
+                    }
+                    advance();
+                    k += kStep;
+                    if (ks + 1 == k_steps) {
+                        pair = 1;
+                        k = 0;
+                    }
                 }
             }
         }
@@ -709,69 +733,92 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
         int st = 0, acc = 0;
         uint32_t ph = 0, aph = 0, cph = 0;                              // cph: a bit a stage
         bool ok = true;
+        const uint64_t ad0 = KIND == kTN ? desc_mn(smem0) : desc_sw128(smem0);
+        const uint64_t bd0 = KIND == kNT ? desc_sw128(smem0 + P::kABytes) : desc_mn(smem0 + P::kABytes);
+        constexpr uint32_t kNextA = KIND == kTN ? kSliceBytes >> 4 : 2, kNextB = KIND == kNT ? 2 : kSliceBytes >> 4;   // from instruction to instruction
+        auto commit = [&](uint32_t bar) {
+            if (leader) {
+                if (PAIR) mma_commit_pair(bar);
+                else mma_commit(bar);
+            }
+        };
         for (int tile = first_tile; ok && tile < total; tile += stride) {
             const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
-            const int steps = steps_of(t);
-            const bool clear = to_clear(t);
-            ok = wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1);
-            tc_fence_after();
-            uint32_t d = tmem + acc * BN;
+            const int steps = steps_of(t), ks0 = first_step(steps), ks1 = last_step(steps);
             // columns past the last are not multiplied (whole instructions of 16)
             const uint32_t id = idesc_bf16<KIND>(P::kRows, PAIR || DUAL ? BN : min(BN, (a.N - t.col0 + 15) & ~15));
-            const int ks0 = first_step(steps), ks1 = last_step(steps);
+            ok = wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1);
+            tc_fence_after();
+            uint32_t d = tmem + acc * BN, more = 0;                   // more: there are sums in the accumulators
             // the accumulators are the epilogue's, and the next ones this warp's
             auto hand_over = [&]() {
-                if (leader) {
-                    if (PAIR) mma_commit_pair(smem_u32(&sh.acc_full[acc]));
-                    else mma_commit(smem_u32(&sh.acc_full[acc]));
-                }
+                commit(smem_u32(&sh.acc_full[acc]));
                 if (++acc == 2) {
                     acc = 0;
                     aph ^= 1;
                 }
             };
-            int fresh = ks0;                                          // the step that starts the sums in the accumulators
-            for (int ks = ks0; ok && ks < ks1; ++ks) {
-                if (!DUAL && a.y_f32 && ks - fresh == kSegment) {
+            auto leave_stage = [&]() {
+                commit(smem_u32(&sh.empty[0]) + 8 * st);
+                if (++st == P::kStages) {
+                    st = 0;
+                    ph ^= 1;
+                }
+            };
+            // whole steps
+            const int whole = KIND == kTN ? min(ks1, t.terms / kStep) : ks1;
+            int left = kSegment;
+#pragma unroll 1
+            for (int ks = ks0; ok && ks < whole; ++ks) {
+                if (!DUAL && a.y_f32 && left-- == 0) {
                     hand_over();
                     ok = wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1);
                     if (!ok) break;
                     tc_fence_after();
                     d = tmem + acc * BN;
-                    fresh = ks;
+                    more = 0;
+                    left = kSegment - 1;
                 }
-                ok = wait(smem_u32(&sh.full[st]), ph);
-                if (PAIR && ok && clear && ks == steps - 1) {
+                ok = wait(smem_u32(&sh.full[0]) + 8 * st, ph);
+                if (!ok) break;
+                tc_fence_after();
+                const uint64_t ad = ad0 + st * (P::kStageBytes >> 4), bd = bd0 + st * (P::kStageBytes >> 4);
+                // instructions of 16 terms: 32 bytes along K-major rows, 16 rows of MN-major blocks; the last step of K may have fewer
+                int kk = 4;
+                if (KIND != kTN && (ks + 1 == k_steps || ks + 1 == 2 * k_steps)) kk = (a.K - (k_steps - 1) * kStep + 15) / 16;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * kNextA, bd + j * kNextB, id, more, KIND == kTN ? leader : leader & (uint32_t)(j < kk));
+                    more = 1;
+                }
+                leave_stage();
+            }
+            if (KIND == kTN && ok && ks0 < ks1 && ks1 > whole) {
+                // the end of a sum, in slices of 16 terms, a block of each behind the other
+                if (a.y_f32 && left == 0) {
+                    hand_over();
+                    ok = wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1);
+                    tc_fence_after();
+                    d = tmem + acc * BN;
+                    more = 0;
+                }
+                ok = ok && wait(smem_u32(&sh.full[st]), ph);
+                if (PAIR && ok && to_clear(t)) {
                     ok = wait(smem_u32(&sh.cleared[st]), cph >> st & 1);
                     cph ^= 1u << st;
                 }
                 if (!ok) break;
                 tc_fence_after();
                 const uint32_t base = smem0 + st * P::kStageBytes;
-                uint64_t ad = KIND == kTN ? desc_mn(base) : desc_sw128(base);
-                uint64_t bd = KIND == kNT ? desc_sw128(base + P::kABytes) : desc_mn(base + P::kABytes);
-                uint32_t da = KIND == kTN ? kSliceBytes >> 4 : 2, db = KIND == kNT ? 2 : kSliceBytes >> 4;   // from instruction to instruction
-                // instructions of 16 terms: 32 bytes along K-major rows, 16 rows of MN-major blocks
-                const int left = KIND == kTN ? t.terms - ks * kStep : a.K - (ks >= k_steps ? ks - k_steps : ks) * kStep;
-                const int kk = (left + 15) / 16;
-                if (KIND == kTN && left < kStep) {                    // in slices, a block of 16 terms behind the other
-                    ad = desc_mn(base, kSliceBytes);
-                    bd = desc_mn(base + P::kABytes, kSliceBytes);
-                    da = 2 * kSliceBytes >> 4;
-                    db = (P::kHeld / 64) * kSliceBytes >> 4;
-                }
+                const uint64_t ad = desc_mn(base, kSliceBytes), bd = desc_mn(base + P::kABytes, kSliceBytes);
+                const int slices = (t.terms - whole * kStep + 15) / 16;
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * da, bd + j * db, id, ks > fresh || j > 0,
-                                           leader & (uint32_t)(j < kk));
-                if (leader) {
-                    if (PAIR) mma_commit_pair(smem_u32(&sh.empty[st]));
-                    else mma_commit(smem_u32(&sh.empty[st]));
+                for (int j = 0; j < 4; ++j) {
+                    mma_bf16<PAIR ? 2 : 1>(d, ad + j * (2 * kSliceBytes >> 4), bd + j * ((P::kHeld / 64) * kSliceBytes >> 4), id, more,
+                                           leader & (uint32_t)(j < slices));
+                    more = 1;
                 }
-                if (++st == P::kStages) {
-                    st = 0;
-                    ph ^= 1;
-                }
+                leave_stage();
             }
             if (!ok) break;
             hand_over();
