@@ -144,23 +144,44 @@ __device__ __forceinline__ void build_table(const ProductArgs &a, Shared<KIND> &
     }
 }
 
+// Quotients by a divisor of the launch: floor(2^32 / d) is found once, and an estimate with it is one short at most.  (A tile found
+// with divisions cost each role 1,000 to 1,300 cycles, as much as two steps of products.)
+struct Divisor {
+    uint32_t d, m;
+    __device__ __forceinline__ explicit Divisor(int by) : d((uint32_t)by), m(0xFFFFFFFFu / (uint32_t)by) {}
+    __device__ __forceinline__ int operator()(int x) const
+    {
+        const uint32_t q = __umulhi((uint32_t)x, m);
+        return (int)(q + ((uint32_t)x - q * d >= d));
+    }
+};
+
 // Tile `tile`: kBand row tiles of a column follow each other, then those of the next column, so that what the SMs work on at a
 // time shares rows and columns.
 // (Weight gradients of several groups by rows of tiles: the groups share nothing.)
 constexpr int kBand = 8;
+struct TileShape {
+    Divisor n, band, per;                                    // column tiles; those of a band of rows; TN: row tiles of a matrix
+    __device__ __forceinline__ TileShape(int n_tiles, int row_tiles) : n(n_tiles), band(kBand * n_tiles), per(row_tiles) {}
+};
 template <int KIND, int ROWS, int OUT_N>
-__device__ __forceinline__ Tile tile_at(const ProductArgs &a, const Shared<KIND> &sh, int tile, int n_tiles)
+__device__ __forceinline__ Tile tile_at(const ProductArgs &a, const Shared<KIND> &sh, int tile, const TileShape &shape)
 {
-    const int most = KIND == kTN && a.offsets ? 1 : kBand;
-    const int band = tile / (most * n_tiles), in = tile - band * most * n_tiles, high = min(most, sh.row_tiles - band * most);
-    const int nt = in / high, mt = band * most + in - nt * high;
+    int mt, nt;
+    if (KIND == kTN && a.offsets) {
+        mt = shape.n(tile);
+        nt = tile - mt * (int)shape.n.d;
+    } else {
+        const int band = shape.band(tile), in = tile - band * (int)shape.band.d, high = sh.row_tiles - band * kBand;
+        nt = high >= kBand ? in / kBand : in / high;
+        mt = band * kBand + in - nt * min(high, kBand);
+    }
     Tile t;
     t.col0 = nt * OUT_N;
     t.first = t.terms = 0;
     if (KIND == kTN) {
-        const int per = (a.M + ROWS - 1) / ROWS;
-        t.g = mt / per;
-        t.row0 = (mt - t.g * per) * ROWS;
+        t.g = shape.per(mt);
+        t.row0 = (mt - t.g * (int)shape.per.d) * ROWS;
         t.rows = min(a.M - t.row0, ROWS);
         t.first = a.offsets ? a.offsets[t.g] : 0;
         t.terms = (a.offsets && t.g + 1 < a.G ? a.offsets[t.g + 1] : a.R) - t.first;
@@ -552,6 +573,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
     const int rank = PAIR ? (int)cluster_ctarank() : 0, part = SPLIT > 1 ? (int)cluster_ctarank() : 0;
     const int first_tile = blockIdx.x / kCluster, stride = gridDim.x / kCluster;
     const int n_tiles = (a.N + P::kOutN - 1) / P::kOutN, k_steps = (a.K + kStep - 1) / kStep;
+    const TileShape shape(n_tiles, KIND == kTN ? (a.M + P::kRows - 1) / P::kRows : 1);
 
     pdl_trigger();
     if (threadIdx.x == 0) {
@@ -642,7 +664,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
         };
         const uint32_t full0 = PAIR ? mapa_u32(smem_u32(&sh.full[0]), 0) : smem_u32(&sh.full[0]);   // copies complete there
         for (int tile = first_tile; ok && tile < total; tile += stride) {
-            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
+            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, shape);
             const int steps = steps_of(t), ks0 = first_step(steps), ks1 = last_step(steps), row = t.row0 + rank * 128, mine = t.rows - rank * 128;
             // the second operand's columns of this CTA, and how many blocks of 64 of them exist
             const int c0 = t.col0 + rank * P::kHeld, blocks = PAIR || a.blocks_w ? P::kHeld / 64 : min(P::kHeld / 64, (a.N - c0 + 63) / 64);
@@ -743,7 +765,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
             }
         };
         for (int tile = first_tile; ok && tile < total; tile += stride) {
-            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
+            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, shape);
             const int steps = steps_of(t), ks0 = first_step(steps), ks1 = last_step(steps);
             // columns past the last are not multiplied (whole instructions of 16)
             const uint32_t id = idesc_bf16<KIND>(P::kRows, PAIR || DUAL ? BN : min(BN, (a.N - t.col0 + 15) & ~15));
@@ -840,10 +862,10 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
         int it = 0;
         uint32_t tph = 0;                                               // a bit a stage
         for (int tile = first_tile; tile < total; tile += stride) {
-            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
+            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, shape);
             it += last_step(steps_of(t)) - first_step(steps_of(t));
             if (!to_clear(t)) continue;
-            const int st = (it - 1) % P::kStages;
+            const int st = (int)((uint32_t)(it - 1) % P::kStages);
             if (!__all_sync(0xFFFFFFFFu, mbar_wait(smem_u32(&sh.tail[st]), tph >> st & 1, a.wait_limit, abort))) {
                 if (lane == 0) {
                     fail();
@@ -883,7 +905,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
         int acc = 0;
         uint32_t aph = 0;
         for (int tile = first_tile; tile < total; tile += stride) {
-            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, n_tiles);
+            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, shape);
             const int r0 = rank * 128 + quad * 32, col0 = t.col0 + half * kCols;
             const int steps = last_step(steps_of(t)) - first_step(steps_of(t));
             const int segments = !DUAL && a.y_f32 ? max(1, (steps + kSegment - 1) / kSegment) : 1;
@@ -955,7 +977,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
     if constexpr (SPLIT > 1) {
         cluster_sync();                                               // all CTAs' sums are there
         if (first_tile < total && !*abort) {
-            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, first_tile, n_tiles);
+            const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, first_tile, shape);
             finish_split<KIND, DUAL, kPartCols, SPLIT>(a, reinterpret_cast<const float4 *>(smem + P::kPartAt), t, t.col0 + part * kPartCols);
         }
     }
