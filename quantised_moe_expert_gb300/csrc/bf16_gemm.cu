@@ -158,7 +158,8 @@ struct Divisor {
 
 // Tile `tile`: kBand row tiles of a column follow each other, then those of the next column, so that what the SMs work on at a
 // time shares rows and columns.
-// (Weight gradients of several groups by rows of tiles: the groups share nothing.)
+// (Weight gradients of several groups by rows of tiles: the groups share nothing, and those worked on at a time are few; runs of tiles of
+// equal cost for each CTA, or the tiles of a shared expert with all tokens first, were 138 to 195 us and no better where this takes 122 and 140.)
 constexpr int kBand = 8;
 struct TileShape {
     Divisor n, band, per;                                    // column tiles; those of a band of rows; TN: row tiles of a matrix
@@ -1203,15 +1204,25 @@ cudaError_t launch_rows_product(const GemmArgs &g, cudaStream_t st)
     };
     auto tiles = [&](int out_n) { return row_tiles(128) * ((a.N + out_n - 1) / out_n); };
     const long long pairs = (a.R / 256) * (long long)((a.N + (DUAL ? 127 : 255)) / (DUAL ? 128 : 256));
-    const bool pair = a.R / a.G >= 256 && pairs >= sms / 2;
+    // A pair of CTAs a tile: groups of 512 rows on average, a tile for every pair, and long sums or several tiles for each.  us, one CTA / a
+    // pair: rows x N x K 4096 x 2048 x 512 10.3 / 11.6, x 1024 15.2 / 16.4, x 2048 24.8 / 25.0, x 4096 49.2 / 45.8; 16384 x 2048 x 512 (512
+    // tiles) 30.2 / 28.1, x 1024 51.5 / 46.1; 1024 x 8192 x 8192 93.9 / 87.3; 64 groups of 256 x 2048 x 512 39.5 / 40.5, of 384 54.2 / 60.6,
+    // of 512 x 512 x 2048 66.7 / 63.8 (gated pairs 66.0 / 71.5, 87.5 / 121.9, 103.9 / 93.1).
+    const bool pair = a.R / a.G >= 512 && pairs >= sms / 2 && ((long long)a.K * a.pairs >= 2048 || pairs >= 3 * sms / 2);
     int bn = 256;
+    // Else the widest tiles, or the narrowest of which there is about one an SM (groups of fewer rows than a tile have one row tile each).  us at
+    // 64 / 128 / 256 columns: 512 rows x 2048 x 1024 (128, 64, 32 tiles) 7.5 / 7.6 / 9.6, x 4096 (256, 128, 64) 11.6 / 8.2 / 10.2, x 8192
+    // (512, 256, 128) 19.2 / 12.3 / 10.2; 16 groups of 100 x 1024 x 1024 (256, 128, 64) 13.0 / 10.3 / 12.4; 64 of 3 x 1032 x 264 (1088, 576, 320) 17.1 /
+    // 12.2 / 13.6, x 512 x 2048 (512, 256, 128) 35.5 / 27.9 / 27.9.
+    const long long likely = a.offsets && a.R / a.G < 128 ? (a.G < a.R ? a.G : a.R) : row_tiles(128);
+    auto about = [&](int out_n) { return likely * ((a.N + out_n - 1) / out_n); };
     Split how{64, 1};
     if (!pair) {
-        if (tiles(DUAL ? 64 : 128) <= sms) {
+        if (about(DUAL ? 64 : 128) <= sms) {
             bn = 128;
             how = split_of(tiles, !DUAL, a.pairs * ((a.K + kStep - 1) / kStep), sms);
         }
-        if (!DUAL && (how.ways > 1 || tiles(64) <= sms)) bn = how.bn;
+        if (!DUAL && (how.ways > 1 || about(64) <= sms)) bn = how.bn;
     }
     Maps maps{};
     bool ok = true;
@@ -1267,7 +1278,10 @@ cudaError_t launch_wgrad(const WgradArgs &g, cudaStream_t st)
     a.wait_limit = g.wait_limit;
     const int sms = device_sm_count();
     auto tiles = [&](int rows, int cols) { return (long long)a.G * ((a.M + rows - 1) / rows) * ((a.N + cols - 1) / cols); };
-    const bool pair = a.R / a.G >= 256 && tiles(256, 256) >= sms / 2;
+    // A pair of CTAs a tile from 384 rows a group on, where there is a tile for every pair.  us, one CTA / a pair, 2048 x 512: 64 groups of 256
+    // rows 43 / 54, of 384 56 / 56, of 512 69 / 61, of 1024 111 / 102, 16 of 4096 106 / 101; 4096 x 4096 from 512 rows 18.0 / 16.4, from
+    // 4096 91 / 86.
+    const bool pair = a.R / a.G >= 384 && tiles(256, 256) >= sms / 2;
     int bn = 256;
     Split how{64, 1};
     if (!pair) {
