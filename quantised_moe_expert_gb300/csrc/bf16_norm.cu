@@ -11,11 +11,14 @@
 //   e = scale f(gate) D,  dx = rx (e w' - x^ mean(e w' x^))       (dx = e without post_norm)
 //   dpre_weight = sum_t dy s^,  dpost_weight = sum_t e x^
 //
-// Bound: bytes.  A thread keeps CH segments of 8 elements of a row in registers from the one read to the write; sums over
-// the row go through shuffles and shared memory.  Backward, a block walks over every gridDim-th row: the next row's
-// elements are on their way under this one's sums, which meet in two rounds (everything that needs only the inputs, then what
-// needs D); the sums over rows of a thread's columns stay in registers, are written as one row of the workspace, and a
-// second launch adds those up in a fixed order.
+// Bound: bytes, then instructions.  Forward, a thread keeps CH segments of 8 elements of a row in registers from the one read to
+// the write; sums over the row go through shuffles and shared memory.  Backward, a block walks over every gridDim-th
+// row: its next rows are on their way (by the copy engine, into a ring) under this one's sums, which meet in two rounds
+// (everything that needs only the inputs, then what needs D); the sums over rows of a thread's columns lie in shared memory, are
+// written as one row of the workspace, and a second launch adds those up in a fixed order.
+// Measured: forward of 16384 x 2048 with a gate per element 59 us (336 MB, 5.7 TB/s; one row a block of 256 threads 86), one row 1.9 us behind
+// another launch; backward of the same 97 us (537 MB, 5.5 TB/s, 64% of the issue slots; 205 with a barrier for each sum and values one by
+// one, 123 with rows through registers), of 777 x 5120 with a gate per channel 23 us, of which the sums over blocks are 5.
 #include "bf16.cuh"
 #include "f32x2.cuh"
 #include "tc_ptx.cuh"

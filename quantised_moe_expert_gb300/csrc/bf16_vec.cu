@@ -9,6 +9,10 @@
 // The products are m16n8k16: 16 weight rows against up to 8 rows of activations, so that a group's rows share one
 // read of its weights.  The order of the terms is free as long as both operands share it: a lane's 16 bytes of a row serve two
 // instructions as they are, and nothing is rearranged.
+//
+// 1 x 4096 x 2048: 3.6 us from L2, 4.9 from HBM (3.4 TB/s), against 10.4 of tiles; one token's gated pair of 9 experts (hidden 2048, inter 512)
+// 7.7 us, its down products 3.9, against 11.8 and 6.8.  1.9 us are launch to launch, 0.4 the search for a chunk of rows.  fp32
+// multiply-adds in place of the instructions, two weight rows a warp: 4.4 us, and 10.2 and 8.0.
 #include "bf16.cuh"
 #include "tc_ptx.cuh"
 
