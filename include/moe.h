@@ -497,7 +497,7 @@ enum moe_activation {
  *   a2, w2       a second pair of the same sizes (both or neither): the input gradient
  *                of a gate/up pair in one sum
  *   bias         [G, N] or NULL
- *   residual     [R, N] or NULL; may be y itself
+ *   residual     [R, N] or NULL; may be y itself (bf16)
  *   pre_out      [R, N] or NULL: pre, rounded, as moe_act_grad takes it
  *   y            [R, N], fp32 with y_f32 = 1
  * N, K: multiples of 8, K at most 65536, N at most 2^20; G <= 1024; R <= 2^21.

@@ -297,3 +297,35 @@ def test_fp32_sums(ws, terms, N, K):
     most = min(terms, 768) / 4 * 2.0 ** -23 + (terms / 768) ** 0.5 * 2.0 ** -24
     for got in outs:
         assert float((got.double() - want).norm() / want.norm()) < most
+
+
+def test_past_32_bits(ws):
+    """Outputs of more than 2^31 elements: the last rows, columns and matrices are where they belong (exact: small whole numbers)."""
+    R, N, K = (1 << 17) + 3, 16392, 8
+    a = torch.zeros(R, K, dtype=torch.bfloat16, device="cuda")
+    a[:, 0] = (torch.arange(R, device="cuda") % 251).bfloat16()
+    w = torch.zeros(1, N, K, dtype=torch.bfloat16, device="cuda")
+    w[0, :, 0] = (torch.arange(N, device="cuda") % 5 - 2).bfloat16()
+    y = torch.empty(R, N, dtype=torch.bfloat16, device="cuda")
+    assert y.numel() > 1 << 31
+    want = lambda r: (a[r, 0].float()[:, None] * w[0, :, 0].float()).bfloat16()
+    for transposed in (0, 1):
+        y.fill_(MARK)
+        qm.moe_gemm(a, w.transpose(1, 2).contiguous() if transposed else w, None, None, transposed, R, N, K, 1, None, None, 0, None, None, y, ws)
+        for r in (slice(0, 5), slice(R // 2, R // 2 + 5), slice(R - 200, R)):
+            assert torch.equal(y[r], want(r))
+    d = torch.empty(R, N, dtype=torch.bfloat16, device="cuda")
+    qm.moe_act_grad(qm.MOE_ACT_NONE, y, y, None, R, N, d, None)
+    assert torch.equal(d[-200:], y[-200:])
+    del d
+    # gradients of many matrices
+    G, N, K = 520, 2048, 2056
+    off = torch.arange(G, dtype=torch.int32, device="cuda")
+    dy, x = torch.zeros(G, N, dtype=torch.bfloat16, device="cuda"), torch.ones(G, K, dtype=torch.bfloat16, device="cuda")
+    dy[:] = (torch.arange(G, device="cuda") % 200).bfloat16()[:, None]
+    del y
+    dw = torch.empty(G, N, K, dtype=torch.bfloat16, device="cuda")
+    assert dw.numel() > 1 << 31
+    qm.moe_gemm_wgrad(dy, x, G, N, K, G, off, 0, dw, None, ws)
+    for g in (0, 255, 511, G - 1):
+        assert bool((dw[g] == g % 200).all())
