@@ -65,10 +65,11 @@ __device__ __forceinline__ void gate_values(int act, uint4 raw, F2 (&f)[4])
     }
 }
 
-// Sums of N values over the TPR threads of a row; buf: a float4 a warp that no thread still reads.  Every thread of the
-// block takes part.  Four values share their first two exchanges (each lane goes on with one of them): 6 shuffles in place of 20.
+// Sums of N values over the TPR threads of a row, and with `more` of one more; buf, more_buf: a float4 a warp that no thread
+// still reads.  Every thread of the block takes part.  Four values share their first two exchanges (each lane goes on with
+// one of them): 6 shuffles in place of 20.
 template <int TPR, int N>
-__device__ __forceinline__ void row_sums(float (&v)[N], float4 *buf)
+__device__ __forceinline__ void row_sums(float (&v)[N], float4 *buf, float *more = nullptr, float4 *more_buf = nullptr)
 {
     static_assert(N <= 4, "a float4 a warp");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, w0 = w / (TPR / 32) * (TPR / 32);
@@ -94,11 +95,18 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float4 *buf)
         if (TPR == 32) return;
         if (lane == 0) buf[w].x = v[0];
     }
+    if (more) {
+#pragma unroll
+        for (int o = 16; o; o >>= 1) *more += __shfl_xor_sync(0xFFFFFFFFu, *more, o);
+        if (lane == 0) more_buf[w].x = *more;
+        *more = 0.f;
+    }
     __syncthreads();
     F2 lo = f2(0.f, 0.f), hi = lo;
     float one = 0.f;
 #pragma unroll 8
     for (int j = 0; j < TPR / 32; ++j) {
+        if (more) *more += more_buf[w0 + j].x;
         if (N == 1) {
             one += buf[w0 + j].x;
         } else if (N == 2) {
@@ -274,7 +282,7 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
     __shared__ float4 buf[2][2][TPR / 32];                     // [row's parity][round]
     __shared__ uint64_t landed[STAGES ? STAGES : 1];
     __shared__ int failed;
-    constexpr bool kAhead = STAGES == 0 && TPR < 1024;
+    constexpr bool kAhead = STAGES == 0 && TPR < 1024, kJoint = STAGES > 0;
     const int nseg = a.n / 8, seg = threadIdx.x;
     const bool on = seg < nseg;
     pdl_trigger();
@@ -285,22 +293,23 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
     }
     if (STAGES) __syncthreads();
     pdl_wait();
-    uint8_t *const ring = reinterpret_cast<uint8_t *>(sums + 6 * TPR);
     const uint32_t row_bytes = 2 * a.n;
+    uint8_t *const ring_x = reinterpret_cast<uint8_t *>(sums + 6 * TPR), *const ring = ring_x + (STAGES + 1) * row_bytes;
     const bool gate_rows = BY_ELEMENT && a.gate_shape == MOE_GATE_FULL;
-    // row t into the ring's place `st` (one thread)
-    auto fetch = [&](int t, int st) {
+    // row t into the rings' places `st` and `sx` (one thread)
+    auto fetch = [&](int t, int st, int sx) {
         if (t >= a.T) return;
-        const uint32_t bar = tc::smem_u32(&landed[st]), to = tc::smem_u32(ring) + st * 5 * row_bytes;
-        const uint16_t *const src[5] = {a.x, a.sum, a.dy, a.dsum, gate_rows ? a.gate : nullptr};
-        uint32_t arrays = 0;
-        for (int i = 0; i < 5; ++i) arrays += src[i] != nullptr;
+        const uint32_t bar = tc::smem_u32(&landed[st]), to = tc::smem_u32(ring) + st * 4 * row_bytes;
+        const uint16_t *const src[4] = {a.sum, a.dy, a.dsum, gate_rows ? a.gate : nullptr};
+        uint32_t arrays = 1;
+        for (int i = 0; i < 4; ++i) arrays += src[i] != nullptr;
         tc::mbar_arrive_expect_tx(bar, arrays * row_bytes);
-        for (int i = 0; i < 5; ++i)
+        tc::bulk_load(tc::smem_u32(ring_x) + sx * row_bytes, a.x + (size_t)t * a.n, row_bytes, bar);
+        for (int i = 0; i < 4; ++i)
             if (src[i]) tc::bulk_load(to + i * row_bytes, src[i] + (size_t)t * a.n, row_bytes, bar);
     };
     if (STAGES && threadIdx.x == 0)
-        for (int i = 0; i < STAGES - 1; ++i) fetch(blockIdx.x + i * gridDim.x, i);
+        for (int i = 0; i < STAGES; ++i) fetch(blockIdx.x + i * gridDim.x, i, i);
     const bool want_post = a.dpost_weight != nullptr, want_pre = a.dpre_weight != nullptr;
     const bool want_gate = BY_ELEMENT && a.dgate && a.gate_shape == MOE_GATE_CHANNEL;
     const bool full = BY_ELEMENT && a.dgate && a.gate_shape == MOE_GATE_FULL;
@@ -314,48 +323,59 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
     const uint4 channel_gate = BY_ELEMENT && !gate_rows && on ? load8(a.gate, seg) : zero4();
     RawRow next;
     if (kAhead) next = load_row(a, blockIdx.x, nseg, seg, on);
-    int parity = 0, st = 0, t = blockIdx.x;
+    int parity = 0, st = 0, sx = 0, t = blockIdx.x;
     uint32_t ph = 0;
-    for (; t < a.T; t += gridDim.x, parity ^= 1) {
+    // (a wait that runs out is met by all threads behind the next barrier; until then they compute with what is there)
+    auto await = [&](int at, uint32_t phase) {
+        if (!tc::mbar_wait(tc::smem_u32(&landed[at]), phase, kWaitPolls, nullptr)) failed = 1;
+    };
+    auto from_ring = [&](RawRow &r, int at, int at_x) {
+        const uint8_t *const row = ring + at * 4 * row_bytes;
+        r.x = on ? ring8(ring_x, at_x, nseg, seg) : zero4();
+        r.s = on ? ring8(row, 0, nseg, seg) : zero4();
+        r.dy = on && a.dy ? ring8(row, 1, nseg, seg) : zero4();
+    };
+    auto row_gate_of = [&](int row) { return !BY_ELEMENT && a.gate_shape == MOE_GATE_ROW && row < a.T ? bf16_bits_to_float(a.gate[row]) : 0.f; };
+    // a thread's part of what needs only the inputs: sums of s^2, dy w s and x^2
+    auto first_sums = [&](const RawRow &r, float &ss_of, float &m_of, float &xx_of) {
+        F2 ss = f2(0.f, 0.f), m = ss, xx = ss;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const F2 s = pair_of(r.s, i), x = pair_of(r.x, i);
+            ss = fma2(s, s, ss);
+            m = fma2(mul2(pair_of(r.dy, i), pre[i]), s, m);
+            xx = fma2(x, x, xx);
+        }
+        ss_of = sum2(ss);
+        m_of = sum2(m);
+        xx_of = sum2(xx);
+    };
+    float v[3] = {0.f, 0.f, 0.f}, gate_ahead = 0.f;
+    bool broken = false;
+    if constexpr (kJoint) {
         RawRow raw;
-        const uint8_t *const row = ring + st * 5 * row_bytes;
-        if constexpr (STAGES > 0) {
-            // (a wait that runs out is met by all threads behind the next barrier; until then they compute with what is there)
-            if (!tc::mbar_wait(tc::smem_u32(&landed[st]), ph, kWaitPolls, nullptr)) failed = 1;
-            raw.row_gate = a.gate_shape == MOE_GATE_ROW ? bf16_bits_to_float(a.gate[t]) : 0.f;
-            raw.x = on ? ring8(row, 0, nseg, seg) : zero4();
-            raw.s = on ? ring8(row, 1, nseg, seg) : zero4();
-            raw.dy = on && a.dy ? ring8(row, 2, nseg, seg) : zero4();
+        gate_ahead = row_gate_of(t);
+        await(0, 0);                                           // (there are no more blocks than rows)
+        from_ring(raw, 0, 0);
+        first_sums(raw, v[0], v[1], v[2]);
+        row_sums<TPR>(v, buf[1][0]);
+        broken = *static_cast<volatile int *>(&failed);
+    }
+    for (; !broken && t < a.T; t += gridDim.x, parity ^= 1) {
+        RawRow raw;
+        if constexpr (kJoint) {
+            const uint8_t *const row = ring + st * 4 * row_bytes;
+            raw.row_gate = gate_ahead;
+            from_ring(raw, st, sx);
+            raw.ds = on && a.dsum ? ring8(row, 2, nseg, seg) : zero4();
+            raw.gate = gate_rows ? (on ? ring8(row, 3, nseg, seg) : zero4()) : channel_gate;
         } else {
             raw = kAhead ? next : load_row(a, t, nseg, seg, on);
             if (kAhead) next = load_row(a, t + gridDim.x, nseg, seg, on);
+            first_sums(raw, v[0], v[1], v[2]);
+            row_sums<TPR>(v, buf[parity][0]);
         }
         const size_t at = (size_t)t * nseg + seg;
-        float v[3];
-        {
-            F2 ss = f2(0.f, 0.f), m = ss, xx = ss;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const F2 s = pair_of(raw.s, i), x = pair_of(raw.x, i);
-                ss = fma2(s, s, ss);
-                m = fma2(mul2(pair_of(raw.dy, i), pre[i]), s, m);
-                xx = fma2(x, x, xx);
-            }
-            v[0] = sum2(ss);
-            v[1] = sum2(m);
-            v[2] = sum2(xx);
-        }
-        row_sums<TPR>(v, buf[parity][0]);
-        if constexpr (STAGES > 0) {
-            // every thread is past the last row: its place is free
-            if (*static_cast<volatile int *>(&failed)) break;
-            if (threadIdx.x == 0) fetch(t + (STAGES - 1) * gridDim.x, st ? st - 1 : STAGES - 1);
-            raw.x = on ? ring8(row, 0, nseg, seg) : zero4();
-            raw.s = on ? ring8(row, 1, nseg, seg) : zero4();
-            raw.dy = on && a.dy ? ring8(row, 2, nseg, seg) : zero4();
-            raw.ds = on && a.dsum ? ring8(row, 3, nseg, seg) : zero4();
-            raw.gate = gate_rows ? (on ? ring8(row, 4, nseg, seg) : zero4()) : channel_gate;
-        }
         const float rx = a.post_norm ? rsqrtf(v[2] * inv_n + a.eps) : 1.0f;
         const float rs = a.dy ? rsqrtf(v[0] * inv_n + a.eps) : 0.0f, ms = -v[1] * inv_n * rs * rs * rs;
         float2 row_f = make_float2(1.f, 0.f);
@@ -403,7 +423,26 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
         if (on && a.dresidual) reinterpret_cast<uint4 *>(a.dresidual)[at] = make_uint4(wd[0], wd[1], wd[2], wd[3]);
         if (on && full) reinterpret_cast<uint4 *>(a.dgate)[at] = make_uint4(wg[0], wg[1], wg[2], wg[3]);
         float mean = 0.f;
-        if (BY_ELEMENT) {
+        if constexpr (kJoint) {
+            float u[4] = {0.f, 0.f, 0.f, sum2(m)}, sum_db = sum2(db);
+            if (t + (int)gridDim.x < a.T) {
+                const int after = st + 1 == STAGES ? 0 : st + 1, after_x = sx == STAGES ? 0 : sx + 1;
+                RawRow r;
+                gate_ahead = row_gate_of(t + gridDim.x);
+                await(after, after ? ph : ph ^ 1);
+                from_ring(r, after, after_x);
+                first_sums(r, u[0], u[1], u[2]);
+            }
+            row_sums<TPR>(u, buf[parity][0], BY_ELEMENT ? nullptr : &sum_db, buf[parity][1]);
+            if (*static_cast<volatile int *>(&failed)) break;
+            // every thread is past the row before, whose x is free, and needs nothing but x of this row
+            if (threadIdx.x == 0) fetch(t + STAGES * gridDim.x, st, sx ? sx - 1 : STAGES);
+            v[0] = u[0];
+            v[1] = u[1];
+            v[2] = u[2];
+            mean = -u[3] * inv_n;
+            if (!BY_ELEMENT && a.gate_shape == MOE_GATE_ROW && a.dgate && threadIdx.x == 0) static_cast<float *>(a.dgate)[t] = sum_db * row_f.y;
+        } else if (BY_ELEMENT) {
             float u[1] = {sum2(m)};
             if (a.post_norm) row_sums<TPR>(u, buf[parity][1]);
             mean = -u[0] * inv_n;
@@ -414,22 +453,25 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
             mean = -u[0] * inv_n;
         }
         if (a.post_norm) {
-            if (STAGES) raw.x = on ? ring8(row, 0, nseg, seg) : zero4();
+            if (STAGES) raw.x = on ? ring8(ring_x, sx, nseg, seg) : zero4();
             const F2 mean2 = f2(mean * rx, mean * rx);
 #pragma unroll
             for (int i = 0; i < 4; ++i) e[i] = mul2(fma2(pair_of(raw.x, i), mean2, mul2(e[i], post[i])), rx2);
         }
         if (on) reinterpret_cast<uint4 *>(a.dx)[at] = make_uint4(pack_pair(e[0]), pack_pair(e[1]), pack_pair(e[2]), pack_pair(e[3]));
-        if (STAGES && ++st == STAGES) {
-            st = 0;
-            ph ^= 1;
+        if (kJoint) {
+            if (++st == STAGES) {
+                st = 0;
+                ph ^= 1;
+            }
+            if (++sx > STAGES) sx = 0;
         }
     }
     if (STAGES && failed) {
         // nothing is left on its way into this block's shared memory: the rows that were asked for, this one first
         if (threadIdx.x == 0) {
             record_status(a.status, MOE_ERR_TIMEOUT);
-            for (int i = 0; i < STAGES - 1 && t + i * gridDim.x < a.T; ++i) {
+            for (int i = 0; i < STAGES && t + i * gridDim.x < a.T; ++i) {
                 tc::mbar_wait(tc::smem_u32(&landed[st]), ph, kWaitPolls, nullptr);
                 if (++st == STAGES) {
                     st = 0;
@@ -448,10 +490,13 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
             if (k == 0 ? want_post : k == 1 ? want_pre : want_gate) *reinterpret_cast<float4 *>(out + k * a.n + 4 * h) = mine[(2 * k + h) * TPR];
 }
 
-// Adds up the blocks' sums: a block has 32 columns of one of the three gradients, a warp every 32nd block.
-__global__ void __launch_bounds__(1024) gated_norm_sum_kernel(const __grid_constant__ GatedNormArgs a, int blocks)
+// Adds up the blocks' sums: a block has 32 columns of one of the three gradients, a warp every kWarps-th block,
+// kFlight loads on their way at once.
+template <int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) gated_norm_sum_kernel(const __grid_constant__ GatedNormArgs a, int blocks)
 {
-    __shared__ float part[32][33];
+    constexpr int kFlight = 10;                                // the 152 blocks of a wide row over 16 warps
+    __shared__ float part[kWarps][33];
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, col = blockIdx.x * 32 + lane, which = blockIdx.y;
@@ -461,20 +506,25 @@ __global__ void __launch_bounds__(1024) gated_norm_sum_kernel(const __grid_const
     float v = 0.f;
     if (col < a.n) {
         const float *p = a.partial + (size_t)which * a.n + col;
-#pragma unroll 4
-        for (int b = warp; b < blocks; b += 32) v += p[(size_t)b * 3 * a.n];
+        for (int b = warp; b < blocks; b += kFlight * kWarps) {
+            float x[kFlight];
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) x[i] = b + i * kWarps < blocks ? p[(size_t)(b + i * kWarps) * 3 * a.n] : 0.f;
+#pragma unroll
+            for (int i = 0; i < kFlight; ++i) v += x[i];
+        }
     }
     part[warp][lane] = v;
     __syncthreads();
     if (warp) return;
     v = 0.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v += part[i][lane];
+    for (int i = 0; i < kWarps; ++i) v += part[i][lane];
     if (col < a.n) out[col] = v;
 }
 
 // Threads of a block of the backward pass, blocks an SM, stages of its ring.
-constexpr int kGradPlans[][3] = {{32, 16, 0}, {64, 8, 0}, {128, 4, 0}, {256, 3, 2}, {512, 1, 4}, {640, 1, 3}, {768, 1, 2}, {1024, 1, 0}};
+constexpr int kGradPlans[][3] = {{32, 16, 0}, {64, 8, 0}, {128, 4, 0}, {256, 3, 2}, {320, 2, 3}, {416, 2, 2}, {512, 1, 4}, {640, 1, 3}, {768, 1, 2}, {1024, 1, 0}};
 int grad_plan(int n)
 {
     int i = 0;
@@ -490,12 +540,12 @@ int grad_blocks(int T, int n)
 template <int I, bool BY_ELEMENT, int ACT>
 cudaError_t launch_plan(const GatedNormArgs &a, int blocks, cudaStream_t st)
 {
-    constexpr int kThreads = kGradPlans[I][0], kStages = kGradPlans[I][2], kMost = (6 + 5 * kStages) * 16 * kThreads;
-    static_assert(kMost * kGradPlans[I][1] <= 224 * 1024, "shared memory");
+    constexpr int kThreads = kGradPlans[I][0], kStages = kGradPlans[I][2], kRing = kStages ? 5 * kStages + 1 : 0, kMost = (6 + kRing) * 16 * kThreads;
+    static_assert((kMost + 3 * 1024) * kGradPlans[I][1] <= 228 * 1024, "shared memory");
     auto k = gated_norm_grad_kernel<kThreads, kGradPlans[I][1], kStages, BY_ELEMENT, ACT>;
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = set_shared(k, kMost, ready);
-    return e != cudaSuccess ? e : launch_dependent(k, blocks, kThreads, 6 * 16 * kThreads + kStages * 10 * a.n, st, a);
+    return e != cudaSuccess ? e : launch_dependent(k, blocks, kThreads, 6 * 16 * kThreads + kRing * 2 * a.n, st, a);
 }
 template <int I>
 cudaError_t launch_backward(const GatedNormArgs &a, int blocks, cudaStream_t st)
@@ -541,18 +591,21 @@ cudaError_t launch_gated_norm_grad(const GatedNormArgs &a, cudaStream_t st)
     case 5: e = launch_backward<5>(a, blocks, st); break;
     case 6: e = launch_backward<6>(a, blocks, st); break;
     case 7: e = launch_backward<7>(a, blocks, st); break;
+    case 8: e = launch_backward<8>(a, blocks, st); break;
+    case 9: e = launch_backward<9>(a, blocks, st); break;
     }
     if (e != cudaSuccess || !(a.dpost_weight || a.dpre_weight || (a.dgate && a.gate_shape == MOE_GATE_CHANNEL))) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((a.n + 31) / 32, 3);
-    cfg.blockDim = dim3(1024);
+    const bool few = blocks <= 160;
+    cfg.blockDim = dim3(few ? 512 : 1024);
     cfg.stream = st;
     cudaLaunchAttribute attr{};
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    const cudaError_t s = cudaLaunchKernelEx(&cfg, gated_norm_sum_kernel, a, blocks);
+    const cudaError_t s = cudaLaunchKernelEx(&cfg, few ? gated_norm_sum_kernel<16> : gated_norm_sum_kernel<32>, a, blocks);
     return s == cudaSuccess ? s : cudaGetLastError();
 }
 
