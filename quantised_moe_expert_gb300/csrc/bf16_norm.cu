@@ -99,9 +99,27 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float4 *buf, float *more
 #pragma unroll
         for (int o = 16; o; o >>= 1) *more += __shfl_xor_sync(0xFFFFFFFFu, *more, o);
         if (lane == 0) more_buf[w].x = *more;
-        *more = 0.f;
+        if (N == 1 || TPR / 32 <= 4) *more = 0.f;
     }
     __syncthreads();
+    if constexpr (N > 1 && TPR / 32 > 4) {
+        // a lane adds up one value of every eighth warp (a float4 read by all lanes costs four of one word, for each warp)
+        float r = 0.f;
+#pragma unroll
+        for (int j = 0; j < TPR / 32; j += 8)
+            if (j + (lane >> 2) < TPR / 32) r += reinterpret_cast<const float *>(buf + w0 + j)[lane];
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) r += __shfl_xor_sync(0xFFFFFFFFu, r, o);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, r, i);
+        if (more) {
+            float q = lane < TPR / 32 ? more_buf[w0 + lane].x : 0.f;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) q += __shfl_xor_sync(0xFFFFFFFFu, q, o);
+            *more = q;
+        }
+        return;
+    }
     F2 lo = f2(0.f, 0.f), hi = lo;
     float one = 0.f;
 #pragma unroll 8
@@ -541,7 +559,7 @@ template <int I, bool BY_ELEMENT, int ACT>
 cudaError_t launch_plan(const GatedNormArgs &a, int blocks, cudaStream_t st)
 {
     constexpr int kThreads = kGradPlans[I][0], kStages = kGradPlans[I][2], kRing = kStages ? 5 * kStages + 1 : 0, kMost = (6 + kRing) * 16 * kThreads;
-    static_assert((kMost + 3 * 1024) * kGradPlans[I][1] <= 228 * 1024, "shared memory");
+    static_assert((kMost + 2 * kThreads + 1024 + 64) * kGradPlans[I][1] <= 228 * 1024, "shared memory");
     auto k = gated_norm_grad_kernel<kThreads, kGradPlans[I][1], kStages, BY_ELEMENT, ACT>;
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = set_shared(k, kMost, ready);
