@@ -13,12 +13,14 @@
 //
 // Bound: bytes, then instructions.  Forward, a thread keeps CH segments of 8 elements of a row in registers from the one read to
 // the write; sums over the row go through shuffles and shared memory.  Backward, a block walks over every gridDim-th
-// row: its next rows are on their way (by the copy engine, into a ring) under this one's sums, which meet in two rounds
-// (everything that needs only the inputs, then what needs D); the sums over rows of a thread's columns lie in shared memory, are
+// row: its next rows are on their way (by the copy engine, into rings) under this one's sums.  A row needs two rounds of sums:
+// of what needs only the inputs, then of what needs D; the first of the next row go with the second of this one, one
+// barrier a row.  The sums over rows of a thread's columns lie in shared memory, are
 // written as one row of the workspace, and a second launch adds those up in a fixed order.
-// Measured: forward of 16384 x 2048 with a gate per element 59 us (336 MB, 5.7 TB/s; one row a block of 256 threads 86), one row 1.9 us behind
-// another launch; backward of the same 97 us (537 MB, 5.5 TB/s, 64% of the issue slots; 205 with a barrier for each sum and values one by
-// one, 123 with rows through registers), of 777 x 5120 with a gate per channel 23 us, of which the sums over blocks are 5.
+// Measured: forward of 16384 x 2048 with a gate per element 59 us (336 MB, 5.7 TB/s; one row a block of 256 threads 86), one row 1.8 us behind
+// another launch; backward of the same 95 us (537 MB, 5.7 TB/s; 205 with a barrier for each sum and values one by
+// one, 123 with rows through registers), of 8192 x 5120 112 us (6.0 TB/s; 147 with two barriers a row and every thread reading every
+// warp's sums), of 777 x 5120 with a gate per channel 20 us, of which the sums over blocks are 4.
 #include "bf16.cuh"
 #include "f32x2.cuh"
 #include "tc_ptx.cuh"
@@ -287,11 +289,12 @@ __device__ __forceinline__ void gate_pair(F2 raw, F2 &f, F2 &slope)
     }
 }
 
-// A row of the ring: its arrays one behind the other, in the order of RawRow.
+// A place of a ring: its rows one behind the other (of x's one, of the other's s, dy, dsum and a gate per element).
 __device__ __forceinline__ uint4 ring8(const uint8_t *row, int which, int nseg, int seg) { return reinterpret_cast<const uint4 *>(row)[which * nseg + seg]; }
 
-// STAGES: rows come through a ring in shared memory, filled by the copy engine that many rows ahead (less one); 0: through
-// registers, the next row's elements on their way under this row's sums, where the ring does not fit or pays nothing.
+// STAGES: rows come through rings in shared memory, filled by the copy engine STAGES rows ahead of this one, x's a place longer
+// than the others' (x is read once more behind the row's last sums, when the others' places are free); 0: through
+// registers, the next row's elements on their way under this row's sums, where the rings do not fit or pay nothing.
 // Rows are kept as they were read and widened in each round; the sums over rows lie in shared memory, each thread's own.
 template <int TPR, int BLOCKS, int STAGES, bool BY_ELEMENT, int ACT>
 __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __grid_constant__ GatedNormArgs a)
@@ -541,7 +544,9 @@ __global__ void __launch_bounds__(32 * kWarps) gated_norm_sum_kernel(const __gri
     if (col < a.n) out[col] = v;
 }
 
-// Threads of a block of the backward pass, blocks an SM, stages of its ring.
+// Threads of a block of the backward pass, blocks an SM, stages of its rings.  Narrow rows (threads, blocks): 16384 x 1024 in 4 blocks
+// through registers 60 us, 3 or 5 70 and 63, 6 with rings 57, but a gate per channel 44 in 4 and 50 in 6.  2560 columns in two blocks
+// of 320 65 us for 8192 rows, in one of 512 106; 3192 in two of 416 44 us for 3469 rows, in one of 512 51.
 constexpr int kGradPlans[][3] = {{32, 16, 0}, {64, 8, 0}, {128, 4, 0}, {256, 3, 2}, {320, 2, 3}, {416, 2, 2}, {512, 1, 4}, {640, 1, 3}, {768, 1, 2}, {1024, 1, 0}};
 int grad_plan(int n)
 {

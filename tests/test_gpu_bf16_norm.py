@@ -144,6 +144,15 @@ def test_backward(T, n, gate, fn, post, use):
     assert all(torch.equal(got[k], again[k]) for k in got)
 
 
+# every width of block of the backward pass, each with more rows than the blocks hold at once
+@pytest.mark.parametrize("T,n,gate,fn,post", [(1500, 64, "row", "silu", 1), (1111, 512, "full", "silu", 1), (1900, 1032, "full", "none", 1),
+                                              (1400, 2048, "row", "sigmoid", 1), (1100, 2056, "none", "none", 1), (1003, 2560, "full", "silu", 0),
+                                              (801, 3320, "channel", "sigmoid", 1), (997, 4096, "row", "silu", 1), (900, 5000, "full", "sigmoid", 1),
+                                              (620, 6144, "none", "none", 0), (457, 8184, "channel", "none", 1)])
+def test_backward_of_many_rows(T, n, gate, fn, post):
+    test_backward(T, n, gate, fn, post, "both")
+
+
 @pytest.mark.parametrize("gate,fn", [("full", "silu"), ("row", "sigmoid"), ("channel", "none")])
 def test_backward_against_differences(gate, fn):
     """The formulas' gradients against differences of the formulas (in 64 bits), for the loss <dy, y> + <ds, s>."""
