@@ -67,13 +67,14 @@ __device__ __forceinline__ void gate_values(int act, uint4 raw, F2 (&f)[4])
     }
 }
 
-// Sums of N values over the TPR threads of a row, and with `more` of one more; buf, more_buf: a float4 a warp that no thread
+// Sums of N values over the TPR threads of a row, and with `more` (N > 1, rows of more than four warps) of one more; buf, more_buf: a float4 a warp that no thread
 // still reads.  Every thread of the block takes part.  Four values share their first two exchanges (each lane goes on with
 // one of them): 6 shuffles in place of 20.
 template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float4 *buf, float *more = nullptr, float4 *more_buf = nullptr)
 {
     static_assert(N <= 4, "a float4 a warp");
+    constexpr bool kWide = N > 1 && TPR / 32 > 4;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, w0 = w / (TPR / 32) * (TPR / 32);
     if (N > 1) {
         const float v2 = N > 2 ? v[N > 2 ? 2 : 0] : 0.f, v3 = N > 3 ? v[N > 3 ? 3 : 0] : 0.f;
@@ -97,14 +98,13 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float4 *buf, float *more
         if (TPR == 32) return;
         if (lane == 0) buf[w].x = v[0];
     }
-    if (more) {
+    if (kWide && more) {
 #pragma unroll
         for (int o = 16; o; o >>= 1) *more += __shfl_xor_sync(0xFFFFFFFFu, *more, o);
         if (lane == 0) more_buf[w].x = *more;
-        if (N == 1 || TPR / 32 <= 4) *more = 0.f;
     }
     __syncthreads();
-    if constexpr (N > 1 && TPR / 32 > 4) {
+    if constexpr (kWide) {
         // a lane adds up one value of every eighth warp (a float4 read by all lanes costs four of one word, for each warp)
         float r = 0.f;
 #pragma unroll
@@ -126,7 +126,6 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float4 *buf, float *more
     float one = 0.f;
 #pragma unroll 8
     for (int j = 0; j < TPR / 32; ++j) {
-        if (more) *more += more_buf[w0 + j].x;
         if (N == 1) {
             one += buf[w0 + j].x;
         } else if (N == 2) {
@@ -293,17 +292,19 @@ __device__ __forceinline__ void gate_pair(F2 raw, F2 &f, F2 &slope)
 __device__ __forceinline__ uint4 ring8(const uint8_t *row, int which, int nseg, int seg) { return reinterpret_cast<const uint4 *>(row)[which * nseg + seg]; }
 
 // STAGES: rows come through rings in shared memory, filled by the copy engine STAGES rows ahead of this one, x's a place longer
-// than the others' (x is read once more behind the row's last sums, when the others' places are free); 0: through
-// registers, the next row's elements on their way under this row's sums, where the rings do not fit or pay nothing.
+// than the others' (x is read once more behind the row's last sums, when the others' places are free).  ARRAYS of a place
+// besides x: all 4, or s and dy alone, where dsum and a gate per element come through registers a row ahead.  No stages: all of
+// it through registers, the next row's elements on their way under this row's sums, where the rings pay nothing.
 // Rows are kept as they were read and widened in each round; the sums over rows lie in shared memory, each thread's own.
-template <int TPR, int BLOCKS, int STAGES, bool BY_ELEMENT, int ACT>
+template <int TPR, int BLOCKS, int STAGES, int ARRAYS, bool BY_ELEMENT, int ACT>
 __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __grid_constant__ GatedNormArgs a)
 {
     extern __shared__ float4 sums[];                           // [post, pre, gate][half of a segment][thread]
     __shared__ float4 buf[2][2][TPR / 32];                     // [row's parity][round]
     __shared__ uint64_t landed[STAGES ? STAGES : 1];
     __shared__ int failed;
-    constexpr bool kAhead = STAGES == 0 && TPR < 1024, kJoint = STAGES > 0;
+    constexpr bool kJoint = STAGES > 0;
+    constexpr bool kLate = kJoint && ARRAYS < 4;
     const int nseg = a.n / 8, seg = threadIdx.x;
     const bool on = seg < nseg;
     pdl_trigger();
@@ -320,13 +321,13 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
     // row t into the rings' places `st` and `sx` (one thread)
     auto fetch = [&](int t, int st, int sx) {
         if (t >= a.T) return;
-        const uint32_t bar = tc::smem_u32(&landed[st]), to = tc::smem_u32(ring) + st * 4 * row_bytes;
+        const uint32_t bar = tc::smem_u32(&landed[st]), to = tc::smem_u32(ring) + st * ARRAYS * row_bytes;
         const uint16_t *const src[4] = {a.sum, a.dy, a.dsum, gate_rows ? a.gate : nullptr};
         uint32_t arrays = 1;
-        for (int i = 0; i < 4; ++i) arrays += src[i] != nullptr;
+        for (int i = 0; i < ARRAYS; ++i) arrays += src[i] != nullptr;
         tc::mbar_arrive_expect_tx(bar, arrays * row_bytes);
         tc::bulk_load(tc::smem_u32(ring_x) + sx * row_bytes, a.x + (size_t)t * a.n, row_bytes, bar);
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < ARRAYS; ++i)
             if (src[i]) tc::bulk_load(to + i * row_bytes, src[i] + (size_t)t * a.n, row_bytes, bar);
     };
     if (STAGES && threadIdx.x == 0)
@@ -343,7 +344,7 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
     for (int i = 0; i < 6; ++i) mine[i * TPR] = make_float4(0.f, 0.f, 0.f, 0.f);
     const uint4 channel_gate = BY_ELEMENT && !gate_rows && on ? load8(a.gate, seg) : zero4();
     RawRow next;
-    if (kAhead) next = load_row(a, blockIdx.x, nseg, seg, on);
+    if (!kJoint) next = load_row(a, blockIdx.x, nseg, seg, on);
     int parity = 0, st = 0, sx = 0, t = blockIdx.x;
     uint32_t ph = 0;
     // (a wait that runs out is met by all threads behind the next barrier; until then they compute with what is there)
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
         if (!tc::mbar_wait(tc::smem_u32(&landed[at]), phase, kWaitPolls, nullptr)) failed = 1;
     };
     auto from_ring = [&](RawRow &r, int at, int at_x) {
-        const uint8_t *const row = ring + at * 4 * row_bytes;
+        const uint8_t *const row = ring + at * ARRAYS * row_bytes;
         r.x = on ? ring8(ring_x, at_x, nseg, seg) : zero4();
         r.s = on ? ring8(row, 0, nseg, seg) : zero4();
         r.dy = on && a.dy ? ring8(row, 1, nseg, seg) : zero4();
@@ -371,11 +372,18 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
         m_of = sum2(m);
         xx_of = sum2(xx);
     };
+    uint4 late_ds = zero4(), late_gate = zero4();
+    auto load_late = [&](int row) {
+        if (!kLate || !on) return;
+        if (a.dsum) late_ds = load8(a.dsum + (size_t)row * a.n, seg);
+        if (gate_rows) late_gate = load8(a.gate + (size_t)row * a.n, seg);
+    };
     float v[3] = {0.f, 0.f, 0.f}, gate_ahead = 0.f;
     bool broken = false;
     if constexpr (kJoint) {
         RawRow raw;
         gate_ahead = row_gate_of(t);
+        load_late(t);
         await(0, 0);                                           // (there are no more blocks than rows)
         from_ring(raw, 0, 0);
         first_sums(raw, v[0], v[1], v[2]);
@@ -385,14 +393,19 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
     for (; !broken && t < a.T; t += gridDim.x, parity ^= 1) {
         RawRow raw;
         if constexpr (kJoint) {
-            const uint8_t *const row = ring + st * 4 * row_bytes;
+            const uint8_t *const row = ring + st * ARRAYS * row_bytes;
             raw.row_gate = gate_ahead;
             from_ring(raw, st, sx);
-            raw.ds = on && a.dsum ? ring8(row, 2, nseg, seg) : zero4();
-            raw.gate = gate_rows ? (on ? ring8(row, 3, nseg, seg) : zero4()) : channel_gate;
+            if (kLate) {
+                raw.ds = late_ds;
+                raw.gate = gate_rows ? late_gate : channel_gate;
+            } else {
+                raw.ds = on && a.dsum ? ring8(row, 2, nseg, seg) : zero4();
+                raw.gate = gate_rows ? (on ? ring8(row, 3, nseg, seg) : zero4()) : channel_gate;
+            }
         } else {
-            raw = kAhead ? next : load_row(a, t, nseg, seg, on);
-            if (kAhead) next = load_row(a, t + gridDim.x, nseg, seg, on);
+            raw = next;
+            next = load_row(a, t + gridDim.x, nseg, seg, on);
             first_sums(raw, v[0], v[1], v[2]);
             row_sums<TPR>(v, buf[parity][0]);
         }
@@ -450,6 +463,7 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
                 const int after = st + 1 == STAGES ? 0 : st + 1, after_x = sx == STAGES ? 0 : sx + 1;
                 RawRow r;
                 gate_ahead = row_gate_of(t + gridDim.x);
+                load_late(t + gridDim.x);
                 await(after, after ? ph : ph ^ 1);
                 from_ring(r, after, after_x);
                 first_sums(r, u[0], u[1], u[2]);
@@ -474,7 +488,7 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
             mean = -u[0] * inv_n;
         }
         if (a.post_norm) {
-            if (STAGES) raw.x = on ? ring8(ring_x, sx, nseg, seg) : zero4();
+            if (kJoint) raw.x = on ? ring8(ring_x, sx, nseg, seg) : zero4();
             const F2 mean2 = f2(mean * rx, mean * rx);
 #pragma unroll
             for (int i = 0; i < 4; ++i) e[i] = mul2(fma2(pair_of(raw.x, i), mean2, mul2(e[i], post[i])), rx2);
@@ -544,10 +558,14 @@ __global__ void __launch_bounds__(32 * kWarps) gated_norm_sum_kernel(const __gri
     if (col < a.n) out[col] = v;
 }
 
-// Threads of a block of the backward pass, blocks an SM, stages of its rings.  Narrow rows (threads, blocks): 16384 x 1024 in 4 blocks
+// Threads of a block of the backward pass, blocks an SM, stages of its rings and arrays of a place.  Narrow rows (threads, blocks): 16384 x 1024 in 4 blocks
 // through registers 60 us, 3 or 5 70 and 63, 6 with rings 57, but a gate per channel 44 in 4 and 50 in 6.  2560 columns in two blocks
 // of 320 65 us for 8192 rows, in one of 512 106; 3192 in two of 416 44 us for 3469 rows, in one of 512 51.
-constexpr int kGradPlans[][3] = {{32, 16, 0}, {64, 8, 0}, {128, 4, 0}, {256, 3, 2}, {320, 2, 3}, {416, 2, 2}, {512, 1, 4}, {640, 1, 3}, {768, 1, 2}, {1024, 1, 0}};
+// With two arrays a place more blocks fit: 4096 columns in two blocks of 512 and 64 registers 87 us for 8192 rows with a gate per
+// token (one block 99), but 62 for 4096 rows with a gate per element (54), 16384 x 2048 in four blocks 107 (95); 6144 columns, three stages of two
+// arrays 76.5, two of four 80; 8192 columns 122, with everything through registers and no rings 154.
+constexpr int kGradPlans[][4] = {{32, 16, 0, 0}, {64, 8, 0, 0}, {128, 4, 0, 0}, {256, 3, 2, 4}, {320, 2, 3, 4},
+                                 {416, 2, 2, 4}, {512, 1, 4, 4}, {640, 1, 3, 4}, {768, 1, 3, 2}, {1024, 1, 2, 2}};
 int grad_plan(int n)
 {
     int i = 0;
@@ -565,9 +583,9 @@ int grad_blocks(int T, int n)
 template <int I, bool BY_ELEMENT, int ACT>
 cudaError_t launch_plan(const GatedNormArgs &a, int blocks, cudaStream_t st)
 {
-    constexpr int kThreads = kGradPlans[I][0], kStages = kGradPlans[I][2], kRing = kStages ? 5 * kStages + 1 : 0, kMost = (6 + kRing) * 16 * kThreads;
+    constexpr int kThreads = kGradPlans[I][0], kStages = kGradPlans[I][2], kArrays = kGradPlans[I][3], kRing = kStages ? (1 + kArrays) * kStages + 1 : 0, kMost = (6 + kRing) * 16 * kThreads;
     static_assert((kMost + 2 * kThreads + 1024 + 64) * kGradPlans[I][1] <= 228 * 1024, "shared memory");
-    auto k = gated_norm_grad_kernel<kThreads, kGradPlans[I][1], kStages, BY_ELEMENT, ACT>;
+    auto k = gated_norm_grad_kernel<kThreads, kGradPlans[I][1], kStages, kArrays, BY_ELEMENT, ACT>;
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = set_shared(k, kMost, ready);
     return e != cudaSuccess ? e : launch_dependent(k, blocks, kThreads, 6 * 16 * kThreads + kRing * 2 * a.n, st, a);
