@@ -667,12 +667,34 @@ class ScaledLayer:
         return cls(host.shape, fmt, router, v, mat(gate, None), mat(up, None), mat(down, h_scale), h_scale)
 
 
+def _on_stream(stream, device, used, call):
+    """The tensors that `call` returns (or None in their places), called with `stream` (a torch stream or a handle) as the
+    current one: the memory that it makes and drops is that stream's.  What it returns may be dropped by its caller while the
+    caller's own stream still reads it, and `used`, which may be other streams' memory, while this one does."""
+    here = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        # handles 0 and 1 both mean the default stream
+        stream = torch.cuda.ExternalStream(int(stream), device) if int(stream) > 1 else torch.cuda.default_stream(device)
+    for t in used:
+        if t is not None:
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        out = call()
+    for t in out:
+        if t is not None:
+            t.record_stream(here)
+    return out
+
+
 class Experts16:
     """The experts of a layer in 16 bits, forward and backward: stacks gate, up [G, inter, hidden] and down [G, hidden, inter]
     (bf16 device tensors), the shared expert's matrices last.
 
     Routing comes from moe_route and moe_permute (or any that gives the same): inv_perm [T k], offsets of the sorted rows, pick
-    weights p [T, k] and the shared expert's w_shared [T]."""
+    weights p [T, k] and the shared expert's w_shared [T].
+
+    With stream= both passes run on that stream and their memory belongs to it, as under torch.cuda.stream; what they are given
+    has to be ready there, and what they return is ready when that stream has come so far."""
 
     def __init__(self, gate, up, down, top_k: int, has_shared: bool, act: int = MOE_ACT_SILU):
         G, I, H = gate.shape
@@ -683,21 +705,33 @@ class Experts16:
 
     def forward(self, x, inv_perm, offsets, p, w_shared, ws, keep: bool = False, stream=None):
         """y [T, hidden] (bf16), and with keep what backward needs."""
+        if stream is not None:
+            out = _on_stream(stream, x.device, (), lambda: self._forward(x, inv_perm, offsets, p, w_shared, ws, keep))
+        else:
+            out = self._forward(x, inv_perm, offsets, p, w_shared, ws, keep)
+        return (out[0], (*out[1:], inv_perm, offsets, p, w_shared)) if keep else out[0]
+
+    def _forward(self, x, inv_perm, offsets, p, w_shared, ws, keep):
         (G, I, H), T, k, sh = self.gate.shape, x.shape[0], self.top_k, self.has_shared
         R = T * (k + sh)
         new = lambda *n: torch.empty(n, dtype=torch.bfloat16, device=x.device)
         rows, h, slots, y = new(R, H), new(R, I), new(R, H), new(T, H)
         g, u = (new(R, I), new(R, I)) if keep else (None, None)
-        moe_dispatch(x, T, H, k, sh, inv_perm, rows, ws, stream)
-        moe_gemm_glu(rows, self.gate, self.up, None, None, self.act, R, I, H, G, offsets, g, u, h, ws, stream)
-        moe_gemm(h, self.down, None, None, 0, R, H, I, G, offsets, None, MOE_ACT_NONE, None, None, slots, ws, stream)
-        moe_weighted_sum(slots, T, H, k, sh, inv_perm, p, w_shared, y, ws, stream)
-        return (y, (rows, g, u, h, slots, inv_perm, offsets, p, w_shared)) if keep else y
+        moe_dispatch(x, T, H, k, sh, inv_perm, rows, ws)
+        moe_gemm_glu(rows, self.gate, self.up, None, None, self.act, R, I, H, G, offsets, g, u, h, ws)
+        moe_gemm(h, self.down, None, None, 0, R, H, I, G, offsets, None, MOE_ACT_NONE, None, None, slots, ws)
+        moe_weighted_sum(slots, T, H, k, sh, inv_perm, p, w_shared, y, ws)
+        return (y, rows, g, u, h, slots) if keep else (y,)
 
     def backward(self, dy, kept, ws, stream=None, dgate=None, dup=None, ddown=None, accumulate: bool = False):
         """Gradients of x, p, w_shared (None without a shared expert), gate, up and down, from dy [T, hidden] and what
         forward kept.  dgate, dup, ddown: where to write them (fp32 or bf16, new bf16 tensors by default), or with accumulate
         where to add them (fp32)."""
+        if stream is not None:
+            return _on_stream(stream, dy.device, kept, lambda: self._backward(dy, kept, ws, dgate, dup, ddown, accumulate))
+        return self._backward(dy, kept, ws, dgate, dup, ddown, accumulate)
+
+    def _backward(self, dy, kept, ws, dgate, dup, ddown, accumulate):
         rows, g, u, h, slots, inv_perm, offsets, p, w_shared = kept
         (G, I, H), T, k, sh = self.gate.shape, dy.shape[0], self.top_k, self.has_shared
         R = T * (k + sh)
@@ -707,15 +741,15 @@ class Experts16:
         dp = torch.empty((T, k), device=dy.device)
         dw_shared = torch.empty((T,), device=dy.device) if sh else None
         acc = int(accumulate)
-        moe_weighted_sum_grad(dy, slots, T, H, k, sh, inv_perm, p, w_shared, dslots, dp, dw_shared, ws, stream)
-        moe_gemm_wgrad(dslots, h, R, H, I, G, offsets, acc, ddown, None, ws, stream)
-        moe_gemm(dslots, self.down, None, None, 1, R, I, H, G, offsets, None, MOE_ACT_NONE, None, None, dh, ws, stream)
-        moe_act_grad(self.act, dh, g, u, R, I, dg, du, stream)
-        moe_gemm_wgrad(dg, rows, R, I, H, G, offsets, acc, dgate, None, ws, stream)
-        moe_gemm_wgrad(du, rows, R, I, H, G, offsets, acc, dup, None, ws, stream)
+        moe_weighted_sum_grad(dy, slots, T, H, k, sh, inv_perm, p, w_shared, dslots, dp, dw_shared, ws)
+        moe_gemm_wgrad(dslots, h, R, H, I, G, offsets, acc, ddown, None, ws)
+        moe_gemm(dslots, self.down, None, None, 1, R, I, H, G, offsets, None, MOE_ACT_NONE, None, None, dh, ws)
+        moe_act_grad(self.act, dh, g, u, R, I, dg, du)
+        moe_gemm_wgrad(dg, rows, R, I, H, G, offsets, acc, dgate, None, ws)
+        moe_gemm_wgrad(du, rows, R, I, H, G, offsets, acc, dup, None, ws)
         # dslots' place serves for the gradient of the rows
-        moe_gemm(dg, self.gate, du, self.up, 1, R, H, I, G, offsets, None, MOE_ACT_NONE, None, None, dslots, ws, stream)
-        moe_weighted_sum(dslots, T, H, k, sh, inv_perm, None, None, dx, ws, stream)
+        moe_gemm(dg, self.gate, du, self.up, 1, R, H, I, G, offsets, None, MOE_ACT_NONE, None, None, dslots, ws)
+        moe_weighted_sum(dslots, T, H, k, sh, inv_perm, None, None, dx, ws)
         return dx, dp, dw_shared, dgate, dup, ddown
 
 
