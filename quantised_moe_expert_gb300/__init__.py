@@ -738,8 +738,8 @@ class Experts16:
         new = lambda *n: torch.empty(n, dtype=torch.bfloat16, device=dy.device)
         dgate, dup, ddown = (torch.empty_like(m) if d is None else d for d, m in ((dgate, self.gate), (dup, self.up), (ddown, self.down)))
         dslots, dh, dg, du, dx = new(R, H), new(R, I), new(R, I), new(R, I), new(T, H)
-        dp = torch.empty((T, k), device=dy.device)
-        dw_shared = torch.empty((T,), device=dy.device) if sh else None
+        dp = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+        dw_shared = torch.empty((T,), dtype=torch.float32, device=dy.device) if sh else None
         acc = int(accumulate)
         moe_weighted_sum_grad(dy, slots, T, H, k, sh, inv_perm, p, w_shared, dslots, dp, dw_shared, ws)
         moe_gemm_wgrad(dslots, h, R, H, I, G, offsets, acc, ddown, None, ws)

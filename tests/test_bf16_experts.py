@@ -104,3 +104,14 @@ def test_memory_belongs_to_the_stream_without_keeping(world):
     y = experts().forward(rows(T, H), *arguments(), WS, stream=SIDE)
     assert world.owner[y.data_ptr()] == SIDE and HERE in world.uses[y.data_ptr()]
     assert all(owner == SIDE for owner in world.owner.values())
+
+
+@pytest.mark.parametrize("default", [torch.float64, torch.bfloat16])
+def test_gradients_of_pick_weights_are_fp32(world, default):
+    """Whatever torch's default element type is: the library would refuse the call half way through the pass."""
+    torch.set_default_dtype(default)
+    try:
+        _, (dx, dp, dw_shared, *_) = both(experts())
+    finally:
+        torch.set_default_dtype(torch.float32)
+    assert dp.dtype == dw_shared.dtype == torch.float32 and dx.dtype == torch.bfloat16
