@@ -703,8 +703,17 @@ class Experts16:
         self.gate, self.up, self.down = gate, up, down
         self.n_experts, self.top_k, self.has_shared, self.act = G - int(has_shared), top_k, int(has_shared), act
 
+    def _refuse(self, bad, status=MOE_ERR_INVALID_ARG):
+        # the library sees addresses, and the sizes that x and the matrices have
+        if bad:
+            raise MoeError("Experts16", status)
+
     def forward(self, x, inv_perm, offsets, p, w_shared, ws, keep: bool = False, stream=None):
-        """y [T, hidden] (bf16), and with keep what backward needs."""
+        """y [T, hidden] (bf16), and with keep what backward needs.  The routing's tensors may be longer than T tokens need."""
+        (G, _, H), T = self.gate.shape, x.shape[0]
+        self._refuse(x.dim() != 2 or x.shape[1] != H or inv_perm.numel() < T * self.top_k or offsets.numel() < G or
+                     p.numel() < T * self.top_k or (T > 0 and (w_shared is not None) != bool(self.has_shared)) or
+                     (w_shared is not None and w_shared.numel() < T))
         if stream is not None:
             out = _on_stream(stream, x.device, (), lambda: self._forward(x, inv_perm, offsets, p, w_shared, ws, keep))
         else:
@@ -726,7 +735,12 @@ class Experts16:
     def backward(self, dy, kept, ws, stream=None, dgate=None, dup=None, ddown=None, accumulate: bool = False):
         """Gradients of x, p, w_shared (None without a shared expert), gate, up and down, from dy [T, hidden] and what
         forward kept.  dgate, dup, ddown: where to write them (fp32 or bf16, new bf16 tensors by default), or with accumulate
-        where to add them (fp32)."""
+        where to add them (fp32, all three)."""
+        (G, I, H), rows = self.gate.shape, kept[0]
+        self._refuse(dy.dim() != 2 or dy.shape[1] != H or dy.shape[0] * (self.top_k + self.has_shared) != rows.shape[0])
+        for d in (dgate, dup, ddown):
+            self._refuse(d is not None and d.numel() != G * I * H)
+            self._refuse(accumulate and (d is None or d.dtype != torch.float32), MOE_ERR_UNSUPPORTED)
         if stream is not None:
             return _on_stream(stream, dy.device, kept, lambda: self._backward(dy, kept, ws, dgate, dup, ddown, accumulate))
         return self._backward(dy, kept, ws, dgate, dup, ddown, accumulate)

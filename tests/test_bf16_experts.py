@@ -115,3 +115,51 @@ def test_gradients_of_pick_weights_are_fp32(world, default):
     finally:
         torch.set_default_dtype(torch.float32)
     assert dp.dtype == dw_shared.dtype == torch.float32 and dx.dtype == torch.bfloat16
+
+
+def short(t):
+    return t.reshape(-1)[:-1].contiguous()
+
+
+@pytest.mark.parametrize("name,bad", [
+    ("x", rows(T, H - 8)), ("x", rows(T, H + 8)), ("x", rows(T * H)), ("inv_perm", short(arguments()[0])), ("offsets", arguments()[1][:E]),
+    ("p", short(rows(T, K))), ("w_shared", rows(T - 1)), ("w_shared", None)])
+def test_sizes_that_do_not_fit_are_refused_forward(world, name, bad):
+    """The library sees addresses and the sizes that follow from x and the matrices: a tensor that holds less would be read past its end."""
+    e, given = experts(), dict(zip(("x", "inv_perm", "offsets", "p", "w_shared"), (rows(T, H), *arguments())))
+    e.forward(**given, ws=WS)
+    count = len(world.calls)
+    with pytest.raises(qm.MoeError) as err:
+        e.forward(**{**given, name: bad}, ws=WS)
+    assert err.value.status == qm.MOE_ERR_INVALID_ARG and len(world.calls) == count
+
+
+def f32(*shape):
+    return torch.zeros(shape)
+
+
+@pytest.mark.parametrize("bad", [
+    dict(dy=rows(T, H - 8)), dict(dy=rows(T + 1, H)), dict(dy=rows(T - 1, H)), dict(dy=rows(T * H)), dict(dgate=short(f32(E + 1, I, H))),
+    dict(dup=f32(E, I, H)), dict(ddown=f32(E + 2, H, I)),
+    # added to: only what the caller holds, in 32 bits, and none of the three before all of them are known to be
+    dict(accumulate=True), dict(accumulate=True, dgate=f32(E + 1, I, H), ddown=f32(E + 1, H, I)),
+    dict(accumulate=True, dgate=f32(E + 1, I, H), dup=rows(E + 1, I, H), ddown=f32(E + 1, H, I))])
+def test_what_does_not_fit_is_refused_backward(world, bad):
+    e = experts()
+    _, kept = e.forward(rows(T, H), *arguments(), WS, keep=True)
+    given = dict(dy=rows(T, H), dgate=f32(E + 1, I, H), dup=f32(E + 1, I, H), ddown=f32(E + 1, H, I))
+    e.backward(**given, kept=kept, ws=WS, accumulate=True)
+    count = len(world.calls)
+    with pytest.raises(qm.MoeError) as err:
+        e.backward(**({"dy": given["dy"], **bad} if "accumulate" in bad else {**given, **bad}), kept=kept, ws=WS)
+    assert err.value.status in (qm.MOE_ERR_INVALID_ARG, qm.MOE_ERR_UNSUPPORTED) and len(world.calls) == count
+
+
+def test_longer_routing_buffers_and_no_tokens(world):
+    """Routing buffers may hold more than the tokens need; there may be no tokens."""
+    inv, offsets, p, w_s = arguments()
+    for shared in (True, False):
+        e, longer = experts(shared), lambda t: torch.cat([t.reshape(-1), t.reshape(-1)])
+        for n in (T, 0):
+            y, kept = e.forward(rows(n, H), longer(inv), longer(offsets), longer(p), longer(w_s) if shared else None, WS, keep=True)
+            assert y.shape == (n, H) and e.backward(rows(n, H), kept, WS)[0].shape == (n, H)
