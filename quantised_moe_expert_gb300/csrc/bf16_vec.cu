@@ -25,6 +25,7 @@ using tc::pdl_wait;
 constexpr int kWarps = 8, kThreads = 32 * kWarps;
 constexpr int kMaxGroups = 1024;
 constexpr int kChunk = 32;                         // terms of a lane quartet's load: 8 of each lane
+constexpr int kSegment = 768;                      // terms of an fp32 output that the instructions add up in one go (as in bf16_gemm.cu)
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
 {
@@ -91,7 +92,10 @@ __device__ __forceinline__ Chunk find_chunk(const GemmArgs &a, int index)
 }
 
 // A CTA has the outputs of kWarps / S tiles of 16 for one chunk of rows; S warps share a tile's terms.  NB: 8 rows each.
-template <bool DUAL, int NB, int S>
+// SEGMENTS: a slice's sums leave the instructions' accumulators every kSegment terms and meet in shared memory, since no registers
+// are left.  65536 terms: error in the 2-norm 9.2e-6 -> 7.2e-7 (two pairs 1.9e-5 -> 7.4e-7), 8 x 1024 x 65536 47 us either way, 30 rows of 3
+// groups x 72 71 -> 86.  A kernel of its own: as a branch in the others it took 2 to 17% of their time.
+template <bool DUAL, int NB, int S, bool SEGMENTS>
 __global__ void __launch_bounds__(kThreads, 2) gemm_vec_kernel(const __grid_constant__ GemmArgs a, int blocks)
 {
     constexpr int kMats = DUAL ? 2 : 1, kTiles = kWarps / S, kOut = 16 * kTiles, kRows = 8 * NB;
@@ -109,6 +113,10 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_vec_kernel(const __grid_cons
     const size_t matrix = (size_t)c.g * a.N;
     const int chunks = (a.K + kChunk - 1) / kChunk, per = (chunks + S - 1) / S, lo = slice * per, hi = min(lo + per, chunks);
     float acc[kMats][NB][4] = {};
+    // the thread's own places in the slices' sums
+    auto place = [&](int m, int b, int e) -> float & { return part[m][slice][8 * b + 2 * q + (e & 1)][16 * tile + i + 8 * (e >> 1)]; };
+    int rounds = 0;                                // of loads since the last segment
+    bool more = false;                             // there are sums of earlier segments
     if (first < a.N) {
         for (int pair = 0; pair < a.pairs; ++pair) {
             const uint16_t *w[kMats][2], *x[NB];
@@ -120,6 +128,17 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_vec_kernel(const __grid_cons
 #pragma unroll
             for (int b = 0; b < NB; ++b) x[b] = a.a[pair] + (size_t)(c.row + min(8 * b + i, c.rows - 1)) * a.K + 8 * q;
             for (int c0 = lo; c0 < hi; c0 += kAhead) {
+                if (SEGMENTS && rounds++ == kSegment / (kAhead * kChunk)) {
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            place(0, b, e) = more ? place(0, b, e) + acc[0][b][e] : acc[0][b][e];
+                            acc[0][b][e] = 0.f;
+                        }
+                    more = true;
+                    rounds = 1;
+                }
                 uint4 u[kAhead][kMats][2], v[kAhead][NB];
 #pragma unroll
                 for (int j = 0; j < kAhead; ++j) {
@@ -151,7 +170,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_vec_kernel(const __grid_cons
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) part[m][slice][8 * b + 2 * q + (e & 1)][16 * tile + i + 8 * (e >> 1)] = acc[m][b][e];
+            for (int e = 0; e < 4; ++e) place(m, b, e) = SEGMENTS && more ? place(m, b, e) + acc[m][b][e] : acc[m][b][e];
     __syncthreads();
     for (int t = threadIdx.x; t < c.rows * kOut; t += kThreads) {
         const int r = t / kOut, o = t - r * kOut, n = n0 + o;
@@ -174,16 +193,18 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_vec_kernel(const __grid_cons
     }
 }
 
-template <bool DUAL, int NB, int S>
+template <bool DUAL, int NB, int S, bool SEGMENTS = false>
 cudaError_t launch(const GemmArgs &a, cudaStream_t st)
 {
     constexpr int kOut = 16 * (kWarps / S), kRows = 8 * NB;
     const int blocks = (a.N + kOut - 1) / kOut, chunks = a.offsets ? a.R / kRows + (a.G < a.R ? a.G : a.R) : (a.R + kRows - 1) / kRows;
-    return launch_dependent(gemm_vec_kernel<DUAL, NB, S>, (unsigned)chunks * blocks, kThreads, 0, st, a, blocks);
+    return launch_dependent(gemm_vec_kernel<DUAL, NB, S, SEGMENTS>, (unsigned)chunks * blocks, kThreads, 0, st, a, blocks);
 }
 template <bool DUAL, int NB>
 cudaError_t launch_slices(const GemmArgs &a, cudaStream_t st)
 {
+    if constexpr (!DUAL)
+        if (a.y_f32 && (long long)a.K * a.pairs > kWarps * kSegment) return launch<DUAL, NB, kWarps, true>(a, st);
     // a slice of 256 terms is one round of loads
     if (a.K > 1024) return launch<DUAL, NB, 8>(a, st);
     if (a.K > 512) return launch<DUAL, NB, 4>(a, st);
