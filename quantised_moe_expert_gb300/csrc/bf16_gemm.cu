@@ -42,7 +42,9 @@ constexpr int kSliceBytes = 16 * 128;              // one of 16 terms
 // fp32 outputs: steps after which a tile's sums leave tensor memory, to be added up in registers.  The tensor cores' additions do not
 // round to nearest, so that their error grows with the number of terms, not its root (2-norm, 512, 1024, 2048, 4096 and 8192 terms in
 // one go: 4.7e-7, 1.0e-6, 2.1e-6, 2.1e-6, 4.4e-6; fp32 on the other units 1.6e-7 to 9.6e-7).
-constexpr int kSegment = 12;
+// bf16 outputs: 8192 terms of one sign lose at most 512 times 2^-24 of their sum, 1/64 of the rounding to come (262,144 in one go
+// lost 6e-4, and a third of the outputs were rounded to the wrong value).
+constexpr int kSegmentF32 = 12, kSegment16 = 128;
 enum Kind { kNT, kNN, kTN };
 
 template <int KIND, bool DUAL, int BN, bool PAIR, int SPLIT>
@@ -800,17 +802,18 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
             };
             // whole steps
             const int whole = KIND == kTN ? min(ks1, t.terms / kStep) : ks1;
-            int left = kSegment;
+            const int segment = !DUAL && a.y_f32 ? kSegmentF32 : kSegment16;
+            int left = segment;
 #pragma unroll 1
             for (int ks = ks0; ok && ks < whole; ++ks) {
-                if (!DUAL && a.y_f32 && left-- == 0) {
+                if (left-- == 0) {
                     hand_over();
                     ok = wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1);
                     if (!ok) break;
                     tc_fence_after();
                     d = tmem + acc * BN;
                     more = 0;
-                    left = kSegment - 1;
+                    left = segment - 1;
                 }
                 ok = wait(smem_u32(&sh.full[0]) + 8 * st, ph);
                 if (!ok) break;
@@ -828,7 +831,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
             }
             if (KIND == kTN && ok && ks0 < ks1 && ks1 > whole) {
                 // the end of a sum, in slices of 16 terms, a block of each behind the other
-                if (a.y_f32 && left == 0) {
+                if (left == 0) {
                     hand_over();
                     ok = wait(smem_u32(&sh.acc_empty[acc]), aph ^ 1);
                     tc_fence_after();
@@ -919,7 +922,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
             const Tile t = tile_at<KIND, P::kRows, P::kOutN>(a, sh, tile, shape);
             const int r0 = rank * 128 + quad * 32, col0 = t.col0 + half * kCols;
             const int steps = last_step(steps_of(t)) - first_step(steps_of(t));
-            const int segments = !DUAL && a.y_f32 ? max(1, (steps + kSegment - 1) / kSegment) : 1;
+            const int segments = max(1, !DUAL && a.y_f32 ? (steps + kSegmentF32 - 1) / kSegmentF32 : (steps + kSegment16 - 1) / kSegment16);
             const bool any = r0 < t.rows && (SPLIT > 1 || col0 < a.N);
             float v[kCols], u[DUAL ? kCols : 1];
             if (KIND != kTN && !DUAL && any && a.residual && lane < t.rows - r0) {
@@ -937,6 +940,7 @@ product_kernel(const __grid_constant__ ProductArgs a, const __grid_constant__ Ma
                     // to registers before anything is computed from them or stored: free for later products
                     if (seg) {
                         add_columns(d, v);
+                        if constexpr (DUAL) add_columns(d + BN / 2, u);
                     } else {
                         load_columns(d, v);
                         if constexpr (DUAL) load_columns(d + BN / 2, u);
