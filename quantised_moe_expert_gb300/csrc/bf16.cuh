@@ -43,9 +43,9 @@ __device__ __forceinline__ float2 act_slope(int act, float v)
         return make_float2(v * s, s + v * s * (1.0f - s));
     }
     case MOE_ACT_GELU: {
-        // past +-10 the slope is 1 or 0 to 30 digits, and v^2 would leave fp32's range
+        // past +-10 the slope is 1 or 0 to 30 digits, and v^2 would leave fp32's range; the value is v or 0 (1e-38 of 3e38 would not be)
         const float c = fminf(fmaxf(v, -10.0f), 10.0f), s = sigmoid(kGelu2 * (c + kGelu3 * c * c * c));
-        return make_float2(v * s, v != v ? v : s + c * s * (1.0f - s) * (kGelu2 * (1.0f + 3.0f * kGelu3 * c * c)));
+        return make_float2(v * (v < -10.0f ? 0.0f : s), v != v ? v : s + c * s * (1.0f - s) * (kGelu2 * (1.0f + 3.0f * kGelu3 * c * c)));
     }
     case MOE_ACT_RELU: return v > 0.f ? make_float2(v, 1.f) : make_float2(v != v ? v : 0.f, 0.f);
     case MOE_ACT_SIGMOID: {

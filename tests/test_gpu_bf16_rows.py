@@ -167,3 +167,27 @@ def test_act_grad_against_differences():
         ok = width > 0
         tol = BF16 * want.abs() + 1.2 * width + 6 * 2.0 ** -20 / width.clamp_min(1e-9)
         within(got[ok], want[ok], tol[ok])
+
+
+@pytest.mark.parametrize("name", ACTS)
+def test_act_grad_at_the_ends_of_the_range(name):
+    """Values and slopes at the largest arguments and around the point past which GELU's slope is held; the value is the one that the
+    products' epilogue gives."""
+    v = torch.tensor([3e38, -3e38, 1e38, -1e38, 1e20, -1e20, 300.0, -300.0, 12.0, -12.0, 10.0, -10.0, 10.25, -10.25, 9.75, -9.75], device="cuda").bfloat16()
+    n = v.numel()
+    ones, up, d, dup = torch.ones(1, n, dtype=torch.bfloat16, device="cuda"), torch.full((1, n), 2.0, dtype=torch.bfloat16, device="cuda"), *(
+        torch.empty(1, n, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    qm.moe_act_grad(ACTS[name], ones, v.view(1, n), up, 1, n, d, dup)
+    c = v.double().clamp(-1e4, 1e4)                          # v^3 of the 64-bit form stays in range
+    value, slope = act(name, c)
+    if name != "none":
+        value = torch.where(v.double() > 1e4, v.double(), value)
+    else:
+        value = v.double()
+    # past +-9 a function is v or 0, and its slope 1 or 0, to fewer than 2^-20 of 12
+    within(dup[0], value, BF16 * value.abs() + 2.0 ** -16)
+    within(d[0], 2 * slope, BF16 * 2 * slope.abs() + 2.0 ** -16)
+    ws = torch.zeros(512, dtype=torch.uint8, device="cuda")
+    zero, y = torch.zeros(1, n, dtype=torch.bfloat16, device="cuda"), torch.empty(1, n, device="cuda")
+    qm.moe_gemm(zero, torch.zeros(1, n, n, dtype=torch.bfloat16, device="cuda"), None, None, 0, 1, n, n, 1, None, v, ACTS[name], None, None, y, ws)
+    within(dup, y.double(), BF16 * y.double().abs())
