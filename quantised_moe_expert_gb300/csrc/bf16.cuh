@@ -47,7 +47,10 @@ __device__ __forceinline__ float2 act_slope(int act, float v)
         const float c = fminf(fmaxf(v, -10.0f), 10.0f), s = sigmoid(kGelu2 * (c + kGelu3 * c * c * c));
         return make_float2(v * (v < -10.0f ? 0.0f : s), v != v ? v : s + c * s * (1.0f - s) * (kGelu2 * (1.0f + 3.0f * kGelu3 * c * c)));
     }
-    case MOE_ACT_RELU: return v > 0.f ? make_float2(v, 1.f) : make_float2(v != v ? v : 0.f, 0.f);
+    case MOE_ACT_RELU: {
+        const float f = v <= 0.f ? 0.f : v;                  // (NaN stays, here and in the slope)
+        return make_float2(f, f > 0.f ? 1.f : f);
+    }
     case MOE_ACT_SIGMOID: {
         const float s = sigmoid(v);
         return make_float2(s, s * (1.0f - s));

@@ -191,3 +191,20 @@ def test_act_grad_at_the_ends_of_the_range(name):
     zero, y = torch.zeros(1, n, dtype=torch.bfloat16, device="cuda"), torch.empty(1, n, device="cuda")
     qm.moe_gemm(zero, torch.zeros(1, n, n, dtype=torch.bfloat16, device="cuda"), None, None, 0, 1, n, n, 1, None, v, ACTS[name], None, None, y, ws)
     within(dup, y.double(), BF16 * y.double().abs())
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu", "relu"])
+def test_nan_reaches_the_gradients(name):
+    """Of an element whose pre is NaN, and of no other, value and slope are NaN, plain and as a gated pair."""
+    pre = torch.linspace(-3, 3, 16, device="cuda").bfloat16().view(2, 8)
+    dy, up, odd = torch.ones_like(pre), torch.full_like(pre, 2.0), pre.clone()
+    odd[1, 3] = float("nan")
+    outs = []
+    for v in (pre, odd):
+        plain, d, dup = (torch.empty_like(pre) for _ in range(3))
+        qm.moe_act_grad(ACTS[name], dy, v, None, 2, 8, plain, None)
+        qm.moe_act_grad(ACTS[name], dy, v, up, 2, 8, d, dup)
+        outs.append((plain, d, dup))
+    for a, b in zip(*outs):
+        assert bool(b[1, 3].isnan()) and int(b.isnan().sum()) == 1
+        assert torch.equal(torch.where(odd.isnan(), 0.0, a), torch.where(odd.isnan(), 0.0, b))
