@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
     extern __shared__ float4 sums[];                           // [post, pre, gate][half of a segment][thread]
     __shared__ float4 buf[2][2][TPR / 32];                     // [row's parity][round]
     __shared__ uint64_t landed[STAGES ? STAGES : 1];
-    __shared__ int failed;
+    __shared__ int failed[2];                                  // by the row's parity: whether a wait for the row after it ran out
     constexpr bool kJoint = STAGES > 0;
     constexpr bool kLate = kJoint && ARRAYS < 4;
     const int nseg = a.n / 8, seg = threadIdx.x;
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
     pdl_trigger();
     if (STAGES && threadIdx.x == 0) {
         for (int i = 0; i < STAGES; ++i) tc::mbar_init(tc::smem_u32(&landed[i]), 1);
-        failed = 0;
+        failed[0] = failed[1] = 0;
         tc::fence_mbar_init();
     }
     if (STAGES) __syncthreads();
@@ -347,10 +347,12 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
     if (!kJoint) next = load_row(a, blockIdx.x, nseg, seg, on);
     int parity = 0, st = 0, sx = 0, t = blockIdx.x;
     uint32_t ph = 0;
-    // (a wait that runs out is met by all threads behind the next barrier; until then they compute with what is there)
-    auto await = [&](int at, uint32_t phase) {
-        if (!tc::mbar_wait(tc::smem_u32(&landed[at]), phase, kWaitPolls, nullptr)) failed = 1;
+    // A wait that runs out is met by all threads behind the next barrier; until then they compute with what is there.  A thread ahead of
+    // the others may give up on a later row before they have looked: that is the other flag, so that all leave behind the same barrier.
+    auto await = [&](int at, uint32_t phase, int which) {
+        if (!tc::mbar_wait(tc::smem_u32(&landed[at]), phase, kWaitPolls, nullptr)) failed[which] = 1;
     };
+    auto given_up = [&](int which) { return *static_cast<volatile int *>(&failed[which]) != 0; };
     auto from_ring = [&](RawRow &r, int at, int at_x) {
         const uint8_t *const row = ring + at * ARRAYS * row_bytes;
         r.x = on ? ring8(ring_x, at_x, nseg, seg) : zero4();
@@ -384,11 +386,11 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
         RawRow raw;
         gate_ahead = row_gate_of(t);
         load_late(t);
-        await(0, 0);                                           // (there are no more blocks than rows)
+        await(0, 0, 1);                                        // (there are no more blocks than rows)
         from_ring(raw, 0, 0);
         first_sums(raw, v[0], v[1], v[2]);
         row_sums<TPR>(v, buf[1][0]);
-        broken = *static_cast<volatile int *>(&failed);
+        broken = given_up(1);
     }
     for (; !broken && t < a.T; t += gridDim.x, parity ^= 1) {
         RawRow raw;
@@ -464,12 +466,13 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
                 RawRow r;
                 gate_ahead = row_gate_of(t + gridDim.x);
                 load_late(t + gridDim.x);
-                await(after, after ? ph : ph ^ 1);
+                await(after, after ? ph : ph ^ 1, parity);
                 from_ring(r, after, after_x);
                 first_sums(r, u[0], u[1], u[2]);
             }
             row_sums<TPR>(u, buf[parity][0], BY_ELEMENT ? nullptr : &sum_db, buf[parity][1]);
-            if (*static_cast<volatile int *>(&failed)) break;
+            broken = given_up(parity);
+            if (broken) break;
             // every thread is past the row before, whose x is free, and needs nothing but x of this row
             if (threadIdx.x == 0) fetch(t + STAGES * gridDim.x, st, sx ? sx - 1 : STAGES);
             v[0] = u[0];
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(TPR, BLOCKS) gated_norm_grad_kernel(const __gr
             if (++sx > STAGES) sx = 0;
         }
     }
-    if (STAGES && failed) {
+    if (STAGES && broken) {
         // nothing is left on its way into this block's shared memory: the rows that were asked for, this one first
         if (threadIdx.x == 0) {
             record_status(a.status, MOE_ERR_TIMEOUT);

@@ -25,3 +25,15 @@ def test_every_kernel_waits_for_its_predecessor(name):
         code = f.read()
     kernels = code.count("__global__ void")
     assert kernels and len(re.findall(r"\bpdl_wait\(\);", code)) == kernels == len(re.findall(r"\bpdl_trigger\(\);", code))
+
+
+def test_waits_that_run_out_are_met_by_all_threads_at_once():
+    """In the norm's gradients a thread that gives up says so before a barrier and all read it behind that: a flag of the row's own, since
+    a thread ahead may give up on the next row before the others have read this one's, and they would leave at different barriers.
+    After the rows, what a thread met is its own."""
+    with open(os.path.join(CSRC, "bf16_norm.cu")) as f:
+        code = re.sub(r"//[^\n]*", "", f.read())
+    code = code[code.index("gated_norm_grad_kernel("):code.index("gated_norm_sum_kernel(")]
+    uses = re.findall(r"\bfailed\b(.{0,14})", code)
+    assert len(uses) >= 4 and all(u.startswith("[") for u in uses), uses
+    assert code.count("failed[which]") == 2 and "given_up(parity)" in code and "ph ^ 1, parity)" in code
