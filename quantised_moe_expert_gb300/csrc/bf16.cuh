@@ -34,6 +34,13 @@ __device__ __forceinline__ float act_value(int act, float v)
     default: return v;
     }
 }
+// The logistic function's value and slope, s and s (1 - s), from e = exp(-|v|): the smaller of s and 1 - s is e / (1 + e), where 1 - s
+// would lose its digits to s (all of them past 17).
+__device__ __forceinline__ float2 sigmoid_slope(float v)
+{
+    const float e = __expf(-fabsf(v)), r = __fdividef(1.0f, 1.0f + e), small = e * r;
+    return make_float2(v < 0.f ? small : r, small * r);
+}
 // A function's value and derivative.
 __device__ __forceinline__ float2 act_slope(int act, float v)
 {
@@ -51,10 +58,7 @@ __device__ __forceinline__ float2 act_slope(int act, float v)
         const float f = v <= 0.f ? 0.f : v;                  // (NaN stays, here and in the slope)
         return make_float2(f, f > 0.f ? 1.f : f);
     }
-    case MOE_ACT_SIGMOID: {
-        const float s = sigmoid(v);
-        return make_float2(s, s * (1.0f - s));
-    }
+    case MOE_ACT_SIGMOID: return sigmoid_slope(v);
     default: return make_float2(v, 1.f);
     }
 }

@@ -278,13 +278,15 @@ __device__ __forceinline__ void gate_pair(F2 raw, F2 &f, F2 &slope)
     slope = f2(1.f, 1.f);
     if (ACT == MOE_ACT_NONE) return;
     const float2 g = unf2(raw);
-    const F2 s = f2(sigmoid(g.x), sigmoid(g.y)), minus = f2(-1.f, -1.f);
     if (ACT == MOE_ACT_SILU) {
+        const F2 s = f2(sigmoid(g.x), sigmoid(g.y)), minus = f2(-1.f, -1.f);
         f = mul2(raw, s);
         slope = fma2(f, fma2(s, minus, f2(1.f, 1.f)), s);       // s + g s (1 - s)
     } else {
-        f = s;
-        slope = fma2(mul2(s, minus), s, s);
+        // (one by one: in pairs 2 to 5% slower)
+        const float2 lo = sigmoid_slope(g.x), hi = sigmoid_slope(g.y);
+        f = f2(lo.x, hi.x);
+        slope = f2(lo.y, hi.y);
     }
 }
 

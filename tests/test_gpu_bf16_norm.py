@@ -214,3 +214,26 @@ def test_zero_rows_and_no_rows():
     ws = torch.zeros(qm.moe_gated_norm_workspace_size(0, n), dtype=torch.uint8, device="cuda")
     qm.moe_gated_norm_grad(e, e, None, 0, 0, 1.0, 1, i["post"], i["pre"], 0.0, EPS, 0, n, e, e, e, None, None, dpost, dpre, ws)
     assert bool((dpost == 0).all()) and bool((dpre == 0).all())
+
+
+@pytest.mark.parametrize("T,n,gate", [(40, 264, "row"), (40, 264, "full"), (40, 264, "channel"), (600, 2048, "full"), (600, 2056, "row")])
+@pytest.mark.parametrize("fn", ["sigmoid", "silu"])
+def test_saturated_gates(T, n, gate, fn):
+    """Gates of -30 to 30: where the function is next to 0 or 1, its slope is small and not 0, and as exact, relative to itself, as
+    others (SiLU's between its zero and 0 is left out: a difference of two terms)."""
+    i, scale = inputs(T, n, gate, seed=70), 0.75
+    g = torch.linspace(-30, 30, i["gate"].numel(), dtype=torch.float64, device="cuda").view(i["gate"].shape)
+    if fn == "silu":
+        g = torch.where((g > -4) & (g < 0), -g, g)
+    i["gate"] = g.bfloat16()
+    s = bf16(T, n, seed=71, size=3.0)
+    # what the gate multiplies, times the slope without 1 - s, which is off by 2^-53 of 1 in 64 bits too (1e-3 of itself at 30)
+    g = i["gate"].double()
+    up, down = torch.sigmoid(g), torch.sigmoid(-g)
+    slope = up * down if fn == "sigmoid" else up * (1 + g * down)
+    v, size = (t * (slope if k == 0 else slope.abs()) for k, t in enumerate(backward(i, s, gate, "none", 1, scale, 0.0)["dgate"]))
+    got = run_grad(i, s, gate, fn, 1, scale, 0.0)["dgate"]
+    # as test_backward; the exponential of up to 30 is off by 2^-23 of 2 + 1.2 x 30 units
+    each = 32 * 2.0 ** -24 + 2 * n * 2.0 ** -24 + 40 * 2.0 ** -23
+    summed = T * 2.0 ** -24 if gate == "channel" else 0.0
+    within(got, v, (BF16 * v.abs() if gate == "full" else 0.0) + 2 * (each + summed) * size)
