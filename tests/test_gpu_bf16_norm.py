@@ -237,3 +237,35 @@ def test_saturated_gates(T, n, gate, fn):
     each = 32 * 2.0 ** -24 + 2 * n * 2.0 ** -24 + 40 * 2.0 ** -23
     summed = T * 2.0 ** -24 if gate == "channel" else 0.0
     within(got, v, (BF16 * v.abs() if gate == "full" else 0.0) + 2 * (each + summed) * size)
+
+
+# dsum and a gate per element come a row ahead through registers past 5120 columns: several rows a block, with and without each
+@pytest.mark.parametrize("use", ["both", "dy", "ds"])
+@pytest.mark.parametrize("T,n,gate,fn,post", [(700, 5640, "full", "silu", 1), (500, 8192, "full", "sigmoid", 1), (613, 6152, "full", "none", 0),
+                                              (470, 8192, "row", "silu", 1), (613, 5128, "channel", "sigmoid", 1)])
+def test_backward_of_many_wide_rows(T, n, gate, fn, post, use):
+    test_backward(T, n, gate, fn, post, use)
+
+
+@pytest.mark.parametrize("n", [2048, 5120, 8192])
+def test_rows_apart_and_in_place_of_many_rows(n):
+    """As test_rows_apart_and_in_place, with several rows a block: what a row leaves in shared memory does not reach the next."""
+    T = 1000
+    i = inputs(T, n, "full", seed=80)
+    s = bf16(T, n, seed=90)
+    clean = run_grad(i, s, "full", "silu", 1, 1.0, 0.0)
+    j = {k: (v.clone() if v is not None else v) for k, v in i.items()}
+    for r, bad in ((5, float("nan")), (400, float("inf")), (T - 200, -float("inf"))):
+        j["x"][r], j["dy"][r, 3], j["gate"][r, n - 1] = bad, bad, bad
+    got = run_grad(j, s, "full", "silu", 1, 1.0, 0.0)
+    keep = torch.ones(T, dtype=torch.bool, device="cuda")
+    keep[[5, 400, T - 200]] = False
+    for k in ("dx", "dres", "dgate"):
+        assert torch.equal(got[k][keep], clean[k][keep])
+    ws = torch.zeros(qm.moe_gated_norm_workspace_size(T, n), dtype=torch.uint8, device="cuda")
+    for dx, dres in (("x", "ds"), ("dy", "s"), ("ds", "dy")):    # outputs in the inputs' places
+        b = {"x": i["x"].clone(), "dy": i["dy"].clone(), "ds": i["ds"].clone(), "s": s.clone()}
+        qm.moe_gated_norm_grad(b["x"], b["s"], i["gate"], 3, 1, 1.0, 1, i["post"], i["pre"], 0.0, EPS, T, n, b["dy"], b["ds"], b[dx], b[dres],
+                               None, None, None, ws)
+        assert torch.equal(b[dx], clean["dx"]) and torch.equal(b[dres], clean["dres"])
+    assert qm.moe_get_device_status(ws) == 0
