@@ -114,7 +114,7 @@ cudaError_t launch_dispatch(const RoutedArgs &a, cudaStream_t st);
 cudaError_t launch_weighted_sum(const RoutedArgs &a, cudaStream_t st);
 cudaError_t launch_weighted_sum_grad(const RoutedArgs &a, cudaStream_t st);
 
-// Norms around a block (gated_norm.cu).
+// Norms around a block (bf16_norm.cu).
 struct GatedNormArgs {
     const uint16_t *x, *residual, *gate, *post_weight, *pre_weight;
     uint16_t *sum, *y;                   // forward: written; backward: sum read

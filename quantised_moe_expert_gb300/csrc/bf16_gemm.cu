@@ -19,7 +19,7 @@
 // Bounds and measurements: 8192 x 8192 x 4096 with bias, GELU and residual 310 to 330 us (1.7 PFLOP/s; 291 to 297 without them, where the
 // library's product alone takes 271 to 279): tensor cores, and what the epilogue takes from them.  Its tiles are
 // 1,024 for 76 pairs of SMs; 4096 x 2048 x 4096 43 us for 39 of the library's, 128 tiles in two rounds of 76.
-// Experts of 512 tokens (hidden 2048, inter 512, 257 groups): gated pair 165 us, down products 87, 6.4 and 6.2 TB/s of weights.  Of 4096
+// Experts of 512 tokens (hidden 2048, inter 512, 257 groups): gated pair 165 us (171 with both products kept), down products 87, 6.4 and 6.2 TB/s of weights.  Of 4096
 // tokens: input gradients 117 and 200 us (6.2 and 6.5 TB/s), weight gradients 139 to 141 each for 730 MB (5.2 TB/s, three
 // quarters of it writes; groups of 3 rows, whose writes are all, 88 us).  There no unit is full (tensor pipe 21%, DRAM 40% where half of
 // the output stays in L2): copies wait behind writes in a ring of four stages, and the write of a tile's 64 KB takes 2,100 of its
@@ -1306,6 +1306,7 @@ cudaError_t launch_wgrad(const WgradArgs &g, cudaStream_t st)
         if (how.ways > 1 || tiles(128, 64) <= sms) bn = how.bn;
     }
     Maps maps{};
+    // (the 128-column plans spill 12 to 32 bytes of an epilogue warp's registers, the 256-column one 8)
     const int blocks = pair ? 2 : bn / 64;
     if (!map_mn(&maps.a[0], g.dy, a.M, a.R, 1, kStep, 2, &a.blocks_a) || !map_mn(&maps.a16, g.dy, a.M, a.R, 1, 16, 2, &a.blocks_a) ||
         !map_mn(&maps.w[0], g.x, a.N, a.R, 1, kStep, blocks, &a.blocks_w) || !map_mn(&maps.w16, g.x, a.N, a.R, 1, 16, blocks, &a.blocks_w))

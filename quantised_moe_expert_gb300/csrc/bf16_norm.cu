@@ -565,7 +565,7 @@ __global__ void __launch_bounds__(32 * kWarps) gated_norm_sum_kernel(const __gri
 
 // Threads of a block of the backward pass, blocks an SM, stages of its rings and arrays of a place.  Narrow rows (threads, blocks): 16384 x 1024 in 4 blocks
 // through registers 60 us, 3 or 5 70 and 63, 6 with rings 57, but a gate per channel 44 in 4 and 50 in 6.  2560 columns in two blocks
-// of 320 65 us for 8192 rows, in one of 512 106; 3192 in two of 416 44 us for 3469 rows, in one of 512 51.
+// of 320 61 us for 8192 rows, in one of 512 106; 3192 in two of 416 44 us for 3469 rows, in one of 512 51.
 // With two arrays a place more blocks fit: 4096 columns in two blocks of 512 and 64 registers 87 us for 8192 rows with a gate per
 // token (one block 99), but 62 for 4096 rows with a gate per element (54), 16384 x 2048 in four blocks 107 (95); 6144 columns, three stages of two
 // arrays 76.5, two of four 80; 8192 columns 122, with everything through registers and no rings 154.
