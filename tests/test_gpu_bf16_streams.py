@@ -43,3 +43,36 @@ def test_a_given_stream(by_handle):
         assert all(bool(t.isnan().all()) for t in written)
         y = got = None
     assert qm.moe_get_device_status(ws2) == 0
+
+
+@pytest.mark.parametrize("forked", [False, True])
+def test_a_given_stream_captured(forked):
+    """The same in a captured graph, on the capturing stream and on one that it forks to and joins, replayed with other inputs."""
+    T, E, I, H, k = 90, 6, 136, 264, 2
+    e = layer(E, I, H, k, 1)
+    _, inv, offsets = routing(T, E, k)
+    p, w_s = torch.softmax(bf16(T, k, seed=6).float(), 1).bfloat16(), torch.sigmoid(bf16(T, seed=7).float()).bfloat16()
+    ws = torch.zeros(512, dtype=torch.uint8, device="cuda")
+    xs, dys = [bf16(T, H, seed=20 + i) for i in range(3)], [bf16(T, H, seed=30 + i) for i in range(3)]
+
+    def both(x, dy, stream=None):
+        y, kept = e.forward(x, inv, offsets, p, w_s, ws, keep=True, stream=stream)
+        return (y, *e.backward(dy, kept, ws, stream=stream))
+
+    want = [[t.clone() for t in both(x, dy)] for x, dy in zip(xs, dys)]
+    main, other, graph = torch.cuda.Stream(), torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    x, dy = xs[0].clone(), dys[0].clone()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=main):
+        if forked:
+            other.wait_stream(main)
+        out = both(x, dy, other if forked else main)
+        if forked:
+            main.wait_stream(other)
+    for i in (0, 1, 2, 1):
+        x.copy_(xs[i])
+        dy.copy_(dys[i])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+    assert qm.moe_get_device_status(ws) == 0
